@@ -106,7 +106,8 @@ typedef enum NM_INT_ENUM {
   NM_ERR_LAYOUT = 8,      /* unknown layout, or NM_LAYOUT_BLOCKED with K % 64 != 0   */
   NM_ERR_ALIAS = 9,       /* an output overlaps an input it may not replace          */
   NM_ERR_SCRATCH = 10     /* the call needs more than the library's fixed device scratch
-                             buffer (NM_STATIC_SCRATCH_BYTES)                         */
+                             buffer (NM_STATIC_SCRATCH_BYTES), or than the workspace it
+                             was given                                               */
 } nm_status;
 
 /* NM_I8: int8 two's complement ("Tensor Scores 상에서 구조적인 sparse GEMM" lists INT8 among
@@ -324,6 +325,87 @@ nm_status nm_perm_gains_static(const void* W, nm_dtype dt, int64_t R, int64_t K,
 nm_status nm_perm_search(const void* W, nm_dtype dt, int64_t R, int64_t K, int n, int m,
                          int max_rounds, int32_t* perm, int* rounds, void* workspace,
                          size_t workspace_bytes, nm_stream_t stream);
+
+/* ---- weights in 4 bits ------------------------------------------------------------------
+ *
+ * A matrix of R rows and C stored columns -- a dense one, or the C = K/2 kept values a row of
+ * a 2:4 compressed R x K one -- held as codes of 4 bits with one 16-bit scale for each group of
+ * `group` (32, 64 or 128, else NM_ERR_UNSUPPORTED) consecutive stored columns of a row; the last
+ * group of a row may be short:
+ *   scale = max |w| / 7 over the group, rounded to the scales' type;
+ *   code  = w / scale rounded to an integer (ties to even), held within -8 .. 7;
+ * and a code stands for scale * code.  A group of zeros (or whose scale rounds to 0) has scale 0
+ * and codes 0; a group that holds a NaN or an infinity has that as its scale, and stands for NaN.
+ *
+ *   codes   nm_codes_bytes(R, C) bytes.  Blocks of 16 rows x 128 columns, row after row of
+ *           blocks, 1 KB each (S = ceil(C / 128) blocks to 16 rows): 32-bit word
+ *             ((g * S + s) * 64 + 16 j + r) * 4 + w
+ *           holds columns 128 s + 32 w + 8 j .. + 7 of row 16 g + r, column i of the eight as
+ *           code + 8 in bits 4 (i / 2) + 16 (i % 2) .. + 3.  Places past the matrix hold code 0.
+ *   scales  nm_scales_bytes(R, C, group) bytes: scale of group i of row 16 g + r at
+ *             (g * ceil(C / group) + i) * 16 + r;  0 past row R. */
+size_t nm_codes_bytes(int64_t R, int64_t C);
+size_t nm_scales_bytes(int64_t R, int64_t C, int group);
+
+/* Codes and scales of W (dt NM_F32, NM_F16 or NM_BF16).  NM_LAYOUT_ROWS: W is R x C, row-major.
+ * NM_LAYOUT_BLOCKED: W is the value array of a 2:4 pair in that layout, C = K/2 (a multiple
+ * of 32, else NM_ERR_LAYOUT); the pair's metadata goes with the codes unchanged.  scale_dt:
+ * NM_F16 or NM_BF16.  One pass over W. */
+nm_status nm_quantize(const void* W, nm_dtype dt, int64_t R, int64_t C, nm_layout layout, int group,
+                      void* codes, void* scales, nm_dtype scale_dt, nm_stream_t stream);
+
+/* The values that the codes stand for, rounded once to scale_dt, in W's layout (see
+ * nm_quantize; NM_LAYOUT_BLOCKED gives a value array that nm_spmm takes with the metadata). */
+nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt, int64_t R,
+                        int64_t C, nm_layout layout, int group, void* W_out, nm_stream_t stream);
+
+/* Y = Wq X: the R x K matrix that codes, scales (and metadata) stand for, times X (K x T), for
+ * one column or a few (every T is taken; beyond some tens a dequantised product is faster).
+ * meta NULL: dense codes of C = K columns.  Else the metadata, in NM_LAYOUT_BLOCKED, of a 2:4
+ * pair whose values the codes hold (C = K/2; K % 64 == 0, else NM_ERR_LAYOUT); it is trusted.
+ * dt is the type of X and of the scales, NM_F16 or NM_BF16; y_dt is dt or NM_F32.  Codes enter
+ * the matrix cores exactly, sums are fp32, a group's sum is scaled in fp32 and Y is rounded once.
+ * workspace: nm_matvec_workspace_bytes(K, T) bytes of device memory (0 for T = 1). */
+size_t nm_matvec_workspace_bytes(int64_t K, int64_t T);
+nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
+                    int64_t K, int group, const void* X, int64_t T, nm_dtype dt, void* Y,
+                    nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream);
+
+/* ---- cross entropy of a large vocabulary --------------------------------------------------
+ *
+ * Logits L = W X of W (V x K) and X (K x T, one column a token), dt NM_F16 or NM_BF16 for both;
+ * L is never stored.  target: T entries; a token whose target is outside 0 .. V-1 is left out
+ * (its loss is 0 and it adds nothing to the gradient, whatever its column of X holds).
+ *   lse[t]  = log sum over v of exp L[v, t]       (of every token)
+ *   loss[t] = lse[t] - L[target[t], t]
+ * loss and lse are fp32; sums are fp32.  V >= 1 where T > 0, V < 2^31, K < 2^22, T < 2^22,
+ * else NM_ERR_SHAPE.  Fastest where K % 64 == 0 (else W is copied, padded, into the workspace)
+ * and T % 8 == 0. */
+size_t nm_xent_workspace_bytes(int64_t V, int64_t K, int64_t T);
+nm_status nm_xent(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
+                  const int64_t* target, float* loss, float* lse, void* workspace,
+                  size_t workspace_bytes, nm_stream_t stream);
+
+/* The gradient of sum over t of gout[t] * loss[t] (gout: T fp32 numbers; 1 / tokens for a mean):
+ *   dW (V x K) = P X^T,  dX (K x T) = W^T P,  P[v, t] = (exp(L[v, t] - lse[t]) - [v = target[t]]) gout[t]
+ * with lse from nm_xent, in dt.  The logits are computed again, a piece of the vocabulary at a
+ * time; P of a piece is rounded to dt, sums are fp32, results are rounded once. */
+size_t nm_xent_grad_workspace_bytes(int64_t V, int64_t K, int64_t T);
+nm_status nm_xent_grad(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
+                       const int64_t* target, const float* lse, const float* gout, void* dW,
+                       void* dX, void* workspace, size_t workspace_bytes, nm_stream_t stream);
+
+/* ---- orthogonalised update ----------------------------------------------------------------
+ *
+ * Newton-Schulz steps on an update G (R x K; dt NM_F32, NM_F16 or NM_BF16):
+ *   X = G / (|G|_F + eps);  `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315), on the shorter side (X^T X where R > K), which
+ * moves the singular values of G to near 1 and keeps its singular vectors.  Products are of
+ * fp16 numbers with fp32 sums: one fp16 an entry for NM_BF16, two (22 bits) for NM_F16 and
+ * NM_F32.  out (R x K, dt) may be G.  steps 1 .. 100, eps >= 0, R, K < 2^22, else NM_ERR_SHAPE. */
+size_t nm_orthogonalize_workspace_bytes(int64_t R, int64_t K, nm_dtype dt);
+nm_status nm_orthogonalize(const void* G, nm_dtype dt, int64_t R, int64_t K, int steps, float eps,
+                           void* out, void* workspace, size_t workspace_bytes, nm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,15 @@ library functions raises.
     Wt = tprune(W, 2, 4)                      # transposable 2:4 mask applied (4x4 blocks)
     vt, mt = compress_t(Wt, 2, 4)             # compressed W^T: spmm(vt, mt, dY) = W^T dY
 
+    loss, lse = xent(W, X, target)            # cross entropy of the logits W X, never stored
+    dW, dX = xent_grad(W, X, target, lse, gout)
+    U = orthogonalize(G)                      # Newton-Schulz steps on an update
+    codes, scales = quantize(W, group=64)     # 4-bit codes, one 16-bit scale a group
+    y = matvec(codes, scales, x, group=64, rows=R)          # x: (K, T), T a few tokens
+    v, m = compress(W, 2, 4, layout="blocked")              # the same on a 2:4 weight
+    codes, scales = quantize(v, 64, layout="blocked", rows=R)
+    y = matvec(codes, scales, x, 64, rows=R, meta=m)
+
 The compressed pair comes in two layouts (defined in include/nm.h): "rows"
 (values (R, K*n/m), meta (R, words)) and "blocked" (blocks of 16 rows x 64
 columns, the order the sparse product streams; values (G, S, 16, 64*n/m), meta
@@ -47,7 +56,12 @@ EXPORTS = ("nm_abi_version", "nm_status_str", "nm_values_bytes", "nm_meta_bytes"
            "nm_meta_words_per_row", "nm_mask", "nm_compress", "nm_decompress", "nm_spmm",
            "nm_prune", "nm_srste_grad", "nm_tmask", "nm_tprune", "nm_compress_t",
            "nm_perm_workspace_bytes", "nm_perm_gains", "nm_perm_search", "nm_check_meta",
-           "nm_mask_compress", "nm_perm_gains_static")
+           "nm_mask_compress", "nm_perm_gains_static",
+           "nm_codes_bytes", "nm_scales_bytes", "nm_quantize", "nm_dequantize", "nm_matvec",
+           "nm_matvec_workspace_bytes", "nm_xent", "nm_xent_workspace_bytes", "nm_xent_grad",
+           "nm_xent_grad_workspace_bytes", "nm_orthogonalize",
+           "nm_orthogonalize_workspace_bytes")
+GROUPS = (32, 64, 128)   # stored columns that share a scale of the 4-bit codes
 STATIC_SCRATCH_BYTES = 64 << 20  # NM_STATIC_SCRATCH_BYTES
 SRSTE_DECAY = 0.0002  # the SR-STE page's default decay
 
@@ -97,6 +111,26 @@ def lib() -> ctypes.CDLL:
         L.nm_perm_search.argtypes = [vp, i32, i64, i64, i32, i32, i32, vp, vp, vp,
                                      ctypes.c_size_t, vp]
         L.nm_perm_gains_static.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, vp, vp]
+        f32, size = ctypes.c_float, ctypes.c_size_t
+        L.nm_codes_bytes.argtypes = [i64, i64]
+        L.nm_scales_bytes.argtypes = [i64, i64, i32]
+        L.nm_quantize.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, i32, vp]
+        L.nm_dequantize.argtypes = [vp, vp, i32, i64, i64, i32, i32, vp, vp]
+        L.nm_matvec_workspace_bytes.argtypes = [i64, i64]
+        L.nm_matvec.argtypes = [vp, vp, vp, i64, i64, i32, vp, i64, i32, vp, i32, vp, size, vp]
+        L.nm_xent_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nm_xent.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, size, vp]
+        L.nm_xent_grad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nm_xent_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, size, vp]
+        L.nm_orthogonalize_workspace_bytes.argtypes = [i64, i64, i32]
+        L.nm_orthogonalize.argtypes = [vp, i32, i64, i64, i32, f32, vp, vp, size, vp]
+        for f in ("nm_codes_bytes", "nm_scales_bytes", "nm_matvec_workspace_bytes",
+                  "nm_xent_workspace_bytes", "nm_xent_grad_workspace_bytes",
+                  "nm_orthogonalize_workspace_bytes"):
+            getattr(L, f).restype = size
+        for f in ("nm_quantize", "nm_dequantize", "nm_matvec", "nm_xent", "nm_xent_grad",
+                  "nm_orthogonalize"):
+            getattr(L, f).restype = i32
         for f in ("nm_mask", "nm_compress", "nm_decompress", "nm_spmm", "nm_prune",
                   "nm_srste_grad", "nm_tmask", "nm_tprune", "nm_compress_t", "nm_perm_gains",
                   "nm_perm_search", "nm_perm_gains_static"):
@@ -436,3 +470,190 @@ def perm_search(W: torch.Tensor, n: int = 2, m: int = 4, max_rounds: int = 1000,
         _ptr(W), dt, R, K, n, m, int(max_rounds), p.ctypes.data_as(ctypes.c_void_p),
         ctypes.byref(rounds), _ptr(ws), ws.numel(), _stream(W)))
     return torch.from_numpy(p), rounds.value
+
+
+# ---- weights in 4 bits ---------------------------------------------------------------------
+
+
+def _half(dtype: torch.dtype, name: str) -> int:
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be float16 or bfloat16")
+    return _DT[dtype]
+
+
+def _group(group: int) -> int:
+    if group not in GROUPS:
+        raise ValueError(f"group must be one of {GROUPS}")
+    return group
+
+
+def code_shapes(R: int, C: int, group: int):
+    """Shapes of (codes int32, scales) of R rows of C stored columns."""
+    return (-(-R // 16), -(-C // 128), 64, 4), (-(-R // 16), -(-C // _group(group)), 16)
+
+
+def _check_codes(codes: torch.Tensor, scales: torch.Tensor, R: int, C: int, group: int) -> int:
+    cshape, sshape = code_shapes(R, C, group)
+    if codes.dtype != torch.int32 or tuple(codes.shape) != cshape or not codes.is_cuda or \
+            not codes.is_contiguous():
+        raise ValueError(f"codes must be a contiguous int32 {cshape} GPU tensor")
+    dt = _half(scales.dtype, "scales")
+    if tuple(scales.shape) != sshape or not scales.is_contiguous() or \
+            scales.device != codes.device:
+        raise ValueError(f"scales must be a contiguous {sshape} tensor on the codes' device")
+    return dt
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def quantize(W: torch.Tensor, group: int = 64, layout: str = "rows", rows: int | None = None,
+             scale_dtype: torch.dtype | None = None):
+    """(codes, scales) of W in 4 bits, `group` (32, 64 or 128) stored columns of a row to a scale:
+    scale = max |w| / 7, code = round(w / scale) in -8 .. 7.  layout "rows": W is (R, K).  layout
+    "blocked": W is the value array of a 2:4 pair from compress(..., layout="blocked"), of a
+    matrix of `rows` rows; its metadata goes with the codes unchanged.  Scales are in
+    scale_dtype, by default W's type if it has 16 bits, else bfloat16."""
+    _group(group)
+    s_dt = scale_dtype or (torch.bfloat16 if W.dtype == torch.float32 else W.dtype)
+    if _layout(layout) == 0:
+        dt = _dense_input(W, "W", int8=False)
+        R, C = W.shape
+        if rows is not None and rows != R:
+            raise ValueError(f"rows={rows} does not match W ({R} rows)")
+    else:
+        if W.dtype not in _FLOAT or not W.is_cuda or not W.is_contiguous():
+            raise ValueError("values must be a contiguous float32/float16/bfloat16 GPU tensor")
+        if rows is None:
+            raise ValueError("the blocked layout needs rows= (the matrix's row count)")
+        if W.dim() != 4 or W.shape[0] != -(-rows // 16) or tuple(W.shape[2:]) != (16, 32):
+            raise ValueError(f"blocked 2:4 values must be ({-(-rows // 16)}, S, 16, 32)")
+        dt, R, C = _DT[W.dtype], rows, 32 * W.shape[1]
+    sc = _half(s_dt, "scale_dtype")
+    cshape, sshape = code_shapes(R, C, group)
+    codes = torch.empty(cshape, dtype=torch.int32, device=W.device)
+    scales = torch.empty(sshape, dtype=s_dt, device=W.device)
+    _check("nm_quantize", lib().nm_quantize(_ptr(W), dt, R, C, _layout(layout), group, _ptr(codes),
+                                            _ptr(scales), sc, _stream(W)))
+    return codes, scales
+
+
+def dequantize(codes: torch.Tensor, scales: torch.Tensor, C: int, group: int = 64,
+               layout: str = "rows", rows: int | None = None) -> torch.Tensor:
+    """The values that the codes of `rows` rows of C stored columns stand for, in the scales'
+    type: (rows, C), or in layout "blocked" (G, C/32, 16, 32), values that spmm takes."""
+    if rows is None:
+        raise ValueError("dequantize needs rows= (the matrix's row count)")
+    dt = _check_codes(codes, scales, rows, C, group)
+    if _layout(layout) == 0:
+        shape = (rows, C)
+    elif C % 32:
+        _check("nm_dequantize", 8)
+    else:
+        shape = (-(-rows // 16), C // 32, 16, 32)
+    out = torch.empty(shape, dtype=scales.dtype, device=codes.device)
+    _check("nm_dequantize", lib().nm_dequantize(_ptr(codes), _ptr(scales), dt, rows, C,
+                                                _layout(layout), group, _ptr(out), _stream(codes)))
+    return out
+
+
+def matvec(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group: int = 64,
+           rows: int | None = None, meta: torch.Tensor | None = None,
+           out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y (rows, T) = the matrix that codes, scales (and, for 2:4 codes, the blocked metadata)
+    stand for, times X (K, T); T is one token or a few.  out_dtype is X's type or float32."""
+    if rows is None:
+        raise ValueError("matvec needs rows= (the matrix's row count)")
+    _dense_input(X, "X", int8=False)
+    dt = _half(X.dtype, "X")
+    K, T = X.shape
+    if meta is not None and K % 64:
+        _check("nm_matvec", 8)
+    if _check_codes(codes, scales, rows, K // 2 if meta is not None else K, group) != dt:
+        raise ValueError("scales and X must have the same dtype")
+    if meta is not None:
+        mshape = compressed_shapes(rows, K, 2, 4, "blocked")[1]
+        if meta.dtype != torch.int32 or tuple(meta.shape) != tuple(mshape) or \
+                not meta.is_contiguous():
+            raise ValueError(f"meta must be a contiguous int32 {tuple(mshape)} tensor")
+    if any(t is not None and t.device != X.device for t in (codes, meta)):
+        raise ValueError("codes, meta and X must be on the same device")
+    y_dtype = out_dtype or X.dtype
+    if y_dtype not in (X.dtype, torch.float32):
+        raise ValueError("out_dtype must be X's dtype or float32")
+    if out is None:
+        out = torch.empty((rows, T), dtype=y_dtype, device=X.device)
+    elif out.shape != (rows, T) or out.dtype != y_dtype or not out.is_contiguous() or \
+            out.device != X.device:
+        raise ValueError("out has the wrong shape, dtype, layout or device")
+    ws = _workspace(int(lib().nm_matvec_workspace_bytes(K, T)), X.device)
+    _check("nm_matvec", lib().nm_matvec(
+        _ptr(codes), _ptr(scales), None if meta is None else _ptr(meta), rows, K, group, _ptr(X), T,
+        dt, _ptr(out), _DT[y_dtype], _ptr(ws), ws.numel(), _stream(X)))
+    return out
+
+
+# ---- cross entropy of a large vocabulary -----------------------------------------------------
+
+
+def _xent_inputs(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor):
+    _dense_input(W, "W", int8=False)
+    _dense_input(X, "X", int8=False)
+    dt = _half(W.dtype, "W")
+    (V, K), T = W.shape, X.shape[1]
+    if X.dtype != W.dtype or X.shape[0] != K or X.device != W.device:
+        raise ValueError(f"X must be ({K}, T) in W's dtype on W's device")
+    if target.dtype != torch.int64 or tuple(target.shape) != (T,) or \
+            not target.is_contiguous() or target.device != W.device:
+        raise ValueError(f"target must be a contiguous int64 ({T},) tensor on W's device")
+    return dt, V, K, T
+
+
+def xent(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor):
+    """(loss, lse), float32 (T,): softmax cross entropy of the logits W X -- W (V, K), X (K, T),
+    bfloat16 or float16, a column a token -- at target (int64), and the logits' log sum exp.  A
+    target outside 0 .. V - 1 leaves its token out: loss 0.  The logits are not stored."""
+    dt, V, K, T = _xent_inputs(W, X, target)
+    loss = torch.empty((T,), dtype=torch.float32, device=W.device)
+    lse = torch.empty_like(loss)
+    ws = _workspace(int(lib().nm_xent_workspace_bytes(V, K, T)), W.device)
+    _check("nm_xent", lib().nm_xent(_ptr(W), _ptr(X), dt, V, K, T, _ptr(target), _ptr(loss),
+                                    _ptr(lse), _ptr(ws), ws.numel(), _stream(W)))
+    return loss, lse
+
+
+def xent_grad(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+              gout: torch.Tensor):
+    """(dW, dX), in W's type: the gradient of sum(gout * loss) with xent's loss and lse; gout is
+    float32 (T,), for a mean 1 / tokens.  Tokens left out add nothing."""
+    dt, V, K, T = _xent_inputs(W, X, target)
+    for name, t in (("lse", lse), ("gout", gout)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (T,) or not t.is_contiguous() or \
+                t.device != W.device:
+            raise ValueError(f"{name} must be a contiguous float32 ({T},) tensor on W's device")
+    dW, dX = torch.empty_like(W), torch.empty_like(X)
+    ws = _workspace(int(lib().nm_xent_grad_workspace_bytes(V, K, T)), W.device)
+    _check("nm_xent_grad", lib().nm_xent_grad(
+        _ptr(W), _ptr(X), dt, V, K, T, _ptr(target), _ptr(lse), _ptr(gout), _ptr(dW), _ptr(dX),
+        _ptr(ws), ws.numel(), _stream(W)))
+    return dW, dX
+
+
+# ---- orthogonalised update -------------------------------------------------------------------
+
+
+def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """G (R, K) after `steps` Newton-Schulz steps from G / (|G|_F + eps): the same singular
+    vectors, singular values near 1 (out may be G)."""
+    dt = _dense_input(G, "G", int8=False)
+    R, K = G.shape
+    if out is None:
+        out = torch.empty_like(G)
+    else:
+        _same_dense(out, G, "out")
+    ws = _workspace(int(lib().nm_orthogonalize_workspace_bytes(R, K, dt)), G.device)
+    _check("nm_orthogonalize", lib().nm_orthogonalize(
+        _ptr(G), dt, R, K, int(steps), float(eps), _ptr(out), _ptr(ws), ws.numel(), _stream(G)))
+    return out

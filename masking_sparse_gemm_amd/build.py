@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnm.so")
 SOURCES = ["nm_api.hip", "nm_compress.hip", "nm_spmm.hip", "nm_spmm_sk.hip", "nm_srste.hip",
-           "nm_tmask.hip", "nm_perm.hip"]
+           "nm_tmask.hip", "nm_perm.hip", "nm_quant.hip", "nm_xent.hip", "nm_orth.hip"]
 # the measurement probes (include/nm_probe.h) link into a library of their own
 PROBE_SOURCES = ["nm_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libnm_probe.so")

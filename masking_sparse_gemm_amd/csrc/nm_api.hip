@@ -496,3 +496,216 @@ nm_status nm_perm_search(const void* W, nm_dtype dt, int64_t R, int64_t K, int n
 }
 
 }  // extern "C"
+
+namespace {
+
+bool half_dtype(int dt) { return dt == NM_F16 || dt == NM_BF16; }
+bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+int64_t codes_bytes(int64_t R, int64_t C) { return (R + 15) / 16 * ((C + 127) / 128) * 1024; }
+int64_t scales_bytes(int64_t R, int64_t C, int group) {
+  return (R + 15) / 16 * ((C + group - 1) / group) * 32;
+}
+
+// The stored matrix of nm_quantize and nm_dequantize: sizes, layout and group.
+nm_status check_codes(int64_t R, int64_t C, int layout, int group) {
+  const nm_status st = check_shape(R, C, 1);
+  if (st != NM_OK) return st;
+  if (!group_ok(group)) return NM_ERR_UNSUPPORTED;
+  if (layout == NM_LAYOUT_BLOCKED ? C % 32 != 0 : layout != NM_LAYOUT_ROWS) return NM_ERR_LAYOUT;
+  return NM_OK;
+}
+
+constexpr int64_t kMaxSide = (int64_t)1 << 22;  // 64 rows of 16-bit numbers within 32-bit offsets
+
+nm_status check_xent(nm_dtype dt, int64_t V, int64_t K, int64_t T) {
+  if (!half_dtype(dt)) return NM_ERR_DTYPE;
+  if (V < 0 || K < 0 || T < 0 || V >= (int64_t)1 << 31 || K >= kMaxSide || T >= kMaxSide ||
+      (V == 0 && T > 0))
+    return NM_ERR_SHAPE;
+  return check_shape(V, K, 1);
+}
+
+nm_status check_workspace(const void* p, size_t have, size_t need) {
+  if (have < need) return NM_ERR_SCRATCH;
+  if (need > 0 && p == nullptr) return NM_ERR_NULL;
+  return aligned16(p) ? NM_OK : NM_ERR_ALIGN;
+}
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+};
+// Does a written range overlap another of the call's ranges (the written ones come first)?
+bool any_alias(const Range* r, int written, int all) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < all; ++j)
+      if (overlaps(r[i].p, r[i].bytes, r[j].p, r[j].bytes)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nm_codes_bytes(int64_t R, int64_t C) {
+  return check_shape(R, C, 1) == NM_OK ? (size_t)codes_bytes(R, C) : 0;
+}
+
+size_t nm_scales_bytes(int64_t R, int64_t C, int group) {
+  return check_shape(R, C, 1) == NM_OK && group_ok(group) ? (size_t)scales_bytes(R, C, group) : 0;
+}
+
+nm_status nm_quantize(const void* W, nm_dtype dt, int64_t R, int64_t C, nm_layout layout, int group,
+                      void* codes, void* scales, nm_dtype scale_dt, nm_stream_t stream) {
+  if (!float_dtype(dt) || !half_dtype(scale_dt)) return NM_ERR_DTYPE;
+  nm_status st = check_codes(R, C, layout, group);
+  if (st != NM_OK) return st;
+  if (missing(W, R * C) || missing(codes, R * C) || missing(scales, R * C)) return NM_ERR_NULL;
+  if (R * C == 0) return NM_OK;
+  if (!aligned16(W) || !aligned16(codes) || !aligned16(scales)) return NM_ERR_ALIGN;
+  const Range r[] = {{codes, codes_bytes(R, C)},
+                     {scales, scales_bytes(R, C, group)},
+                     {W, padded_rows(R, layout) * C * elem_bytes(dt)}};
+  if (any_alias(r, 2, 3)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_quantize(W, (int)dt, R, C, layout == NM_LAYOUT_BLOCKED, group, codes,
+                                      scales, (int)scale_dt, static_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt, int64_t R,
+                        int64_t C, nm_layout layout, int group, void* W_out, nm_stream_t stream) {
+  if (!half_dtype(scale_dt)) return NM_ERR_DTYPE;
+  nm_status st = check_codes(R, C, layout, group);
+  if (st != NM_OK) return st;
+  if (missing(W_out, R * C) || missing(codes, R * C) || missing(scales, R * C)) return NM_ERR_NULL;
+  if (R * C == 0) return NM_OK;
+  if (!aligned16(W_out) || !aligned16(codes) || !aligned16(scales)) return NM_ERR_ALIGN;
+  const Range r[] = {{W_out, padded_rows(R, layout) * C * 2},
+                     {codes, codes_bytes(R, C)},
+                     {scales, scales_bytes(R, C, group)}};
+  if (any_alias(r, 1, 3)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_dequantize(codes, scales, (int)scale_dt, R, C,
+                                        layout == NM_LAYOUT_BLOCKED, group, W_out,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t nm_matvec_workspace_bytes(int64_t K, int64_t T) {
+  if (K < 0 || T < 0 || T >= kMaxSide || K >= (int64_t)1 << 31) return 0;
+  return nm::matvec_workspace_bytes(K, T);
+}
+
+nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
+                    int64_t K, int group, const void* X, int64_t T, nm_dtype dt, void* Y,
+                    nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
+  if (!half_dtype(dt) || (y_dt != dt && y_dt != NM_F32)) return NM_ERR_DTYPE;
+  nm_status st = check_shape(R, K, 1);
+  if (st != NM_OK) return st;
+  if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 31) return NM_ERR_SHAPE;
+  if (!group_ok(group)) return NM_ERR_UNSUPPORTED;
+  if (meta != nullptr && K % 64 != 0) return NM_ERR_LAYOUT;
+  if (missing(codes, R * K) || missing(scales, R * K) || missing(X, K * T) || missing(Y, R * T))
+    return NM_ERR_NULL;
+  if (R * T == 0) return NM_OK;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(meta) || !aligned16(X) || !aligned16(Y))
+    return NM_ERR_ALIGN;
+  const size_t need = nm::matvec_workspace_bytes(K, T);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const int64_t C = meta != nullptr ? K / 2 : K;
+  const Range r[] = {{Y, R * T * elem_bytes(y_dt)},
+                     {workspace, (int64_t)need},
+                     {codes, codes_bytes(R, C)},
+                     {scales, scales_bytes(R, C, group)},
+                     {meta, meta != nullptr ? (R + 15) / 16 * 16 * (K / 8) : 0},
+                     {X, K * T * 2}};
+  if (any_alias(r, 2, 6)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_matvec(codes, scales, meta, R, K, group, X, T, (int)dt, Y, (int)y_dt,
+                                    workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t nm_xent_workspace_bytes(int64_t V, int64_t K, int64_t T) {
+  return check_xent(NM_BF16, V, K, T) == NM_OK ? nm::xent_workspace_bytes(V, K, T) : 0;
+}
+
+size_t nm_xent_grad_workspace_bytes(int64_t V, int64_t K, int64_t T) {
+  return check_xent(NM_BF16, V, K, T) == NM_OK && V * K * T > 0
+             ? nm::xent_grad_workspace_bytes(V, K, T)
+             : 0;
+}
+
+nm_status nm_xent(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
+                  const int64_t* target, float* loss, float* lse, void* workspace,
+                  size_t workspace_bytes, nm_stream_t stream) {
+  nm_status st = check_xent(dt, V, K, T);
+  if (st != NM_OK) return st;
+  if (missing(W, V * K) || missing(X, K * T) || missing(target, T) || missing(loss, T) ||
+      missing(lse, T))
+    return NM_ERR_NULL;
+  if (T == 0) return NM_OK;
+  if (!aligned16(W) || !aligned16(X) || !aligned16(target) || !aligned16(loss) || !aligned16(lse))
+    return NM_ERR_ALIGN;
+  const size_t need = nm::xent_workspace_bytes(V, K, T);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Range r[] = {{loss, T * 4}, {lse, T * 4},     {workspace, (int64_t)need},
+                     {W, V * K * 2}, {X, K * T * 2}, {target, T * 8}};
+  if (any_alias(r, 3, 6)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_xent(W, X, (int)dt, V, K, T, target, loss, lse, workspace,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_xent_grad(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
+                       const int64_t* target, const float* lse, const float* gout, void* dW,
+                       void* dX, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
+  nm_status st = check_xent(dt, V, K, T);
+  if (st != NM_OK) return st;
+  if (missing(W, V * K) || missing(X, K * T) || missing(target, T) || missing(lse, T) ||
+      missing(gout, T) || missing(dW, V * K) || missing(dX, K * T))
+    return NM_ERR_NULL;
+  if (K == 0 || V == 0) return NM_OK;  // both results are empty
+  if (!aligned16(W) || !aligned16(X) || !aligned16(target) || !aligned16(lse) || !aligned16(gout) ||
+      !aligned16(dW) || !aligned16(dX))
+    return NM_ERR_ALIGN;
+  const size_t need = T > 0 ? nm::xent_grad_workspace_bytes(V, K, T) : 0;
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Range r[] = {{dW, V * K * 2}, {dX, K * T * 2},  {workspace, (int64_t)need}, {W, V * K * 2},
+                     {X, K * T * 2},  {target, T * 8}, {lse, T * 4},              {gout, T * 4}};
+  if (any_alias(r, 3, 8)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_xent_grad(W, X, (int)dt, V, K, T, target, lse, gout, dW, dX, workspace,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+nm_status check_orth(nm_dtype dt, int64_t R, int64_t K) {
+  if (!float_dtype(dt)) return NM_ERR_DTYPE;
+  if (R < 0 || K < 0 || R >= kMaxSide || K >= kMaxSide) return NM_ERR_SHAPE;
+  return check_shape(R, K, 1);
+}
+}  // namespace
+
+size_t nm_orthogonalize_workspace_bytes(int64_t R, int64_t K, nm_dtype dt) {
+  return check_orth(dt, R, K) == NM_OK && R * K > 0 ? nm::orth_workspace_bytes(R, K, (int)dt) : 0;
+}
+
+nm_status nm_orthogonalize(const void* G, nm_dtype dt, int64_t R, int64_t K, int steps, float eps,
+                           void* out, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
+  nm_status st = check_orth(dt, R, K);
+  if (st != NM_OK) return st;
+  if (steps < 1 || steps > 100 || !(eps >= 0.f)) return NM_ERR_SHAPE;
+  if (missing(G, R * K) || missing(out, R * K)) return NM_ERR_NULL;
+  if (R * K == 0) return NM_OK;
+  if (!aligned16(G) || !aligned16(out)) return NM_ERR_ALIGN;
+  const size_t need = nm::orth_workspace_bytes(R, K, (int)dt);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const int64_t bytes = R * K * elem_bytes(dt);
+  const Range r[] = {{workspace, (int64_t)need}, {G, bytes}, {out, bytes}};
+  if (any_alias(r, 1, 3) || (out != G && overlaps(out, G, bytes))) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_orthogonalize(G, (int)dt, R, K, steps, eps, out, workspace,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,250 @@
+// nm_gemm.h -- the dense 16-bit matrix product on the matrix cores (gfx950) that the cross
+// entropy and the orthogonalised update are built from: one workgroup's tile of
+//   C[m, n] = sum over k of A(m, k) B(n, k),
+// fp32 accumulators, which the calling kernel's epilogue then turns into what it needs.
+//
+// Either operand is stored with k contiguous (rows of k) or with k as the row index
+// ("strided"), so no operand is ever transposed in memory.  The sum's length is a multiple of
+// 64 (the callers pad with zeros); rows of m and n past the matrix read another of its rows
+// and the epilogue drops them.  A strided operand's rows are whole 16-byte pieces (ld and the
+// width are multiples of 8).
+//
+// A step of 64 k of both operands is brought into LDS by direct loads, one step ahead of the
+// step that is being multiplied (two stages).  A wave owns 32 FM x 32 FN of the tile and uses
+// v_mfma_f32_32x32x16.  LDS layouts of a stage, both free of bank conflicts for their reads:
+//   k contiguous: 128 bytes a row of the tile, 16-byte chunk c at c ^ (row & 7); a fragment is
+//     one 16-byte read per lane;
+//   strided: a row of the tile's columns for each k, 32-byte pair p at p ^ 2 (k & 3); a
+//     fragment is two transposing reads (ds_read_b64_tr_b16).
+#pragma once
+
+#include "nm_launch.h"
+#include "nm_mfma.h"
+
+namespace nm {
+namespace {
+
+constexpr int kGemmStep = 64;  // k per step
+
+// One operand: element (row, k) at p[row * ld + k], or at p[k * ld + row] if strided.  rows:
+// rows of the whole matrix from p on (loads past them read the last one).
+struct GemmOperand {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t rows;
+};
+
+// Workgroups are dealt to the XCDs in turn; each XCD takes a contiguous run of tiles, walked
+// in blocks of gm x gn so that the tiles it works on at once share rows of A and B in its L2.
+struct GemmMap {
+  int tiles_m, tiles_n, xcds, per_xcd, gm, gn;
+  __device__ __forceinline__ bool tile_of(int b, int& tm, int& tn) const {
+    const int t = (b % xcds) * per_xcd + b / xcds;
+    if (t >= tiles_m * tiles_n) return false;
+    const int g_m = t / (gm * tiles_n);
+    const int rows = min(gm, tiles_m - g_m * gm);
+    const int u = t - g_m * gm * tiles_n;
+    const int g_n = u / (rows * gn);
+    const int v = u - g_n * rows * gn;
+    tm = g_m * gm + v % rows;
+    tn = g_n * gn + v / rows;
+    return true;
+  }
+  int groups() const { return per_xcd * xcds; }
+};
+
+inline GemmMap make_gemm_map(int64_t tiles_m, int64_t tiles_n) {
+  GemmMap map;
+  map.tiles_m = (int)tiles_m;
+  map.tiles_n = (int)tiles_n;
+  map.xcds = xcd_count();
+  map.per_xcd = (int)((tiles_m * tiles_n + map.xcds - 1) / map.xcds);
+  map.gn = tiles_n < 4 ? (int)tiles_n : 4;
+  map.gm = 32 / map.gn;
+  return map;
+}
+
+// WM x WN waves of 32 FM rows x 32 FN columns each; AS / BS: operand stored strided;
+// SWAP: accumulators hold C transposed within a fragment (lane = row, registers = columns).
+template <int WM, int WN, int FM, int FN, bool AS, bool BS, bool BF16, bool SWAP>
+struct Gemm {
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kBM = 32 * FM * WM, kBN = 32 * FN * WN;
+  static constexpr int kABytes = kBM * 2 * kGemmStep, kBBytes = kBN * 2 * kGemmStep;
+  static constexpr int kStage = kABytes + kBBytes, kLds = 2 * kStage;
+  static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "whole loads");
+  static_assert(kLds <= 160 * 1024, "LDS");
+
+  typedef float16v_t Acc[FM][FN];
+
+  // Byte offset from (row0, k = 0) of what lane `lane` reads in load `j` of wave `wave`; left:
+  // rows of the matrix from row0 on, kleft: k's from the step's first one on.
+  template <bool STRIDED, int ROWS>
+  static __device__ __forceinline__ uint32_t source(int j, int wave, int lane, int64_t ld,
+                                                    int64_t left, int64_t kleft) {
+    const int slot = (j * kWaves + wave) * 64 + lane;  // 16-byte slot of the tile
+    if constexpr (!STRIDED) {
+      const int r = slot >> 3, c = (slot & 7) ^ (r & 7);
+      const int64_t row = r < left ? r : left - 1;
+      return (uint32_t)(row * ld * 2 + 16 * c);
+    } else {
+      constexpr int kChunks = ROWS / 8, kPairs = ROWS / 16;
+      const int k = slot / kChunks, pc = slot % kChunks;
+      const int c = 2 * ((pc >> 1) ^ (((k & 3) << 1) & (kPairs - 1))) + (pc & 1);
+      const int64_t col = 8 * c < left ? 8 * c : 0;
+      const int64_t row = k < kleft ? k : kleft - 1;
+      return (uint32_t)((row * ld + col) * 2);
+    }
+  }
+
+  // Byte offset within an operand's part of a stage of the calling lane's fragment `f` (32 rows
+  // from 32 f of the wave's first row w0) for k 16 kk .. 16 kk + 15.
+  template <bool STRIDED, int ROWS>
+  static __device__ __forceinline__ u32x4_t fragment(const uint8_t* tile, int w0, int f, int kk,
+                                                     int lane) {
+    const int q = lane >> 5;
+    if constexpr (!STRIDED) {
+      const int r = w0 + 32 * f + (lane & 31);
+      return *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((2 * kk + q) ^ (r & 7)) << 4));
+    } else {
+      [[maybe_unused]] constexpr int kPairs = ROWS / 16;
+      const int l16 = lane & 15, half = (lane >> 4) & 1;
+      [[maybe_unused]] const int k = 16 * kk + 8 * q + (l16 >> 2);
+      [[maybe_unused]] const int p = (w0 + 32 * f + 16 * half) / 16;
+#if defined(__HIP_DEVICE_COMPILE__)
+      // rows k and k + 4 have the same swizzle
+      const uint8_t* at =
+          tile + k * (ROWS * 2) + ((p ^ (((k & 3) << 1) & (kPairs - 1))) << 5) + 8 * (l16 & 3);
+      const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)at);
+      const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(at + 4 * ROWS * 2));
+      return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#else
+      return u32x4_t{};
+#endif
+    }
+  }
+
+  static __device__ __forceinline__ float16v_t mfma(const u32x4_t& a, const u32x4_t& b,
+                                                    const float16v_t& c) {
+    const u32x4_t& x = SWAP ? b : a;
+    const u32x4_t& y = SWAP ? a : b;
+    if constexpr (BF16)
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, x),
+                                                     __builtin_bit_cast(bf16x8_t, y), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, x),
+                                                    __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
+  }
+
+  // acc += the tile at (m0, n0) over `steps` steps of each of `segments` pairs of operands.
+  // Three segments are the pairs (a, b), (a, b + b_lo), (a + a_lo, b), offsets in elements.
+  // klen: rows of a strided A (past them its last step reads the last one again, against zeros
+  // of B); B always has whole steps.
+  static __device__ __forceinline__ void run(const GemmOperand& a, const GemmOperand& b,
+                                             int64_t m0, int64_t n0, int steps, int64_t klen,
+                                             uint8_t* smem, Acc& acc, int segments = 1,
+                                             int64_t a_lo = 0, int64_t b_lo = 0) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int64_t a_left = a.rows - m0, b_left = b.rows - n0;
+    const uint16_t* a0 = a.p + (AS ? m0 : m0 * a.ld);
+    const uint16_t* b0 = b.p + (BS ? n0 : n0 * b.ld);
+    const int64_t a_step = AS ? kGemmStep * a.ld : kGemmStep;
+    const int64_t b_step = BS ? kGemmStep * b.ld : kGemmStep;
+    const bool ragged = AS && klen < (int64_t)steps * kGemmStep;
+    uint32_t av[kALoads], bv[kBLoads];
+#pragma unroll
+    for (int j = 0; j < kALoads; ++j)
+      av[j] = source<AS, kBM>(j, wave, lane, a.ld, a_left, kGemmStep);
+#pragma unroll
+    for (int j = 0; j < kBLoads; ++j)
+      bv[j] = source<BS, kBN>(j, wave, lane, b.ld, b_left, kGemmStep);
+    const uint32_t lds0 = lds_addr(smem);
+    const int total = steps * segments;
+
+    auto issue = [&](int s) {
+      const int seg = segments == 1 ? 0 : s / steps, t = segments == 1 ? s : s % steps;
+      // segments: (hi, hi), (hi, lo), (lo, hi)
+      const uint16_t* pa = a0 + t * a_step + (seg == 2 ? a_lo : 0);
+      const uint16_t* pb = b0 + t * b_step + (seg == 1 ? b_lo : 0);
+      const uint32_t st = lds0 + (s & 1) * kStage;
+      if (ragged && t == steps - 1) {  // A's rows end inside this step
+        const int64_t kleft = klen - (int64_t)t * kGemmStep;
+#pragma unroll
+        for (int j = 0; j < kALoads; ++j)
+          global_to_lds_sv<16>(pa, source<AS, kBM>(j, wave, lane, a.ld, a_left, kleft),
+                               st + (j * kWaves + wave) * 1024);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kALoads; ++j)
+          global_to_lds_sv<16>(pa, av[j], st + (j * kWaves + wave) * 1024);
+      }
+#pragma unroll
+      for (int j = 0; j < kBLoads; ++j)
+        global_to_lds_sv<16>(pb, bv[j], st + kABytes + (j * kWaves + wave) * 1024);
+    };
+
+    if (total > 0) issue(0);
+    for (int s = 0; s < total; ++s) {
+      // step s has landed for every wave, and no wave reads the other stage any more
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (s + 1 < total) issue(s + 1);
+      const uint8_t* ta = smem + (s & 1) * kStage;
+      const uint8_t* tb = ta + kABytes;
+#pragma unroll
+      for (int kk = 0; kk < kGemmStep / 16; ++kk) {
+        u32x4_t fa[FM], fb[FN];
+#pragma unroll
+        for (int f = 0; f < FM; ++f) fa[f] = fragment<AS, kBM>(ta, wm * 32 * FM, f, kk, lane);
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fb[f] = fragment<BS, kBN>(tb, wn * 32 * FN, f, kk, lane);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // smem may be reused
+  }
+
+  // Launches kKernel, which uses this tile's LDS, on map.groups() x splits workgroups.
+  template <auto kKernel, typename Args>
+  static hipError_t launch(const Args& args, const GemmMap& map, int splits, hipStream_t s) {
+    static const hipError_t attr = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (attr != hipSuccess) return attr;
+    kKernel<<<dim3((unsigned)map.groups(), (unsigned)splits), kThreads, kLds, s>>>(args);
+    return hipGetLastError();
+  }
+
+  static __device__ __forceinline__ void clear(Acc& acc) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = float16v_t{};
+  }
+
+  // Calls f(row, col, v) for every four consecutive columns (SWAP) that the calling lane holds;
+  // row and col are of the whole matrix, v the four values.
+  template <typename F>
+  static __device__ __forceinline__ void each4(const Acc& acc, int64_t m0, int64_t n0, F&& f) {
+    static_assert(SWAP, "rows by lane");
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row0 = m0 + (wave / WN) * 32 * FM + (lane & 31);
+    const int64_t col0 = n0 + (wave % WN) * 32 * FN + 4 * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          f(row0 + 32 * i, col0 + 32 * j + 8 * g,
+            float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                     acc[i][j][4 * g + 3]});
+  }
+};
+
+}  // namespace
+}  // namespace nm

@@ -66,4 +66,30 @@ hipError_t launch_prune(const void* W, int dt, int64_t R, int64_t K, int n, int 
 hipError_t launch_srste_grad(const void* W, const void* G, int dt, int64_t R, int64_t K, int n,
                              int m, float decay, void* out, hipStream_t s);
 
+// 4-bit weights (nm_quant.hip): codes and scales in the order of include/nm.h; blocked: W is
+// the 2:4 value array of NM_LAYOUT_BLOCKED with C kept values a row; meta null for dense codes.
+hipError_t launch_quantize(const void* W, int dt, int64_t R, int64_t C, bool blocked, int group,
+                           void* codes, void* scales, int scale_dt, hipStream_t s);
+hipError_t launch_dequantize(const void* codes, const void* scales, int scale_dt, int64_t R,
+                             int64_t C, bool blocked, int group, void* W, hipStream_t s);
+size_t matvec_workspace_bytes(int64_t K, int64_t T);
+hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
+                         int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
+                         void* workspace, hipStream_t s);
+
+// Cross entropy of W X and its gradient (nm_xent.hip); the workspaces are 256-byte aligned parts.
+size_t xent_workspace_bytes(int64_t V, int64_t K, int64_t T);
+size_t xent_grad_workspace_bytes(int64_t V, int64_t K, int64_t T);
+hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t K, int64_t T,
+                       const int64_t* target, float* loss, float* lse, void* workspace,
+                       hipStream_t s);
+hipError_t launch_xent_grad(const void* W, const void* X, int dt, int64_t V, int64_t K, int64_t T,
+                            const int64_t* target, const float* lse, const float* gout, void* dW,
+                            void* dX, void* workspace, hipStream_t s);
+
+// Newton-Schulz steps on G (nm_orth.hip).
+size_t orth_workspace_bytes(int64_t R, int64_t K, int dt);
+hipError_t launch_orthogonalize(const void* G, int dt, int64_t R, int64_t K, int steps, float eps,
+                                void* out, void* workspace, hipStream_t s);
+
 }  // namespace nm

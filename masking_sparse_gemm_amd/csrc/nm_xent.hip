@@ -1,0 +1,539 @@
+// nm_xent.hip -- softmax cross entropy of the logits L = W X (V x T) over a large vocabulary
+// V (nm_xent), and its gradient (nm_xent_grad), without ever storing the logits.
+//
+//   lse[t] = log sum over v of exp L[v, t],   loss[t] = lse[t] - L[y_t, t]
+//   P[v, t] = (exp(L[v, t] - lse[t]) - [v = y_t]) g[t],   dW = P X^T,   dX = W^T P
+//
+// Loss: the product's tiles (nm_gemm.h) end in an epilogue that reduces each wave's rows of a
+// column to their maximum and the sum of exp(. - maximum); a second kernel joins those.
+//
+// Gradient: the vocabulary is taken in pieces whose P fits a bounded workspace.  For each piece
+// the logits are multiplied again and leave the epilogue as P in 16 bits (the operand the next
+// two products need; the rounding is the same relative size as that of dW and dX themselves), then
+// dW of the piece is one product, and W^T P is added to fp32 sums of dX.  g is brought to a
+// power-of-two multiple that fits 16-bit numbers before the rounding, and the products are scaled
+// back in fp32, so fp16 loses no small probabilities to underflow whatever g's size.
+//
+// Tokens with a target outside 0 .. V - 1 are left out: their loss is 0 and their column of X
+// is read as zeros in the gradient, so that not even infinities or NaN in it reach dW.
+#include "nm_gemm.h"
+#include "nm_grid.h"
+
+namespace nm {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int64_t kPieceBytes = 64 << 20;  // of P
+constexpr int kMaxSplit = 8;
+
+int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
+int64_t pad256b(int64_t n) { return (n + 255) / 256 * 256; }
+
+// X (K x T) -> rp x cp with zeros past it, and, given targets, at the columns left out.
+// W rows -> padded rows are the same copy without targets.
+__global__ void __launch_bounds__(256)
+    pad_kernel(const uint16_t* __restrict__ in, int64_t rows, int64_t cols, int64_t rp, int64_t cp,
+               const int64_t* __restrict__ target, int64_t V, uint16_t* __restrict__ out) {
+  const int64_t chunks = cp / 8, total = rp * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / chunks, c = i % chunks * 8;
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      bool take = r < rows && c + e < cols;
+      if (take && target) take = target[c + e] >= 0 && target[c + e] < V;
+      h[e] = take ? in[r * cols + c + e] : 0u;
+    }
+    *reinterpret_cast<u32x4_t*>(out + r * cp + c) =
+        u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  }
+}
+
+// ---- loss ------------------------------------------------------------------------------
+
+struct StatsArgs {
+  GemmOperand w, x;
+  int steps;
+  GemmMap map;
+  int64_t V, T;
+  const int64_t* target;
+  float *top, *sum;  // [rows of waves][T]
+  float* hit;        // [T]: the target's logit
+};
+
+template <class G, int FM, int FN, int WM, int WN>
+__global__ void __launch_bounds__(G::kThreads) stats_kernel(StatsArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int tm, tn;
+  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
+  typename G::Acc acc;
+  G::clear(acc);
+  G::run(p.w, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+  const int64_t row0 = m0 + wm * 32 * FM + 4 * (lane >> 5);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int64_t t = n0 + wn * 32 * FN + 32 * j + (lane & 31);
+    const bool in = t < p.T;
+    // the target as a row of this lane's: its registers hold rows 32 i + 8 g + e
+    const int64_t y = in ? p.target[t] : -1;
+    const int64_t yr = y - row0;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int off = 32 * i + 8 * (r / 4) + r % 4;
+        if (in && y < p.V && yr == off) p.hit[t] = acc[i][j][r];
+        if (row0 + off >= p.V) acc[i][j][r] = -INFINITY;
+        m = fmaxf(m, acc[i][j][r]);
+      }
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float shift = m == -INFINITY ? 0.f : m * kLog2e;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -shift));
+    s += __shfl_xor(s, 32);
+    if (in && lane < 32) {
+      const int64_t at = ((int64_t)tm * WM + wm) * p.T + t;
+      p.top[at] = m;
+      p.sum[at] = s;
+    }
+  }
+}
+
+// 32 tokens a workgroup, 32 threads a token; each joins every 32nd partial, then they join.
+__global__ void __launch_bounds__(1024)
+    join_kernel(const float* __restrict__ top, const float* __restrict__ sum, int64_t parts,
+                int64_t T, int64_t V, const int64_t* __restrict__ target,
+                const float* __restrict__ hit, float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float ms[32][33], ss[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * 32 + x;
+  float m = -INFINITY, s = 0.f;
+  if (t < T) {
+    for (int64_t i = y; i < parts; i += 32) {
+      const float mi = top[i * T + t], si = sum[i * T + t];
+      const float n = fmaxf(m, mi), sh = n == -INFINITY ? 0.f : n;
+      s = s * __builtin_amdgcn_exp2f((m - sh) * kLog2e) +
+          si * __builtin_amdgcn_exp2f((mi - sh) * kLog2e);
+      m = n;
+    }
+  }
+  ms[y][x] = m;
+  ss[y][x] = s;
+  __syncthreads();
+  if (y == 0 && t < T) {
+    float top_all = -INFINITY;
+    for (int i = 0; i < 32; ++i) top_all = fmaxf(top_all, ms[i][x]);
+    const float sh = top_all == -INFINITY ? 0.f : top_all;
+    float total = 0.f;
+    for (int i = 0; i < 32; ++i) total += ss[i][x] * __builtin_amdgcn_exp2f((ms[i][x] - sh) * kLog2e);
+    const float l = sh + __builtin_amdgcn_logf(total) * kLn2;
+    lse[t] = l;
+    const int64_t yt = target[t];
+    loss[t] = yt >= 0 && yt < V ? l - hit[t] : 0.f;
+  }
+}
+
+template <int WM, int WN, int FM, int FN, bool BF16>
+hipError_t launch_stats(StatsArgs p, hipStream_t s) {
+  typedef Gemm<WM, WN, FM, FN, false, true, BF16, false> G;
+  p.map = make_gemm_map((p.V + G::kBM - 1) / G::kBM, (p.T + G::kBN - 1) / G::kBN);
+  return G::template launch<stats_kernel<G, FM, FN, WM, WN>>(p, p.map, 1, s);
+}
+
+struct LossLayout {
+  int64_t Kp, Tp;
+  bool copy_x, copy_w, narrow;
+  int64_t x, w, top, sum, hit, total, parts;
+  LossLayout(int64_t V, int64_t K, int64_t T) {
+    Kp = pad64(K);
+    copy_w = K % 64 != 0;
+    copy_x = copy_w || T % 8 != 0;
+    Tp = copy_x ? pad64(T) : T;
+    // a narrow tile wastes less of the matrix cores on few tokens and spreads W over more units
+    narrow = T <= 64;
+    parts = narrow ? (V + 127) / 128 * 2 : (V + 255) / 256 * 2;
+    x = 0;
+    w = x + (copy_x ? pad256b(Kp * Tp * 2) : 0);
+    top = w + (copy_w ? pad256b(V * Kp * 2) : 0);
+    sum = top + pad256b(parts * T * 4);
+    hit = sum + pad256b(parts * T * 4);
+    total = hit + pad256b(T * 4);
+  }
+};
+
+unsigned pad_grid(int64_t chunks) { return stride_grid(chunks, 256); }
+
+// ---- gradient --------------------------------------------------------------------------
+
+struct TokenArgs {  // of the tokens, padded to a whole number of 64
+  int* y;           // target, -1 where left out
+  float* lse;
+  float* g;         // g 2^e
+  float* back;      // one number: 2^-e
+};
+
+// One workgroup: the largest |g| of the tokens that count, then 2^e with 2^13 <= 2^e max < 2^14.
+__global__ void __launch_bounds__(1024)
+    tokens_kernel(const int64_t* __restrict__ target, const float* __restrict__ lse,
+                  const float* __restrict__ gout, int64_t V, int64_t T, int64_t Tp, TokenArgs out) {
+  __shared__ float part[16];
+  float top = 0.f;
+  for (int64_t t = threadIdx.x; t < T; t += 1024)
+    if (target[t] >= 0 && target[t] < V) top = fmaxf(top, fabsf(gout[t]));
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, part[i]);
+  int e = 0;
+  if (top > 0.f && top < INFINITY) frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
+  e = min(max(14 - e, -100), 100);
+  if (threadIdx.x == 0) *out.back = ldexpf(1.f, -e);
+  for (int64_t t = threadIdx.x; t < Tp; t += 1024) {
+    const bool live = t < T && target[t] >= 0 && target[t] < V;
+    out.y[t] = live ? (int)target[t] : -1;
+    out.lse[t] = live ? lse[t] : 0.f;
+    out.g[t] = live ? ldexpf(gout[t], e) : 0.f;
+  }
+}
+
+struct ProbArgs {
+  GemmOperand w, x;  // w from the piece's first row on
+  int steps;
+  GemmMap map;
+  int64_t v0, V;     // the piece's first row; rows of W
+  int64_t rows, Tp;  // of P, padded
+  TokenArgs tok;
+  uint16_t* P;       // rows x Tp
+};
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return BF16 ? f32_to_bf16(a) | f32_to_bf16(b) << 16 : f32_to_f16(a) | f32_to_f16(b) << 16;
+}
+
+template <class G, bool BF16>
+__global__ void __launch_bounds__(G::kThreads) prob_kernel(ProbArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int tm, tn;
+  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
+  typename G::Acc acc;
+  G::clear(acc);
+  G::run(p.w, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t l) {
+    if (row >= p.rows || col >= p.Tp) return;
+    const float4_t lse = *reinterpret_cast<const float4_t*>(p.tok.lse + col);
+    const float4_t g = *reinterpret_cast<const float4_t*>(p.tok.g + col);
+    const int4 y = *reinterpret_cast<const int4*>(p.tok.y + col);
+    const int v = (int)(p.v0 + row);
+    const int ys[4] = {y.x, y.y, y.z, y.w};
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = __builtin_amdgcn_exp2f((l[i] - lse[i]) * kLog2e);
+      q[i] = v < p.V && ys[i] >= 0 ? (e - (v == ys[i] ? 1.f : 0.f)) * g[i] : 0.f;
+    }
+    *reinterpret_cast<u32x2_t*>(p.P + row * p.Tp + col) =
+        u32x2_t{pack2<BF16>(q[0], q[1]), pack2<BF16>(q[2], q[3])};
+  });
+}
+
+struct GradXArgs {
+  GemmOperand w, q;  // W's piece and P, both with v as their row index
+  int64_t klen;      // rows of the piece
+  int steps, per;    // steps of 64 of them; of which each split takes `per`
+  GemmMap map;
+  int64_t K, Tp;
+  float* sums;       // [splits][K][Tp]
+  bool add;          // to what earlier pieces left there
+};
+
+template <class G>
+__global__ void __launch_bounds__(G::kThreads) grad_x_kernel(GradXArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int tm, tn;
+  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
+  const int s0 = blockIdx.y * p.per, steps = min(p.per, p.steps - s0);
+  GemmOperand w = p.w, q = p.q;
+  w.p += (int64_t)s0 * kGemmStep * w.ld;
+  q.p += (int64_t)s0 * kGemmStep * q.ld;
+  typename G::Acc acc;
+  G::clear(acc);
+  if (steps > 0) G::run(w, q, m0, n0, steps, p.klen - (int64_t)s0 * kGemmStep, smem, acc);
+  float* out = p.sums + (int64_t)blockIdx.y * p.K * p.Tp;
+  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t v) {
+    if (row >= p.K || col >= p.Tp) return;
+    float4_t* o = reinterpret_cast<float4_t*>(out + row * p.Tp + col);
+    if (p.add) {
+      const float4_t b = *o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += b[i];
+    }
+    *o = v;
+  });
+}
+
+struct GradWArgs {
+  GemmOperand q, x;
+  int steps;
+  GemmMap map;
+  int64_t rows, K;  // rows of W in the piece
+  const float* back;
+  uint16_t* dW;     // from the piece's first row on
+};
+
+template <class G, bool BF16>
+__global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int tm, tn;
+  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
+  typename G::Acc acc;
+  G::clear(acc);
+  G::run(p.q, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+  const float back = *p.back;
+  const bool whole = p.K % 4 == 0;
+  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t v) {
+    if (row >= p.rows || col >= p.K) return;
+    uint16_t* o = p.dW + row * p.K + col;
+    const uint32_t a = pack2<BF16>(v[0] * back, v[1] * back);
+    const uint32_t b = pack2<BF16>(v[2] * back, v[3] * back);
+    if (whole) {
+      *reinterpret_cast<u32x2_t*>(o) = u32x2_t{a, b};
+    } else {
+      const uint32_t h[4] = {a & 0xFFFFu, a >> 16, b & 0xFFFFu, b >> 16};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < p.K) o[i] = (uint16_t)h[i];
+    }
+  });
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    finish_x_kernel(const float* __restrict__ sums, int splits, int64_t K, int64_t T, int64_t Tp,
+                    const float* __restrict__ back, uint16_t* __restrict__ dX) {
+  const float f = *back;
+  const int64_t total = K * Tp / 4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    float4_t v = reinterpret_cast<const float4_t*>(sums)[i];
+    for (int z = 1; z < splits; ++z) {
+      const float4_t b = reinterpret_cast<const float4_t*>(sums)[z * total + i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += b[e];
+    }
+    const int64_t k = 4 * i / Tp, t = 4 * i % Tp;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t + e < T) store_from_f32<BF16 ? kBF16 : kF16>(dX, k * T + t + e, v[e] * f);
+  }
+}
+
+struct GradLayout {
+  int64_t Kp, Tp, piece;  // piece: rows of W at a time
+  bool copy_w, big_x;     // big_x: 256 x 256 tiles for dX
+  int splits;
+  int64_t x, w, tok_y, tok_lse, tok_g, back, P, sums, total;
+  GradLayout(int64_t V, int64_t K, int64_t T) {
+    Kp = pad64(K);
+    Tp = pad64(T);
+    copy_w = K % 64 != 0;
+    piece = kPieceBytes / (2 * Tp) / 256 * 256;
+    if (piece < 256) piece = 256;
+    if (piece > V) piece = V;
+    const int64_t big = ((K + 255) / 256) * ((Tp + 255) / 256);
+    const int64_t mid = ((K + 127) / 128) * ((Tp + 127) / 128);
+    big_x = big * kMaxSplit >= 256;
+    const int64_t tiles = big_x ? big : mid;
+    int64_t z = (256 + tiles - 1) / tiles;
+    z = z < 1 ? 1 : z > kMaxSplit ? kMaxSplit : z;
+    const int64_t steps = (piece + 63) / 64;
+    while (z > 1 && steps / z < 8) --z;
+    splits = (int)z;
+    x = 0;
+    w = x + pad256b(Kp * Tp * 2);
+    tok_y = w + (copy_w ? pad256b(V * Kp * 2) : 0);
+    tok_lse = tok_y + pad256b(Tp * 4);
+    tok_g = tok_lse + pad256b(Tp * 4);
+    back = tok_g + pad256b(Tp * 4);
+    P = back + 256;
+    sums = P + pad256b(pad64(piece) * Tp * 2);
+    total = sums + pad256b((int64_t)splits * K * Tp * 4);
+  }
+};
+
+template <class G, bool BF16>
+hipError_t launch_prob(ProbArgs p, hipStream_t s) {
+  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.Tp + G::kBN - 1) / G::kBN);
+  return G::template launch<prob_kernel<G, BF16>>(p, p.map, 1, s);
+}
+template <class G>
+hipError_t launch_grad_x(GradXArgs p, int splits, hipStream_t s) {
+  p.map = make_gemm_map((p.K + G::kBM - 1) / G::kBM, (p.Tp + G::kBN - 1) / G::kBN);
+  return G::template launch<grad_x_kernel<G>>(p, p.map, splits, s);
+}
+template <class G, bool BF16>
+hipError_t launch_grad_w(GradWArgs p, hipStream_t s) {
+  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.K + G::kBN - 1) / G::kBN);
+  return G::template launch<grad_w_kernel<G, BF16>>(p, p.map, 1, s);
+}
+
+__global__ void __launch_bounds__(256) zero_kernel(uint16_t* out, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    out[i] = 0;
+}
+
+template <bool BF16>
+hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, int64_t T,
+                    const int64_t* target, const float* lse, const float* gout, uint16_t* dW,
+                    uint16_t* dX, uint8_t* ws, hipStream_t s) {
+  if (T == 0) {  // no token: dX is empty
+    zero_kernel<<<stride_grid(V * K, 256), 256, 0, s>>>(dW, V * K);
+    return hipGetLastError();
+  }
+  const GradLayout L(V, K, T);
+  uint16_t* Xp = reinterpret_cast<uint16_t*>(ws + L.x);
+  uint16_t* P = reinterpret_cast<uint16_t*>(ws + L.P);
+  float* sums = reinterpret_cast<float*>(ws + L.sums);
+  const TokenArgs tok{reinterpret_cast<int*>(ws + L.tok_y), reinterpret_cast<float*>(ws + L.tok_lse),
+                      reinterpret_cast<float*>(ws + L.tok_g), reinterpret_cast<float*>(ws + L.back)};
+  hipError_t e;
+  tokens_kernel<<<1, 1024, 0, s>>>(target, lse, gout, V, T, L.Tp, tok);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  pad_kernel<<<pad_grid(L.Kp * L.Tp / 8), 256, 0, s>>>(X, K, T, L.Kp, L.Tp, target, V, Xp);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const uint16_t* Wp = W;
+  if (L.copy_w) {
+    uint16_t* w = reinterpret_cast<uint16_t*>(ws + L.w);
+    pad_kernel<<<pad_grid(V * L.Kp / 8), 256, 0, s>>>(W, V, K, V, L.Kp, nullptr, 0, w);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    Wp = w;
+  }
+  const int64_t ldw = L.Kp;
+  for (int64_t v0 = 0; v0 < V; v0 += L.piece) {
+    const int64_t rows = V - v0 < L.piece ? V - v0 : L.piece, rp = pad64(rows);
+    ProbArgs a{};
+    a.w = GemmOperand{Wp + v0 * ldw, ldw, rows};
+    a.x = GemmOperand{Xp, L.Tp, L.Tp};
+    a.steps = (int)(L.Kp / kGemmStep);
+    a.v0 = v0;
+    a.V = V;
+    a.rows = rp;
+    a.Tp = L.Tp;
+    a.tok = tok;
+    a.P = P;
+    const int64_t big = ((rp + 255) / 256) * ((L.Tp + 255) / 256);
+    if (L.Tp > 128 && big >= 128) e = launch_prob<Gemm<2, 4, 4, 2, false, true, BF16, true>, BF16>(a, s);
+    else if (L.Tp > 64) e = launch_prob<Gemm<2, 2, 2, 2, false, true, BF16, true>, BF16>(a, s);
+    else e = launch_prob<Gemm<2, 2, 2, 1, false, true, BF16, true>, BF16>(a, s);
+    if (e != hipSuccess) return e;
+
+    GradWArgs b{};
+    b.q = GemmOperand{P, L.Tp, rp};
+    b.x = GemmOperand{Xp, L.Tp, L.Kp};
+    b.steps = (int)(L.Tp / kGemmStep);
+    b.rows = rows;
+    b.K = K;
+    b.back = tok.back;
+    b.dW = dW + v0 * K;
+    if (((rows + 255) / 256) * ((K + 255) / 256) >= 128)
+      e = launch_grad_w<Gemm<2, 4, 4, 2, false, false, BF16, true>, BF16>(b, s);
+    else
+      e = launch_grad_w<Gemm<2, 2, 2, 2, false, false, BF16, true>, BF16>(b, s);
+    if (e != hipSuccess) return e;
+
+    GradXArgs c{};
+    c.w = GemmOperand{Wp + v0 * ldw, ldw, L.Kp};
+    c.q = GemmOperand{P, L.Tp, L.Tp};
+    c.klen = rows;
+    c.steps = (int)(rp / kGemmStep);
+    c.per = (c.steps + L.splits - 1) / L.splits;
+    c.K = K;
+    c.Tp = L.Tp;
+    c.sums = sums;
+    c.add = v0 > 0;
+    e = L.big_x ? launch_grad_x<Gemm<2, 4, 4, 2, true, true, BF16, true>>(c, L.splits, s)
+                : launch_grad_x<Gemm<2, 2, 2, 2, true, true, BF16, true>>(c, L.splits, s);
+    if (e != hipSuccess) return e;
+  }
+  finish_x_kernel<BF16><<<stride_grid(K * L.Tp / 4, 256), 256, 0, s>>>(sums, L.splits, K, T, L.Tp,
+                                                                     tok.back, dX);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(int64_t V, int64_t K, int64_t T) {
+  return (size_t)LossLayout(V, K, T).total;
+}
+size_t xent_grad_workspace_bytes(int64_t V, int64_t K, int64_t T) {
+  return (size_t)GradLayout(V, K, T).total;
+}
+
+hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t K, int64_t T,
+                       const int64_t* target, float* loss, float* lse, void* workspace,
+                       hipStream_t s) {
+  const LossLayout L(V, K, T);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  StatsArgs p{};
+  const uint16_t* w = static_cast<const uint16_t*>(W);
+  const uint16_t* x = static_cast<const uint16_t*>(X);
+  hipError_t e;
+  if (L.copy_x) {
+    uint16_t* c = reinterpret_cast<uint16_t*>(ws + L.x);
+    pad_kernel<<<pad_grid(L.Kp * L.Tp / 8), 256, 0, s>>>(x, K, T, L.Kp, L.Tp, nullptr, 0, c);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    x = c;
+  }
+  if (L.copy_w) {
+    uint16_t* c = reinterpret_cast<uint16_t*>(ws + L.w);
+    pad_kernel<<<pad_grid(V * L.Kp / 8), 256, 0, s>>>(w, V, K, V, L.Kp, nullptr, 0, c);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    w = c;
+  }
+  p.w = GemmOperand{w, L.Kp, V};
+  p.x = GemmOperand{x, L.Tp, L.Tp};
+  p.steps = (int)(L.Kp / kGemmStep);
+  p.V = V;
+  p.T = T;
+  p.target = target;
+  p.top = reinterpret_cast<float*>(ws + L.top);
+  p.sum = reinterpret_cast<float*>(ws + L.sum);
+  p.hit = reinterpret_cast<float*>(ws + L.hit);
+  const bool bf16 = dt == kBF16;
+  if (L.narrow)
+    e = bf16 ? launch_stats<2, 2, 2, 1, true>(p, s) : launch_stats<2, 2, 2, 1, false>(p, s);
+  else
+    e = bf16 ? launch_stats<2, 4, 4, 2, true>(p, s) : launch_stats<2, 4, 4, 2, false>(p, s);
+  if (e != hipSuccess) return e;
+  join_kernel<<<(unsigned)((T + 31) / 32), 1024, 0, s>>>(p.top, p.sum, L.parts, T, V, target, p.hit,
+                                                       loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_grad(const void* W, const void* X, int dt, int64_t V, int64_t K, int64_t T,
+                            const int64_t* target, const float* lse, const float* gout, void* dW,
+                            void* dX, void* workspace, hipStream_t s) {
+  const uint16_t* w = static_cast<const uint16_t*>(W);
+  const uint16_t* x = static_cast<const uint16_t*>(X);
+  uint16_t* a = static_cast<uint16_t*>(dW);
+  uint16_t* b = static_cast<uint16_t*>(dX);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return dt == kBF16 ? run_grad<true>(w, x, V, K, T, target, lse, gout, a, b, ws, s)
+                     : run_grad<false>(w, x, V, K, T, target, lse, gout, a, b, ws, s);
+}
+
+}  // namespace nm
