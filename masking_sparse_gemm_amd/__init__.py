@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
         L.nm_scales_bytes.argtypes = [i64, i64, i32]
         L.nm_quantize.argtypes = [vp, i32, i64, i64, i32, i32, vp, vp, i32, vp]
         L.nm_dequantize.argtypes = [vp, vp, i32, i64, i64, i32, i32, vp, vp]
-        L.nm_matvec_workspace_bytes.argtypes = [i64, i64]
+        L.nm_matvec_workspace_bytes.argtypes = [i64, i64, i64, i32]
         L.nm_matvec.argtypes = [vp, vp, vp, i64, i64, i32, vp, i64, i32, vp, i32, vp, size, vp]
         L.nm_xent_workspace_bytes.argtypes = [i64, i64, i64]
         L.nm_xent.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, size, vp]
@@ -475,10 +475,20 @@ def perm_search(W: torch.Tensor, n: int = 2, m: int = 4, max_rounds: int = 1000,
 # ---- weights in 4 bits ---------------------------------------------------------------------
 
 
+_HALF = {torch.float16: NM_F16, torch.bfloat16: NM_BF16}
+
+
 def _half(dtype: torch.dtype, name: str) -> int:
-    if dtype not in (torch.float16, torch.bfloat16):
+    dt = _HALF.get(dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float16 or bfloat16")
-    return _DT[dtype]
+    return dt
+
+
+def _current_stream(t: torch.Tensor) -> int:
+    """The current stream's handle on t's device (as _stream, without building a Stream object:
+    these calls' kernels take a few microseconds)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _group(group: int) -> int:
@@ -494,18 +504,21 @@ def code_shapes(R: int, C: int, group: int):
 
 def _check_codes(codes: torch.Tensor, scales: torch.Tensor, R: int, C: int, group: int) -> int:
     cshape, sshape = code_shapes(R, C, group)
-    if codes.dtype != torch.int32 or tuple(codes.shape) != cshape or not codes.is_cuda or \
+    if codes.dtype != torch.int32 or codes.shape != cshape or not codes.is_cuda or \
             not codes.is_contiguous():
         raise ValueError(f"codes must be a contiguous int32 {cshape} GPU tensor")
     dt = _half(scales.dtype, "scales")
-    if tuple(scales.shape) != sshape or not scales.is_contiguous() or \
-            scales.device != codes.device:
+    if scales.shape != sshape or not scales.is_contiguous() or scales.device != codes.device:
         raise ValueError(f"scales must be a contiguous {sshape} tensor on the codes' device")
     return dt
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _workspace(like: torch.Tensor, nbytes: int):
+    """(tensor or None, address or None) of nbytes of scratch on like's device."""
+    if nbytes == 0:
+        return None, None
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    return ws, ws.data_ptr()
 
 
 def quantize(W: torch.Tensor, group: int = 64, layout: str = "rows", rows: int | None = None,
@@ -532,10 +545,11 @@ def quantize(W: torch.Tensor, group: int = 64, layout: str = "rows", rows: int |
         dt, R, C = _DT[W.dtype], rows, 32 * W.shape[1]
     sc = _half(s_dt, "scale_dtype")
     cshape, sshape = code_shapes(R, C, group)
-    codes = torch.empty(cshape, dtype=torch.int32, device=W.device)
-    scales = torch.empty(sshape, dtype=s_dt, device=W.device)
-    _check("nm_quantize", lib().nm_quantize(_ptr(W), dt, R, C, _layout(layout), group, _ptr(codes),
-                                            _ptr(scales), sc, _stream(W)))
+    codes = W.new_empty(cshape, dtype=torch.int32)
+    scales = W.new_empty(sshape, dtype=s_dt)
+    _check("nm_quantize", lib().nm_quantize(
+        W.data_ptr(), dt, R, C, _layout(layout), group, codes.data_ptr(), scales.data_ptr(), sc,
+        _current_stream(W)))
     return codes, scales
 
 
@@ -552,9 +566,10 @@ def dequantize(codes: torch.Tensor, scales: torch.Tensor, C: int, group: int = 6
         _check("nm_dequantize", 8)
     else:
         shape = (-(-rows // 16), C // 32, 16, 32)
-    out = torch.empty(shape, dtype=scales.dtype, device=codes.device)
-    _check("nm_dequantize", lib().nm_dequantize(_ptr(codes), _ptr(scales), dt, rows, C,
-                                                _layout(layout), group, _ptr(out), _stream(codes)))
+    out = scales.new_empty(shape)
+    _check("nm_dequantize", lib().nm_dequantize(
+        codes.data_ptr(), scales.data_ptr(), dt, rows, C, _layout(layout), group, out.data_ptr(),
+        _current_stream(codes)))
     return out
 
 
@@ -573,24 +588,27 @@ def matvec(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group: in
     if _check_codes(codes, scales, rows, K // 2 if meta is not None else K, group) != dt:
         raise ValueError("scales and X must have the same dtype")
     if meta is not None:
-        mshape = compressed_shapes(rows, K, 2, 4, "blocked")[1]
-        if meta.dtype != torch.int32 or tuple(meta.shape) != tuple(mshape) or \
-                not meta.is_contiguous():
-            raise ValueError(f"meta must be a contiguous int32 {tuple(mshape)} tensor")
-    if any(t is not None and t.device != X.device for t in (codes, meta)):
-        raise ValueError("codes, meta and X must be on the same device")
+        mshape = (-(-rows // 16), K // 64, 32)  # compressed_shapes(rows, K, 2, 4, "blocked")[1]
+        if meta.dtype != torch.int32 or meta.shape != mshape or not meta.is_contiguous():
+            raise ValueError(f"meta must be a contiguous int32 {mshape} tensor")
+        if meta.device != X.device:
+            raise ValueError("meta and X must be on the same device")
+    if codes.device != X.device:
+        raise ValueError("codes and X must be on the same device")
     y_dtype = out_dtype or X.dtype
-    if y_dtype not in (X.dtype, torch.float32):
+    if y_dtype != X.dtype and y_dtype != torch.float32:
         raise ValueError("out_dtype must be X's dtype or float32")
     if out is None:
-        out = torch.empty((rows, T), dtype=y_dtype, device=X.device)
+        out = X.new_empty((rows, T), dtype=y_dtype)
     elif out.shape != (rows, T) or out.dtype != y_dtype or not out.is_contiguous() or \
             out.device != X.device:
         raise ValueError("out has the wrong shape, dtype, layout or device")
-    ws = _workspace(int(lib().nm_matvec_workspace_bytes(K, T)), X.device)
-    _check("nm_matvec", lib().nm_matvec(
-        _ptr(codes), _ptr(scales), None if meta is None else _ptr(meta), rows, K, group, _ptr(X), T,
-        dt, _ptr(out), _DT[y_dtype], _ptr(ws), ws.numel(), _stream(X)))
+    L = lib()
+    ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
+    _check("nm_matvec", L.nm_matvec(
+        codes.data_ptr(), scales.data_ptr(), None if meta is None else meta.data_ptr(), rows, K,
+        group, X.data_ptr(), T, dt, out.data_ptr(), _DT[y_dtype], ws_ptr,
+        0 if ws is None else ws.numel(), _current_stream(X)))
     return out
 
 
@@ -615,11 +633,13 @@ def xent(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor):
     bfloat16 or float16, a column a token -- at target (int64), and the logits' log sum exp.  A
     target outside 0 .. V - 1 leaves its token out: loss 0.  The logits are not stored."""
     dt, V, K, T = _xent_inputs(W, X, target)
-    loss = torch.empty((T,), dtype=torch.float32, device=W.device)
-    lse = torch.empty_like(loss)
-    ws = _workspace(int(lib().nm_xent_workspace_bytes(V, K, T)), W.device)
-    _check("nm_xent", lib().nm_xent(_ptr(W), _ptr(X), dt, V, K, T, _ptr(target), _ptr(loss),
-                                    _ptr(lse), _ptr(ws), ws.numel(), _stream(W)))
+    loss = W.new_empty((T,), dtype=torch.float32)
+    lse = W.new_empty((T,), dtype=torch.float32)
+    L = lib()
+    ws, ws_ptr = _workspace(W, L.nm_xent_workspace_bytes(V, K, T))
+    _check("nm_xent", L.nm_xent(
+        W.data_ptr(), X.data_ptr(), dt, V, K, T, target.data_ptr(), loss.data_ptr(),
+        lse.data_ptr(), ws_ptr, 0 if ws is None else ws.numel(), _current_stream(W)))
     return loss, lse
 
 
@@ -633,10 +653,12 @@ def xent_grad(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor, lse: torch
                 t.device != W.device:
             raise ValueError(f"{name} must be a contiguous float32 ({T},) tensor on W's device")
     dW, dX = torch.empty_like(W), torch.empty_like(X)
-    ws = _workspace(int(lib().nm_xent_grad_workspace_bytes(V, K, T)), W.device)
-    _check("nm_xent_grad", lib().nm_xent_grad(
-        _ptr(W), _ptr(X), dt, V, K, T, _ptr(target), _ptr(lse), _ptr(gout), _ptr(dW), _ptr(dX),
-        _ptr(ws), ws.numel(), _stream(W)))
+    L = lib()
+    ws, ws_ptr = _workspace(W, L.nm_xent_grad_workspace_bytes(V, K, T))
+    _check("nm_xent_grad", L.nm_xent_grad(
+        W.data_ptr(), X.data_ptr(), dt, V, K, T, target.data_ptr(), lse.data_ptr(),
+        gout.data_ptr(), dW.data_ptr(), dX.data_ptr(), ws_ptr, 0 if ws is None else ws.numel(),
+        _current_stream(W)))
     return dW, dX
 
 
@@ -653,7 +675,9 @@ def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7,
         out = torch.empty_like(G)
     else:
         _same_dense(out, G, "out")
-    ws = _workspace(int(lib().nm_orthogonalize_workspace_bytes(R, K, dt)), G.device)
-    _check("nm_orthogonalize", lib().nm_orthogonalize(
-        _ptr(G), dt, R, K, int(steps), float(eps), _ptr(out), _ptr(ws), ws.numel(), _stream(G)))
+    L = lib()
+    ws, ws_ptr = _workspace(G, L.nm_orthogonalize_workspace_bytes(R, K, dt))
+    _check("nm_orthogonalize", L.nm_orthogonalize(
+        G.data_ptr(), dt, R, K, int(steps), float(eps), out.data_ptr(), ws_ptr,
+        0 if ws is None else ws.numel(), _current_stream(G)))
     return out

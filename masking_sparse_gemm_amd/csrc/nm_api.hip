@@ -591,18 +591,24 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
                                         static_cast<hipStream_t>(stream)));
 }
 
-size_t nm_matvec_workspace_bytes(int64_t K, int64_t T) {
-  if (K < 0 || T < 0 || T >= kMaxSide || K >= (int64_t)1 << 31) return 0;
-  return nm::matvec_workspace_bytes(K, T);
+namespace {
+nm_status check_matvec(int64_t R, int64_t K, int64_t T) {
+  if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 25) return NM_ERR_SHAPE;
+  return check_shape(R, K, 1);
+}
+}  // namespace
+
+size_t nm_matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, int sparse) {
+  if (check_matvec(R, K, T) != NM_OK || R * T == 0) return 0;
+  return nm::matvec_workspace_bytes(R, K, T, sparse != 0);
 }
 
 nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
                     int64_t K, int group, const void* X, int64_t T, nm_dtype dt, void* Y,
                     nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
   if (!half_dtype(dt) || (y_dt != dt && y_dt != NM_F32)) return NM_ERR_DTYPE;
-  nm_status st = check_shape(R, K, 1);
+  nm_status st = check_matvec(R, K, T);
   if (st != NM_OK) return st;
-  if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 31) return NM_ERR_SHAPE;
   if (!group_ok(group)) return NM_ERR_UNSUPPORTED;
   if (meta != nullptr && K % 64 != 0) return NM_ERR_LAYOUT;
   if (missing(codes, R * K) || missing(scales, R * K) || missing(X, K * T) || missing(Y, R * T))
@@ -610,7 +616,7 @@ nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta,
   if (R * T == 0) return NM_OK;
   if (!aligned16(codes) || !aligned16(scales) || !aligned16(meta) || !aligned16(X) || !aligned16(Y))
     return NM_ERR_ALIGN;
-  const size_t need = nm::matvec_workspace_bytes(K, T);
+  const size_t need = nm::matvec_workspace_bytes(R, K, T, meta != nullptr);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const int64_t C = meta != nullptr ? K / 2 : K;
   const Range r[] = {{Y, R * T * elem_bytes(y_dt)},

@@ -123,13 +123,30 @@ __global__ void __launch_bounds__(256)
     for (int w = 0; w < 4; ++w) {
       const uint32_t s16 = f32_to_scale<BF16S>(__uint_as_float(top[w]) / 7.f);
       const float sc = scale_to_f32<BF16S>(s16);
-      uint32_t word = 0;
+      uint32_t word;
+      if (DT != kF32 && __all(abs_bits(sc) >= 0x0D800000u)) {  // 2^-100: 1 / sc is finite
+        // Both numbers have at most 11 significant bits, so a quotient of this size is a half
+        // integer or at least 2^-13 away from one, and w * (1 / sc) is within 2^-18 of it:
+        // brought to a multiple of 2^-15 (by the addition of 384), it rounds as the quotient.
+        const float inv = 1.f / sc;
+        word = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = rintf(v[w][i] / sc);
-        // a scale of zero, and elements that are no number, take code 0
-        const int code = sc != 0.f && q == q ? (int)fminf(fmaxf(q, -8.f), 7.f) + 8 : 8;
-        word |= (uint32_t)code << (4 * (i >> 1) + 16 * (i & 1));
+        for (int i = 0; i < 8; ++i) {
+          float q = __builtin_amdgcn_fmed3f(v[w][i] * inv, -9.f, 9.f);
+          q = (q + 384.f) - 384.f;
+          q = __builtin_amdgcn_fmed3f(q, -8.f, 7.f) + 12582920.f;  // 1.5 2^23 + 8: code + 8 below
+          word |= (__float_as_uint(q) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
+        }
+        if (abs_bits(sc) >= 0x7F800000u) word = 0x88888888u;  // no numbers: codes 0
+      } else {
+        word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = rintf(v[w][i] / sc);
+          // a scale of zero, and elements that are no number, take code 0
+          const int code = sc != 0.f && q == q ? (int)fminf(fmaxf(q, -8.f), 7.f) + 8 : 8;
+          word |= (uint32_t)code << (4 * (i >> 1) + 16 * (i & 1));
+        }
       }
       out[w] = word;
       const int64_t gi = (kBlockCols * s + 32 * w) >> log_group;
@@ -189,15 +206,18 @@ __global__ void __launch_bounds__(256)
 // sums fp32; the group's sum is scaled in fp32.
 // ---------------------------------------------------------------------------------------
 
-// Four pairs of eight codes as 16-bit floats 16 + u.
+// Four pairs of eight codes as 16-bit floats 16 + u: a shift and an and-or each.  The masks come
+// in registers (mask_of), for an instruction takes only one constant of 32 bits.
 template <bool BF16>
-__device__ __forceinline__ u32x4_t codes_to_float(uint32_t w) {
-  if constexpr (BF16)
-    return u32x4_t{((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                   ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
-  else
-    return u32x4_t{((w << 6) & 0x03C003C0u) | 0x4C004C00u, ((w << 2) & 0x03C003C0u) | 0x4C004C00u,
-                   ((w >> 2) & 0x03C003C0u) | 0x4C004C00u, ((w >> 6) & 0x03C003C0u) | 0x4C004C00u};
+__device__ __forceinline__ u32x4_t codes_to_float(uint32_t w, uint32_t mask, uint32_t sixteen) {
+  constexpr int kUp = BF16 ? 3 : 6;  // to the mantissa's places under the exponent of 16
+  return u32x4_t{((w << kUp) & mask) | sixteen,
+                 (kUp > 4 ? (w << (kUp - 4)) & mask : (w >> (4 - kUp)) & mask) | sixteen,
+                 ((w >> (8 - kUp)) & mask) | sixteen, ((w >> (12 - kUp)) & mask) | sixteen};
+}
+__device__ __forceinline__ uint32_t in_register(uint32_t c) {
+  asm volatile("" : "+v"(c));
+  return c;
 }
 
 template <bool BF16>
@@ -229,100 +249,78 @@ __device__ __forceinline__ float4_t mfma_sparse(const u32x4_t& a, const u32x4_t&
                                                     0, 0);
 }
 
-// X (K x T) in the order of the B operand: for each tile of 16 columns and each eight rows of
-// K, 16 columns of eight values (256 bytes); zeros past K and T.
-__global__ void __launch_bounds__(256)
-    columns_kernel(const uint16_t* __restrict__ X, int64_t K, int64_t T, int64_t K8, int64_t total,
-                   u32x4_t* __restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t n = i & 15, k8 = (i >> 4) % K8, t = (i >> 4) / K8 * 16 + n;
-    uint32_t h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      h[e] = t < T && 8 * k8 + e < K ? X[(8 * k8 + e) * T + t] : 0u;
-    out[i] = u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-  }
-}
-
 struct MatvecArgs {
-  const u32x4_t* codes;
-  const uint16_t* scales;
+  const uint8_t* codes;
+  const uint8_t* scales;
   const uint8_t* meta;  // 2:4: the blocked metadata, else null
-  const u32x4_t* x;     // columns_kernel's order, or for one column X itself
+  const uint16_t* x;
   void* y;
-  int64_t R, T;
-  int64_t K;       // rows of X
-  int64_t K8;      // eights of rows in columns_kernel's order
-  int S;           // blocks of 128 stored columns in a row
-  int steps;       // instructions along a row: 32 stored columns each
-  int groups;      // groups in a row
+  int64_t R, T, K;
+  int S;       // blocks of 128 stored columns in a row
+  int steps;   // instructions along a row: 32 stored columns each
+  int groups;  // groups in a row
+  // several columns:
+  int slice;       // blocks of a slice of the stored columns
+  int log_along;   // log2 of the waves that share 16 rows
+  float4_t* part;  // slices x blocks of 16 rows x tiles of 16 columns x 64 lanes
 };
 
-// Eight values of the single column from row k; zeros past K.  kWhole: K % 8 == 0.
-__device__ __forceinline__ u32x4_t one_column(const MatvecArgs& a, int64_t k) {
-  if (k + 8 <= a.K) return *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(a.x) + k);
-  uint32_t h[8];
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = k + e < a.K ? x[k + e] : 0u;
-  return u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-}
+// One block of 128 stored columns of 16 rows, as one lane holds it, and where the lane finds it:
+// with the wave's own scalar bases the loads need no vector address arithmetic.
+template <bool SPARSE, int LOG_GROUP>
+struct CodeBlock {
+  static constexpr int kGroups = kBlockCols >> LOG_GROUP;
+  u32x4_t codes;
+  u32x2_t scales[kGroups];
+  uint16_t meta[4];
 
-// One workgroup: 16 rows x 16 NT columns of Y; its waves take the blocks of 128 stored columns
-// in turn and add their sums in wave order at the end.
-template <bool BF16, bool SPARSE, int LOG_GROUP, bool ONE, int NT, int WAVES, int YT>
-__global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
-  __shared__ float4_t part[WAVES][NT][64];
-  const int lane = threadIdx.x & 63, n = lane & 15, j = lane >> 4;
-  const int wave = threadIdx.x >> 6;
-  const int64_t g = blockIdx.x, t0 = (int64_t)blockIdx.y * (16 * NT);
-  const uint32_t off = BF16 ? 0xC1C0C1C0u : 0xCE00CE00u;  // -24, -24
-  const u32x4_t offs{off, off, off, off};
-  float4_t total[NT];
+  // Rows of block g, columns of block s.
+  __device__ __forceinline__ void load(const MatvecArgs& a, int64_t g, int s, int lane) {
+    const uint32_t n = lane & 15, j = lane >> 4;
+    codes = *reinterpret_cast<const u32x4_t*>(a.codes + (g * a.S + s) * 1024 + (uint32_t)lane * 16);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) total[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < kGroups; ++i) {
+      const int gi = min(s * kGroups + i, a.groups - 1);
+      scales[i] = *reinterpret_cast<const u32x2_t*>(a.scales + (g * a.groups + gi) * 32 + j * 8);
+    }
+    if constexpr (SPARSE) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int step = min(4 * s + w, a.steps - 1);
+        meta[w] = *reinterpret_cast<const uint16_t*>(a.meta + (g * a.steps + step) * 128 + n * 8 + j * 2);
+      }
+    }
+  }
 
-  for (int s = wave; s < a.S; s += WAVES) {
-    const u32x4_t c = a.codes[(g * a.S + s) * 64 + lane];
+  // total[t] += this block times the B operands operand(w, half, t): for step w 32 rows of X (of
+  // the two halves of 64, for 2:4), 16 columns.
+  template <bool BF16, int NT, typename F>
+  __device__ __forceinline__ void multiply(float4_t (&total)[NT], uint32_t mask, uint32_t sixteen,
+                                           F&& operand) const {
+    constexpr uint32_t off = BF16 ? 0xC1C0C1C0u : 0xCE00CE00u;  // -24, -24
+    const u32x4_t offs{off, off, off, off};
     float4_t acc[NT];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const int step = 4 * s + w;
-      if (step >= a.steps) break;
       if (((32 * w) & ((1 << LOG_GROUP) - 1)) == 0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
       }
-      uint32_t idx = 0;
-      if constexpr (SPARSE)
-        idx = *reinterpret_cast<const uint16_t*>(a.meta + ((g * a.steps + step) * 16 + n) * 8 + 2 * j);
-      const u32x4_t wf = codes_to_float<BF16>(c[w]);
+      const u32x4_t wf = codes_to_float<BF16>(codes[w], mask, sixteen);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        const u32x4_t b0 = operand(w, 0, t);
         if constexpr (SPARSE) {
-          u32x4_t b0, b1;
-          if constexpr (ONE) {
-            b0 = one_column(a, 64 * (int64_t)step + 8 * j);
-            b1 = one_column(a, 64 * (int64_t)step + 32 + 8 * j);
-          } else {
-            const int64_t at = ((t0 / 16 + t) * a.K8 + 8 * (int64_t)step) * 16 + n;
-            b0 = a.x[at + 16 * j];
-            b1 = a.x[at + 16 * (4 + j)];
-          }
-          acc[t] = mfma_sparse<BF16>(wf, b0, b1, acc[t], idx);
-          acc[t] = mfma_sparse<BF16>(offs, b0, b1, acc[t], idx);
+          const u32x4_t b1 = operand(w, 1, t);
+          acc[t] = mfma_sparse<BF16>(wf, b0, b1, acc[t], meta[w]);
+          acc[t] = mfma_sparse<BF16>(offs, b0, b1, acc[t], meta[w]);
         } else {
-          u32x4_t b;
-          if constexpr (ONE) b = one_column(a, 32 * (int64_t)step + 8 * j);
-          else b = a.x[((t0 / 16 + t) * a.K8 + 4 * (int64_t)step + j) * 16 + n];
-          acc[t] = mfma_dense<BF16>(wf, b, acc[t]);
-          acc[t] = mfma_dense<BF16>(offs, b, acc[t]);
+          acc[t] = mfma_dense<BF16>(wf, b0, acc[t]);
+          acc[t] = mfma_dense<BF16>(offs, b0, acc[t]);
         }
       }
-      if (((32 * (w + 1)) & ((1 << LOG_GROUP) - 1)) == 0 || step + 1 == a.steps) {
-        const int gi = (kBlockCols * s + 32 * w) >> LOG_GROUP;
-        const u32x2_t sv = *reinterpret_cast<const u32x2_t*>(a.scales + (g * a.groups + gi) * 16 + 4 * j);
+      if (((32 * (w + 1)) & ((1 << LOG_GROUP) - 1)) == 0) {
+        const u32x2_t sv = scales[(32 * w) >> LOG_GROUP];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -331,50 +329,317 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
       }
     }
   }
+};
+
+// One column.  A workgroup has 16 rows; its waves take the blocks of 128 stored columns in turn,
+// each with the next one's loads in flight, and add their sums in wave order at the end.  X lies
+// in LDS whole; every column of the instruction holds it, and only the first is kept.  Blocks
+// past the matrix's last columns hold code 0 against zeros of X, so there are no ends to treat.
+template <bool BF16, bool SPARSE, int LOG_GROUP, int WAVES, int YT>
+__global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
+  constexpr int kEights = SPARSE ? 8 : 4;  // eights of X's rows to a step
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, j = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t mask = in_register(BF16 ? 0x00780078u : 0x03C003C0u);
+  const uint32_t sixteen = in_register(BF16 ? 0x41804180u : 0x4C004C00u);
+  const int64_t g = blockIdx.x;
+  CodeBlock<SPARSE, LOG_GROUP> next;
+  if (wave < a.S) next.load(a, g, wave, lane);
+  const int chunks = a.S * 4 * kEights;  // X and the zeros after it, to whole blocks
+  for (int c = threadIdx.x; c < chunks; c += 64 * WAVES) {
+    const int64_t k = 8 * (int64_t)c;
+    u32x4_t v;
+    if (k + 8 <= a.K) {
+      v = *reinterpret_cast<const u32x4_t*>(a.x + k);
+    } else {
+      uint32_t h[8];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) part[wave][t][lane] = total[t];
+      for (int e = 0; e < 8; ++e) h[e] = k + e < a.K ? a.x[k + e] : 0u;
+      v = u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+    }
+    reinterpret_cast<u32x4_t*>(smem)[c] = v;
+  }
   __syncthreads();
-  // rows 4 j + i of column n: one output per thread of the first waves
-  for (int e = threadIdx.x; e < NT * 256; e += 64 * WAVES) {
-    const int t = e >> 8, i = (e >> 6) & 3, l = e & 63;
+  float4_t total[1] = {float4_t{0.f, 0.f, 0.f, 0.f}};
+  for (int s = wave; s < a.S; s += WAVES) {
+    const CodeBlock<SPARSE, LOG_GROUP> cur = next;
+    if (s + WAVES < a.S) next.load(a, g, s + WAVES, lane);
+    const u32x4_t* x = reinterpret_cast<const u32x4_t*>(smem) + 4 * s * kEights + j;
+    cur.template multiply<BF16, 1>(total, mask, sixteen, [&](int w, int half, int) {
+      return x[w * kEights + 4 * half];
+    });
+  }
+  __syncthreads();  // X's place in LDS takes the waves' sums
+  float4_t* part = reinterpret_cast<float4_t*>(smem);
+  part[wave * 64 + lane] = total[0];
+  __syncthreads();
+  if (threadIdx.x < 16) {  // rows 4 j + i of column 0
+    const int row = threadIdx.x;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) y += part[w][t][l][i];
-    const int64_t row = 16 * g + 4 * (l >> 4) + i, col = t0 + 16 * t + (l & 15);
-    if (row < a.R && col < a.T) store_from_f32<YT>(a.y, row * a.T + col, y);
+    for (int w = 0; w < WAVES; ++w) y += part[w * 64 + 16 * (row / 4)][row % 4];
+    if (16 * g + row < a.R) store_from_f32<YT>(a.y, 16 * g + row, y);
   }
 }
 
-template <bool BF16, bool SPARSE, int LOG_GROUP, bool ONE, int YT>
-hipError_t launch_matvec_cols(const MatvecArgs& a, hipStream_t s) {
-  constexpr int kWaves = 8;
-  const unsigned rows = (unsigned)((a.R + 15) / 16);
-  if constexpr (ONE) {
-    matvec_kernel<BF16, SPARSE, LOG_GROUP, true, 1, kWaves, YT><<<rows, 64 * kWaves, 0, s>>>(a);
-  } else if (a.T <= 16) {
-    matvec_kernel<BF16, SPARSE, LOG_GROUP, false, 1, kWaves, YT><<<rows, 64 * kWaves, 0, s>>>(a);
+// Several columns.  A workgroup of eight waves has 16 rows for every 2^log_along of them, 16 NT
+// columns and a slice of the stored columns.  X's rows for the slice are laid out in LDS once: 16
+// columns (32 bytes) a row first, then, by one transposing read and one write in place, each 32
+// rows x 16 columns as the B operand that the products read (16 bytes a lane, no bank conflicts).
+// The waves that share rows take the slice's blocks in turn and add their sums in wave order.
+// With more than one slice the sums go to the workspace, where join_slices_kernel adds them in
+// slice order.
+constexpr int kSliceWaves = 8;
+
+template <bool BF16, bool SPARSE, int LOG_GROUP, int NT, int YT>
+__global__ void __launch_bounds__(64 * kSliceWaves) matvec_slice_kernel(MatvecArgs a) {
+  typedef CodeBlock<SPARSE, LOG_GROUP> Block;
+  constexpr int kBlockRows = SPARSE ? 256 : 128;  // rows of X to a block
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, n = lane & 15, j = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int along = 1 << a.log_along, first = wave & (along - 1);
+  const uint32_t mask = in_register(BF16 ? 0x00780078u : 0x03C003C0u);
+  const uint32_t sixteen = in_register(BF16 ? 0x41804180u : 0x4C004C00u);
+  const int64_t last = (a.R + 15) / 16 - 1;
+  const int64_t mine = (int64_t)blockIdx.x * (kSliceWaves >> a.log_along) + (wave >> a.log_along);
+  const int64_t g = mine < last ? mine : last;  // rows past the matrix: dropped below
+  const int t0 = blockIdx.z * (16 * NT), T = (int)a.T, cols = min(T - t0, 16 * NT);
+  const int s0 = blockIdx.y * a.slice, blocks = min(a.slice, a.S - s0);
+
+  Block next;  // loads of the wave's next block; past the last one, of that again
+  if (blocks > 0) next.load(a, g, s0 + min(first, blocks - 1), lane);
+
+  // ---- X ----
+  const int64_t k0 = (int64_t)s0 * kBlockRows;
+  const int rows = blocks * kBlockRows;
+  const int tile_bytes = rows * 32;
+  const int have = (int)(a.K - k0 < rows ? a.K - k0 : rows);  // rows of X in the slice
+  if (T % 8 == 0) {  // rows of X are whole 16-byte pieces
+    constexpr int kBatch = 8;  // loads in flight: a loop of single ones would wait for each
+    for (int c0 = threadIdx.x; c0 < rows * 2 * NT; c0 += kBatch * 64 * kSliceWaves) {
+      u32x4_t v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + i * 64 * kSliceWaves, row = c / (2 * NT), p = c % (2 * NT);
+        v[i] = row < have && 8 * p < cols
+                   ? *reinterpret_cast<const u32x4_t*>(a.x + (k0 + row) * T + t0 + 8 * p)
+                   : u32x4_t{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + i * 64 * kSliceWaves, row = c / (2 * NT), p = c % (2 * NT);
+        if (row < rows)
+          *reinterpret_cast<u32x4_t*>(smem + (p >> 1) * tile_bytes + row * 32 +
+                                      16 * (p & 1)) = v[i];
+      }
+    }
   } else {
-    matvec_kernel<BF16, SPARSE, LOG_GROUP, false, 2, kWaves, YT>
-        <<<dim3(rows, (unsigned)((a.T + 31) / 32)), 64 * kWaves, 0, s>>>(a);
+    for (int c = threadIdx.x; c < rows * 2 * NT; c += 64 * kSliceWaves)
+      reinterpret_cast<u32x4_t*>(smem)[c] = u32x4_t{0, 0, 0, 0};
+    __syncthreads();
+    auto put = [&](int row, int col, uint16_t v) {
+      *reinterpret_cast<uint16_t*>(smem + (col >> 4) * tile_bytes + row * 32 +
+                                   2 * (col & 15)) = v;
+    };
+    if (T <= 16 * NT) {  // X as one run of numbers, eight at a time (k0 T is a multiple of 8)
+      const int numbers = have * T;
+      const uint16_t* x = a.x + k0 * T;
+      for (int e = threadIdx.x * 8; e < numbers; e += 64 * kSliceWaves * 8) {
+        uint32_t h[8];
+        if (e + 8 <= numbers) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = (v[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = e + i < numbers ? x[e + i] : 0u;
+        }
+        int row = e / T, col = e % T;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (e + i < numbers) put(row, col, (uint16_t)h[i]);
+          if (++col == T) {
+            col = 0;
+            ++row;
+          }
+        }
+      }
+    } else {  // columns of a wider X, one number at a time
+      for (int c = threadIdx.x; c < have * 16 * NT; c += 64 * kSliceWaves) {
+        const int row = c / (16 * NT), col = c % (16 * NT);
+        if (col < cols) put(row, col, a.x[(k0 + row) * T + t0 + col]);
+      }
+    }
   }
+  __syncthreads();
+
+  // ---- the slice ----
+  float4_t total[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) total[t] = float4_t{0.f, 0.f, 0.f, 0.f};
+#if defined(__HIP_DEVICE_COMPILE__)
+  for (int c = wave; c < rows / 32 * NT; c += kSliceWaves) {
+    uint8_t* p = smem + c * 1024;
+    const uint32_t off = (8 * j + (n >> 2)) * 32 + 8 * (n & 3);
+    const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(p + off));
+    const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(p + off + 128));
+    *reinterpret_cast<short8_t*>(p + lane * 16) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+#endif
+  __syncthreads();
+#pragma unroll 1  // the loop is entered a few times: unrolled, its code would come from memory anew
+  for (int s = first; s < blocks; s += along) {
+    const Block cur = next;
+    next.load(a, g, s0 + min(s + along, blocks - 1), lane);
+    const uint8_t* x = smem + s * kBlockRows * 32;
+    cur.template multiply<BF16, NT>(total, mask, sixteen, [&](int w, int half, int t) {
+      return *reinterpret_cast<const u32x4_t*>(x + t * tile_bytes +
+                                               (w * (kBlockRows / 128) + half) * 1024 + lane * 16);
+    });
+  }
+
+  if (along > 1) {  // X's place in LDS takes the waves' sums
+    float4_t* part = reinterpret_cast<float4_t*>(smem);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) part[(wave * NT + t) * 64 + lane] = total[t];
+    __syncthreads();
+    if (first != 0) return;
+    for (int w = 1; w < along; ++w)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float4_t v = part[((wave + w) * NT + t) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total[t][i] += v[i];
+      }
+  }
+  if (mine > last) return;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (gridDim.y > 1) {
+      const int64_t tiles = (int64_t)gridDim.z * NT;
+      a.part[((blockIdx.y * (last + 1) + mine) * tiles + blockIdx.z * NT + t) * 64 + lane] = total[t];
+      continue;
+    }
+    const int64_t col = t0 + 16 * t + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = 16 * mine + 4 * j + i;
+      if (row < a.R && col < a.T) store_from_f32<YT>(a.y, row * a.T + col, total[t][i]);
+    }
+  }
+}
+
+// One thread for each four rows of a column; `pieces` of them to a slice.
+template <int YT>
+__global__ void __launch_bounds__(256)
+    join_slices_kernel(const float4_t* __restrict__ part, int slices, int64_t pieces, int64_t tiles,
+                       int64_t R, int64_t T, void* __restrict__ y) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= pieces) return;
+  const int lane = e & 63;
+  const int64_t col = (e >> 6) % tiles * 16 + (lane & 15);
+  const int64_t row = (e >> 6) / tiles * 16 + (lane >> 4) * 4;
+  if (col >= T) return;
+  float4_t total{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < slices; ++s) {
+    const float4_t v = part[s * pieces + e];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (row + i < R) store_from_f32<YT>(y, (row + i) * T + col, total[i]);
+}
+
+constexpr int64_t kColumnLds = 64 << 10;  // most of it that a single column may take
+int64_t column_bytes(int64_t K) { return (K + 255) / 256 * 512; }
+bool one_column(int64_t K, int64_t T) { return T == 1 && column_bytes(K) <= kColumnLds; }
+
+// How several columns are cut.  Each workgroup reads X's rows of its slice, so rows are shared by
+// few waves where that leaves workgroups for all 256 units, and one slice is taken where X fits the
+// LDS; a slice of 64 KB leaves room for a second workgroup on the unit.
+struct MatvecPlan {
+  int nt, log_along, slice, slices;
+  int64_t groups, tiles;  // workgroups along rows, along columns of X
+  int64_t bytes;          // of workspace
+  MatvecPlan(int64_t R, int64_t K, int64_t T, bool sparse) {
+    const int64_t block_rows = sparse ? 256 : 128, S = (K + block_rows - 1) / block_rows;
+    nt = T > 16 ? 2 : 1;
+    tiles = (T + 16 * nt - 1) / (16 * nt);
+    const int64_t block_bytes = block_rows * 32 * nt;
+    const auto groups_of = [&](int log) {
+      const int64_t rows = 16 * (kSliceWaves >> log);
+      return (R + rows - 1) / rows;
+    };
+    if (S * block_bytes <= 128 << 10) {
+      const int64_t most = S * block_bytes <= 64 << 10 ? 512 : 256;
+      slices = 1;
+      log_along = 3;
+      while (log_along > 0 && groups_of(log_along) * tiles > most) --log_along;
+    } else {
+      const int64_t per = (64 << 10) / block_bytes;
+      slices = (int)((S + per - 1) / per);
+      log_along = 0;
+      while (log_along < 3 && groups_of(log_along) * tiles * slices < 256) ++log_along;
+    }
+    slice = (int)std::max<int64_t>(1, (S + slices - 1) / slices);
+    slices = (int)std::max<int64_t>(1, (S + slice - 1) / slice);
+    groups = groups_of(log_along);
+    bytes = slices > 1 ? slices * ((R + 15) / 16) * tiles * nt * 1024 : 0;
+  }
+};
+
+template <bool BF16, bool SPARSE, int LOG_GROUP, int NT, int YT>
+hipError_t launch_matvec_slices(const MatvecArgs& a, const MatvecPlan& p, hipStream_t s) {
+  auto kernel = matvec_slice_kernel<BF16, SPARSE, LOG_GROUP, NT, YT>;
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 128 << 10);
+  if (attr != hipSuccess) return attr;
+  const size_t lds = std::max((size_t)p.slice * (SPARSE ? 8192 : 4096) * NT,
+                              (size_t)kSliceWaves * NT * 1024);
+  kernel<<<dim3((unsigned)p.groups, (unsigned)p.slices, (unsigned)p.tiles), 64 * kSliceWaves, lds,
+           s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.slices == 1) return e;
+  const int64_t tiles = p.tiles * NT, pieces = (a.R + 15) / 16 * tiles * 64;
+  join_slices_kernel<YT><<<(unsigned)((pieces + 255) / 256), 256, 0, s>>>(a.part, p.slices, pieces,
+                                                                        tiles, a.R, a.T, a.y);
   return hipGetLastError();
 }
 
+template <bool BF16, bool SPARSE, int LOG_GROUP, int YT>
+hipError_t launch_matvec_cols(const MatvecArgs& a, const MatvecPlan& p, hipStream_t s) {
+  if (one_column(a.K, a.T)) {
+    // eight waves to 16 rows fill the device where rows are many, sixteen where they are few
+    const size_t lds = std::max((size_t)column_bytes(a.K), (size_t)16 * 1024);
+    const unsigned groups = (unsigned)((a.R + 15) / 16);
+    if (groups > 256)
+      matvec_kernel<BF16, SPARSE, LOG_GROUP, 8, YT><<<groups, 512, lds, s>>>(a);
+    else
+      matvec_kernel<BF16, SPARSE, LOG_GROUP, 16, YT><<<groups, 1024, lds, s>>>(a);
+    return hipGetLastError();
+  }
+  return p.nt == 1 ? launch_matvec_slices<BF16, SPARSE, LOG_GROUP, 1, YT>(a, p, s)
+                   : launch_matvec_slices<BF16, SPARSE, LOG_GROUP, 2, YT>(a, p, s);
+}
+
 template <bool BF16, bool SPARSE, int LOG_GROUP>
-hipError_t launch_matvec_y(const MatvecArgs& a, int y_dt, hipStream_t s) {
+hipError_t launch_matvec_y(const MatvecArgs& a, const MatvecPlan& p, int y_dt, hipStream_t s) {
   constexpr int kSame = BF16 ? kBF16 : kF16;
-  if (a.T == 1)
-    return y_dt == kF32 ? launch_matvec_cols<BF16, SPARSE, LOG_GROUP, true, kF32>(a, s)
-                        : launch_matvec_cols<BF16, SPARSE, LOG_GROUP, true, kSame>(a, s);
-  return y_dt == kF32 ? launch_matvec_cols<BF16, SPARSE, LOG_GROUP, false, kF32>(a, s)
-                      : launch_matvec_cols<BF16, SPARSE, LOG_GROUP, false, kSame>(a, s);
+  return y_dt == kF32 ? launch_matvec_cols<BF16, SPARSE, LOG_GROUP, kF32>(a, p, s)
+                      : launch_matvec_cols<BF16, SPARSE, LOG_GROUP, kSame>(a, p, s);
 }
 
 template <bool BF16, bool SPARSE>
-hipError_t launch_matvec_group(const MatvecArgs& a, int log_group, int y_dt, hipStream_t s) {
-  if (log_group == 5) return launch_matvec_y<BF16, SPARSE, 5>(a, y_dt, s);
-  if (log_group == 6) return launch_matvec_y<BF16, SPARSE, 6>(a, y_dt, s);
-  return launch_matvec_y<BF16, SPARSE, 7>(a, y_dt, s);
+hipError_t launch_matvec_group(const MatvecArgs& a, const MatvecPlan& p, int log_group, int y_dt,
+                               hipStream_t s) {
+  if (log_group == 5) return launch_matvec_y<BF16, SPARSE, 5>(a, p, y_dt, s);
+  if (log_group == 6) return launch_matvec_y<BF16, SPARSE, 6>(a, p, y_dt, s);
+  return launch_matvec_y<BF16, SPARSE, 7>(a, p, y_dt, s);
 }
 
 int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
@@ -432,44 +697,36 @@ hipError_t launch_dequantize(const void* codes, const void* scales, int scale_dt
   return hipGetLastError();
 }
 
-size_t matvec_workspace_bytes(int64_t K, int64_t T) {
-  if (T <= 1) return 0;
-  return (size_t)((K + kBlockCols - 1) / kBlockCols * 16) * (size_t)((T + 31) / 32 * 2) * 256;
+size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse) {
+  return one_column(K, T) ? 0 : (size_t)MatvecPlan(R, K, T, sparse).bytes;
 }
 
 hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
                          int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
                          void* workspace, hipStream_t s) {
   const int64_t C = meta ? K / 2 : K;
+  const MatvecPlan p(R, K, T, meta != nullptr);
   MatvecArgs a;
-  a.codes = static_cast<const u32x4_t*>(codes);
-  a.scales = static_cast<const uint16_t*>(scales);
+  a.codes = static_cast<const uint8_t*>(codes);
+  a.scales = static_cast<const uint8_t*>(scales);
   a.meta = static_cast<const uint8_t*>(meta);
+  a.x = static_cast<const uint16_t*>(X);
   a.y = Y;
   a.R = R;
   a.T = T;
   a.K = K;
-  a.K8 = (K + kBlockCols - 1) / kBlockCols * 16;
   a.S = (int)((C + kBlockCols - 1) / kBlockCols);
   a.steps = (int)((C + 31) / 32);
   a.groups = (int)((C + group - 1) / group);
-  if (T == 1) {
-    a.x = static_cast<const u32x4_t*>(X);
-  } else {
-    u32x4_t* x = static_cast<u32x4_t*>(workspace);
-    const int64_t total = a.K8 * ((T + 31) / 32 * 2) * 16;
-    columns_kernel<<<stride_grid(total, 256), 256, 0, s>>>(static_cast<const uint16_t*>(X), K, T,
-                                                           a.K8, total, x);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    a.x = x;
-  }
+  a.slice = p.slice;
+  a.log_along = p.log_along;
+  a.part = static_cast<float4_t*>(workspace);
   const int lg = log2_of(group);
   if (dt == kBF16)
-    return meta ? launch_matvec_group<true, true>(a, lg, y_dt, s)
-                : launch_matvec_group<true, false>(a, lg, y_dt, s);
-  return meta ? launch_matvec_group<false, true>(a, lg, y_dt, s)
-              : launch_matvec_group<false, false>(a, lg, y_dt, s);
+    return meta ? launch_matvec_group<true, true>(a, p, lg, y_dt, s)
+                : launch_matvec_group<true, false>(a, p, lg, y_dt, s);
+  return meta ? launch_matvec_group<false, true>(a, p, lg, y_dt, s)
+              : launch_matvec_group<false, false>(a, p, lg, y_dt, s);
 }
 
 }  // namespace nm
