@@ -9,14 +9,20 @@
 // and the epilogue drops them.  A strided operand's rows are whole 16-byte pieces (ld and the
 // width are multiples of 8).
 //
-// A step of 64 k of both operands is brought into LDS by direct loads, one step ahead of the
-// step that is being multiplied (two stages).  A wave owns 32 FM x 32 FN of the tile and uses
-// v_mfma_f32_32x32x16.  LDS layouts of a stage, both free of bank conflicts for their reads:
+// Steps of 64 k of both operands are brought into LDS by direct loads, up to STAGES steps ahead of
+// the step that is being multiplied: two stages for the large tiles, whose step is long, and
+// as many as fit for the small ones, whose whole sum may then be in flight at once.  A wave owns
+// 32 FM x 32 FN of the tile and uses v_mfma_f32_32x32x16.  LDS layouts of a stage, both free of
+// bank conflicts for their reads:
 //   k contiguous: 128 bytes a row of the tile, 16-byte chunk c at c ^ (row & 7); a fragment is
 //     one 16-byte read per lane;
 //   strided: a row of the tile's columns for each k, 32-byte pair p at p ^ 2 (k & 3); a
 //     fragment is two transposing reads (ds_read_b64_tr_b16).
+// PARTS = 2: each operand is a sum hi + lo of two 16-bit matrices, and hi hi + hi lo + lo hi is
+// summed; the four tiles are loaded once a step.
 #pragma once
+
+#include <type_traits>
 
 #include "nm_launch.h"
 #include "nm_mfma.h"
@@ -32,14 +38,24 @@ struct GemmOperand {
   const uint16_t* p;
   int64_t ld;
   int64_t rows;
+  int64_t lo;  // elements from p to the lo part, where there is one
 };
 
 // Workgroups are dealt to the XCDs in turn; each XCD takes a contiguous run of tiles, walked
 // in blocks of gm x gn so that the tiles it works on at once share rows of A and B in its L2.
 struct GemmMap {
   int tiles_m, tiles_n, xcds, per_xcd, gm, gn;
+  bool lower;  // only the tiles of a square result with tm >= tn
   __device__ __forceinline__ bool tile_of(int b, int& tm, int& tn) const {
     const int t = (b % xcds) * per_xcd + b / xcds;
+    if (lower) {
+      if (t >= tiles_m * (tiles_m + 1) / 2) return false;
+      tm = (int)((sqrtf(8.f * t + 1.f) - 1.f) * 0.5f);  // within one of the row that holds t
+      if (tm * (tm + 1) / 2 > t) --tm;
+      if ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
+      tn = t - tm * (tm + 1) / 2;
+      return true;
+    }
     if (t >= tiles_m * tiles_n) return false;
     const int g_m = t / (gm * tiles_n);
     const int rows = min(gm, tiles_m - g_m * gm);
@@ -53,12 +69,14 @@ struct GemmMap {
   int groups() const { return per_xcd * xcds; }
 };
 
-inline GemmMap make_gemm_map(int64_t tiles_m, int64_t tiles_n) {
+inline GemmMap make_gemm_map(int64_t tiles_m, int64_t tiles_n, bool lower = false) {
   GemmMap map;
   map.tiles_m = (int)tiles_m;
   map.tiles_n = (int)tiles_n;
+  map.lower = lower;
   map.xcds = xcd_count();
-  map.per_xcd = (int)((tiles_m * tiles_n + map.xcds - 1) / map.xcds);
+  const int64_t tiles = lower ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
+  map.per_xcd = (int)((tiles + map.xcds - 1) / map.xcds);
   map.gn = tiles_n < 4 ? (int)tiles_n : 4;
   map.gm = 32 / map.gn;
   return map;
@@ -66,15 +84,19 @@ inline GemmMap make_gemm_map(int64_t tiles_m, int64_t tiles_n) {
 
 // WM x WN waves of 32 FM rows x 32 FN columns each; AS / BS: operand stored strided;
 // SWAP: accumulators hold C transposed within a fragment (lane = row, registers = columns).
-template <int WM, int WN, int FM, int FN, bool AS, bool BS, bool BF16, bool SWAP>
+template <int WM, int WN, int FM, int FN, bool AS, bool BS, bool BF16, bool SWAP, int STAGES = 2,
+          int PARTS = 1>
 struct Gemm {
+  static constexpr int kFM = FM, kFN = FN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kBM = 32 * FM * WM, kBN = 32 * FN * WN;
   static constexpr int kABytes = kBM * 2 * kGemmStep, kBBytes = kBN * 2 * kGemmStep;
-  static constexpr int kStage = kABytes + kBBytes, kLds = 2 * kStage;
+  static constexpr int kStage = PARTS * (kABytes + kBBytes), kLds = STAGES * kStage;
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  static constexpr int kLoads = PARTS * (kALoads + kBLoads);  // of a wave and step
   static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "whole loads");
   static_assert(kLds <= 160 * 1024, "LDS");
+  static_assert(STAGES >= 2 && (STAGES - 1) * kLoads <= 63, "vmcnt");
 
   typedef float16v_t Acc[FM][FN];
 
@@ -137,14 +159,11 @@ struct Gemm {
                                                     __builtin_bit_cast(f16x8_t, y), c, 0, 0, 0);
   }
 
-  // acc += the tile at (m0, n0) over `steps` steps of each of `segments` pairs of operands.
-  // Three segments are the pairs (a, b), (a, b + b_lo), (a + a_lo, b), offsets in elements.
-  // klen: rows of a strided A (past them its last step reads the last one again, against zeros
-  // of B); B always has whole steps.
+  // acc += the tile at (m0, n0) over `steps` steps.  klen: rows of a strided A (past them its last
+  // step reads the last one again, against zeros of B); B always has whole steps.
   static __device__ __forceinline__ void run(const GemmOperand& a, const GemmOperand& b,
                                              int64_t m0, int64_t n0, int steps, int64_t klen,
-                                             uint8_t* smem, Acc& acc, int segments = 1,
-                                             int64_t a_lo = 0, int64_t b_lo = 0) {
+                                             uint8_t* smem, Acc& acc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -162,49 +181,99 @@ struct Gemm {
     for (int j = 0; j < kBLoads; ++j)
       bv[j] = source<BS, kBN>(j, wave, lane, b.ld, b_left, kGemmStep);
     const uint32_t lds0 = lds_addr(smem);
-    const int total = steps * segments;
 
-    auto issue = [&](int s) {
-      const int seg = segments == 1 ? 0 : s / steps, t = segments == 1 ? s : s % steps;
-      // segments: (hi, hi), (hi, lo), (lo, hi)
-      const uint16_t* pa = a0 + t * a_step + (seg == 2 ? a_lo : 0);
-      const uint16_t* pb = b0 + t * b_step + (seg == 1 ? b_lo : 0);
-      const uint32_t st = lds0 + (s & 1) * kStage;
+    auto issue = [&](int t, int stage) {
+      const uint16_t* pa = a0 + t * a_step;
+      const uint16_t* pb = b0 + t * b_step;
+      const uint32_t st = lds0 + stage * kStage + wave * 1024;
       if (ragged && t == steps - 1) {  // A's rows end inside this step
         const int64_t kleft = klen - (int64_t)t * kGemmStep;
 #pragma unroll
         for (int j = 0; j < kALoads; ++j)
           global_to_lds_sv<16>(pa, source<AS, kBM>(j, wave, lane, a.ld, a_left, kleft),
-                               st + (j * kWaves + wave) * 1024);
+                               st + j * kWaves * 1024);
       } else {
 #pragma unroll
-        for (int j = 0; j < kALoads; ++j)
-          global_to_lds_sv<16>(pa, av[j], st + (j * kWaves + wave) * 1024);
+        for (int j = 0; j < kALoads; ++j) global_to_lds_sv<16>(pa, av[j], st + j * kWaves * 1024);
       }
 #pragma unroll
       for (int j = 0; j < kBLoads; ++j)
-        global_to_lds_sv<16>(pb, bv[j], st + kABytes + (j * kWaves + wave) * 1024);
+        global_to_lds_sv<16>(pb, bv[j], st + PARTS * kABytes + j * kWaves * 1024);
+      if constexpr (PARTS == 2) {
+#pragma unroll
+        for (int j = 0; j < kALoads; ++j)
+          global_to_lds_sv<16>(pa + a.lo, av[j], st + kABytes + j * kWaves * 1024);
+#pragma unroll
+        for (int j = 0; j < kBLoads; ++j)
+          global_to_lds_sv<16>(pb + b.lo, bv[j], st + 2 * kABytes + kBBytes + j * kWaves * 1024);
+      }
     };
 
-    if (total > 0) issue(0);
-    for (int s = 0; s < total; ++s) {
-      // step s has landed for every wave, and no wave reads the other stage any more
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (s + 1 < total) issue(s + 1);
-      const uint8_t* ta = smem + (s & 1) * kStage;
-      const uint8_t* tb = ta + kABytes;
+    struct Fragments {
+      u32x4_t a[PARTS][FM], b[PARTS][FN];
+    };
+    auto read = [&](Fragments& f, int stage, int kk) {
+      const uint8_t* ta = smem + stage * kStage;
+      const uint8_t* tb = ta + PARTS * kABytes;
 #pragma unroll
-      for (int kk = 0; kk < kGemmStep / 16; ++kk) {
-        u32x4_t fa[FM], fb[FN];
-#pragma unroll
-        for (int f = 0; f < FM; ++f) fa[f] = fragment<AS, kBM>(ta, wm * 32 * FM, f, kk, lane);
-#pragma unroll
-        for (int f = 0; f < FN; ++f) fb[f] = fragment<BS, kBN>(tb, wn * 32 * FN, f, kk, lane);
+      for (int q = 0; q < PARTS; ++q) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
+          f.a[q][i] = fragment<AS, kBM>(ta + q * kABytes, wm * 32 * FM, i, kk, lane);
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < FN; ++j)
+          f.b[q][j] = fragment<BS, kBN>(tb + q * kBBytes, wn * 32 * FN, j, kk, lane);
       }
+    };
+    auto multiply = [&](const Fragments& f) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          acc[i][j] = mfma(f.a[0][i], f.b[0][j], acc[i][j]);
+          if constexpr (PARTS == 2) {
+            acc[i][j] = mfma(f.a[0][i], f.b[1][j], acc[i][j]);
+            acc[i][j] = mfma(f.a[1][i], f.b[0][j], acc[i][j]);
+          }
+        }
+    };
+    // Waits until all but the last `keep` steps' loads have landed (all of them where fewer steps
+    // follow) and this wave's reads are done, then meets the other waves.
+    auto meet = [&](auto keep, bool full) {
+      if (full)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(keep)::value * kLoads)
+                     : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    if (steps <= 0) return;
+#pragma unroll
+    for (int t = 0; t < STAGES; ++t)
+      if (t < steps) issue(t, t);
+    meet(std::integral_constant<int, STAGES - 1>{}, steps >= STAGES);
+    Fragments f[2];
+    read(f[0], 0, 0);
+    int stage = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int next = stage + 1 == STAGES ? 0 : stage + 1;
+      // the next 16 k's fragments are read while the matrix cores work on these
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk) {
+        read(f[(kk + 1) & 1], stage, kk + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f[kk & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (s + 1 < steps) {
+        // step s + 1 has landed; no wave reads this step's stage any more
+        meet(std::integral_constant<int, STAGES - 2>{}, s + STAGES <= steps);
+        if (s + STAGES < steps) issue(s + STAGES, stage);
+        read(f[0], next, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      multiply(f[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      stage = next;
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // smem may be reused
   }
@@ -226,23 +295,18 @@ struct Gemm {
       for (int j = 0; j < FN; ++j) acc[i][j] = float16v_t{};
   }
 
-  // Calls f(row, col, v) for every four consecutive columns (SWAP) that the calling lane holds;
-  // row and col are of the whole matrix, v the four values.
-  template <typename F>
-  static __device__ __forceinline__ void each4(const Acc& acc, int64_t m0, int64_t n0, F&& f) {
+  // With SWAP a lane holds, for each i < FM, j < FN and g < 4, four consecutive columns of a row:
+  // quad(acc, i, j, g) at row row0(m0) + 32 i, columns col0(n0) + 32 j + 8 g .. + 3.
+  static __device__ __forceinline__ int64_t row0(int64_t m0) {
+    return m0 + ((threadIdx.x >> 6) / WN) * 32 * FM + (threadIdx.x & 31);
+  }
+  static __device__ __forceinline__ int64_t col0(int64_t n0) {
+    return n0 + ((threadIdx.x >> 6) % WN) * 32 * FN + 4 * ((threadIdx.x >> 5) & 1);
+  }
+  static __device__ __forceinline__ float4_t quad(const Acc& acc, int i, int j, int g) {
     static_assert(SWAP, "rows by lane");
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row0 = m0 + (wave / WN) * 32 * FM + (lane & 31);
-    const int64_t col0 = n0 + (wave % WN) * 32 * FN + 4 * (lane >> 5);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          f(row0 + 32 * i, col0 + 32 * j + 8 * g,
-            float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
-                     acc[i][j][4 * g + 3]});
+    return float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                    acc[i][j][4 * g + 3]};
   }
 };
 

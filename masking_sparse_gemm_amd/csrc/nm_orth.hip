@@ -10,10 +10,12 @@
 // the result.  All three are held times 2^8, which keeps entries of 2^-22 in fp16's normal
 // range.  G itself is only scaled by a power of two (exact for bf16); the rest of its norm, a
 // factor rho in fp32, goes into the first step's epilogues.
-//   bf16 G: operands are one fp16, and the X that a X is formed from is carried in fp32.
+//   bf16 G: operands are one fp16, and the X that a X is formed from has the next four bits
+//     beside it (one fp8 an entry): without them the small singular values lose most.
 //   fp16 and fp32 G: each operand is two fp16, hi + lo (22 bits), and a product is hi hi +
 //     hi lo + lo hi in the same accumulators, as exact as fp32 products.
 // The norm is summed in fp64, so no finite G overflows or vanishes in it.
+#include <algorithm>
 #include <cmath>
 
 #include "nm_gemm.h"
@@ -21,7 +23,7 @@
 namespace nm {
 namespace {
 
-constexpr int kNormBlocks = 512;
+constexpr int kNormBlocks = 1024;
 constexpr float kOrthScale = 256.f;
 
 struct OrthHead {  // first bytes of the workspace
@@ -36,13 +38,30 @@ __device__ __forceinline__ float load_f32(const void* p, int64_t i) {
   else return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
+// Sums of squares in fp64 (exact squares of 16-bit numbers; the accumulation costs nothing beside
+// the reads), 16 bytes a lane at a time.
 template <int DT>
 __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, int64_t n,
                                                    OrthHead* head) {
+  constexpr int kPer = DT == kF32 ? 4 : 8;
   __shared__ double part[4];
   double sum = 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)kNormBlocks * 256) {
-    const double x = load_f32<DT>(G, i);
+  const int64_t whole = n / kPer, stride = (int64_t)gridDim.x * 256;
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+#pragma unroll 4
+  for (int64_t i = first; i < whole; i += stride) {
+    const u32x4_t v = static_cast<const u32x4_t*>(G)[i];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      double x;
+      if constexpr (DT == kF32) x = __uint_as_float(v[e]);
+      else if constexpr (DT == kF16) x = f16_to_f32((v[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
+      else x = bf16_to_f32((v[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
+      sum += x * x;
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x < n - whole * kPer) {
+    const double x = load_f32<DT>(G, whole * kPer + threadIdx.x);
     sum += x * x;
   }
 #pragma unroll
@@ -50,6 +69,9 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
   __syncthreads();
   if (threadIdx.x == 0) head->partial[blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+  // one block may stand for several places that start_kernel adds
+  for (int i = gridDim.x + blockIdx.x; threadIdx.x == 0 && i < kNormBlocks; i += gridDim.x)
+    head->partial[i] = 0;
 }
 
 // X' = G 2^k (rp x kp, zeros past R x K) with 2^k |G|_F in (2^7, 2^8].
@@ -58,7 +80,9 @@ __global__ void __launch_bounds__(256)
     start_kernel(const void* __restrict__ G, int64_t R, int64_t K, int64_t rp, int64_t kp, float eps,
                  OrthHead* head, _Float16* __restrict__ hi, _Float16* __restrict__ lo) {
   __shared__ double part[4];
-  double sum = head->partial[threadIdx.x] + head->partial[threadIdx.x + 256];
+  double sum = 0;
+#pragma unroll
+  for (int i = 0; i < kNormBlocks; i += 256) sum += head->partial[threadIdx.x + i];
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
@@ -89,16 +113,15 @@ enum OrthKind { kGram, kSquare, kUpdate };
 
 struct OrthArgs {
   GemmOperand a, b;
-  int64_t a_lo, b_lo;  // element offset from an operand's hi part to its lo part
-  int steps, segments;
+  int steps;
   GemmMap map;
   int64_t rows, cols;  // of the result, whole multiples of 64; its rows are `cols` apart
   float ca, cb, cc;
   const float* rho;            // the first step's factor, else null
   const _Float16 *from_hi, *from_lo;  // square: A; update: the X before
-  const float* from;           // update: the X before in fp32, or null
   _Float16 *hi, *lo;           // result (lo only with two parts)
-  float* keep;                 // update: the X after in fp32, or null
+  uint32_t* rest;              // one part: what hi lacks of X, four fp8 numbers a word
+  bool from_rest;              // whether the X before has any
   void* out;                   // the last update: the caller's result (R x K), else null
   int out_dt;
   int64_t R, K;
@@ -110,60 +133,100 @@ __device__ __forceinline__ float4_t widen(half4_t h) {
   return float4_t{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
 }
 
+// What fp16 lacks of a number, as fp8 (E4M3) times 2^10: at most 2^7 there, and seen down to 2^-19
+// of the scaled X, whose entries are around 1.
+constexpr float kRestScale = 1024.f;
+__device__ __forceinline__ uint32_t pack_rest(float4_t r) {
+  int w = 0;
+#if defined(__HIP_DEVICE_COMPILE__)
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(r[0] * kRestScale, r[1] * kRestScale, w, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(r[2] * kRestScale, r[3] * kRestScale, w, true);
+#endif
+  return (uint32_t)w;
+}
+__device__ __forceinline__ float4_t unpack_rest(uint32_t w) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const float2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  return float4_t{a[0], a[1], b[0], b[1]} * (1.f / kRestScale);
+#else
+  return float4_t{};
+#endif
+}
+
+// What the epilogue reads of A (square) or of the X before (update) at four columns of a row.
+template <bool SPLIT>
+struct OrthBefore {
+  half4_t hi;
+  half4_t lo;     // two parts
+  uint32_t rest;  // one part
+
+  template <int KIND>
+  __device__ __forceinline__ void load(const OrthArgs& p, int64_t row, int64_t col) {
+    if (row >= p.rows || col >= p.cols) return;
+    const int64_t at = row * p.cols + col;
+    hi = *reinterpret_cast<const half4_t*>(p.from_hi + at);
+    if constexpr (SPLIT) lo = *reinterpret_cast<const half4_t*>(p.from_lo + at);
+    else if (KIND == kUpdate && p.from_rest) rest = p.rest[at / 4];
+  }
+  template <int KIND>
+  __device__ __forceinline__ float4_t value(const OrthArgs& p) const {
+    const float4_t x = widen(hi);
+    if constexpr (SPLIT) return x + widen(lo);
+    return KIND == kUpdate && p.from_rest ? x + unpack_rest(rest) : x;
+  }
+};
+
 template <int KIND, bool SPLIT>
-__device__ __forceinline__ void orth_store(const OrthArgs& p, float rho, int64_t row, int64_t col,
-                                           float4_t v) {
+__device__ __forceinline__ void orth_store(const OrthArgs& p, float rho, bool mirror, int64_t row,
+                                           int64_t col, float4_t v, const OrthBefore<SPLIT>& before) {
   if (row >= p.rows || col >= p.cols) return;
   const int64_t at = row * p.cols + col;
   float4_t r;
   if constexpr (KIND == kGram) {
-    const float f = rho * rho / kOrthScale;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = v[i] * f;
+    r = v * (rho * rho / kOrthScale);
   } else {
-    float4_t x;
-    if (KIND == kUpdate && !SPLIT && p.from) {
-      x = *reinterpret_cast<const float4_t*>(p.from + at);
-    } else {
-      x = widen(*reinterpret_cast<const half4_t*>(p.from_hi + at));
-      if constexpr (SPLIT) {
-        const float4_t l = widen(*reinterpret_cast<const half4_t*>(p.from_lo + at));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] += l[i];
-      }
-    }
-    if constexpr (KIND == kSquare) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = p.cb * x[i] + (p.cc / kOrthScale) * v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = rho * (p.ca * x[i] + v[i] * (1.f / kOrthScale));
-    }
+    const float4_t x = before.template value<KIND>(p);
+    if constexpr (KIND == kSquare) r = p.cb * x + (p.cc / kOrthScale) * v;
+    else r = rho * (p.ca * x + (1.f / kOrthScale) * v);
   }
   if (KIND == kUpdate && p.out) {
     if (row >= p.R) return;
+    const int64_t o = row * p.K + col;
+    r *= 1.f / kOrthScale;
+    if (p.out_dt != kF32 && p.K % 4 == 0) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = p.out_dt == kF16 ? f32_to_f16(r[i]) : f32_to_bf16(r[i]);
+      if (col < p.K)
+        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.out) + o) =
+            u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (col + i >= p.K) continue;
-      const float y = r[i] * (1.f / kOrthScale);
-      const int64_t o = row * p.K + col + i;
-      if (p.out_dt == kF32) store_from_f32<kF32>(p.out, o, y);
-      else if (p.out_dt == kF16) store_from_f32<kF16>(p.out, o, y);
-      else store_from_f32<kBF16>(p.out, o, y);
+      if (p.out_dt == kF32) store_from_f32<kF32>(p.out, o + i, r[i]);
+      else if (p.out_dt == kF16) store_from_f32<kF16>(p.out, o + i, r[i]);
+      else store_from_f32<kBF16>(p.out, o + i, r[i]);
     }
     return;
   }
-  half4_t h;
+  half4_t h, l;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = (_Float16)r[i];
+  for (int i = 0; i < 4; ++i) {
+    h[i] = (_Float16)r[i];
+    l[i] = (_Float16)(r[i] - (float)h[i]);
+  }
   *reinterpret_cast<half4_t*>(p.hi + at) = h;
-  if constexpr (SPLIT) {
-    half4_t l;
+  if constexpr (SPLIT) *reinterpret_cast<half4_t*>(p.lo + at) = l;
+  else if (KIND == kUpdate) p.rest[at / 4] = pack_rest(r - widen(h));
+  if (KIND != kUpdate && mirror) {  // the same numbers above the diagonal, 32 lanes a row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) l[i] = (_Float16)(r[i] - (float)h[i]);
-    *reinterpret_cast<half4_t*>(p.lo + at) = l;
-  } else if (KIND == kUpdate) {
-    *reinterpret_cast<float4_t*>(p.keep + at) = r;
+    for (int i = 0; i < 4; ++i) {
+      p.hi[(col + i) * p.cols + row] = h[i];
+      if constexpr (SPLIT) p.lo[(col + i) * p.cols + row] = l[i];
+    }
   }
 }
 
@@ -173,29 +236,89 @@ __global__ void __launch_bounds__(G::kThreads) orth_kernel(OrthArgs p) {
   int tm, tn;
   if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
+  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
+  const float rho = p.rho ? *p.rho : 1.f;
+  constexpr int kQuads = 4 * G::kFN;  // of a row of fragments
+  OrthBefore<SPLIT> before[kQuads];
+  auto load_row = [&](int i) {
+    if constexpr (KIND != kGram) {
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q)
+        before[q].template load<KIND>(p, row0 + 32 * i, col0 + 32 * (q / 4) + 8 * (q % 4));
+    }
+  };
+  // A small tile's epilogue reads come ahead of its few steps, a large one's a row of fragments
+  // at a time: one by one, between stores that might alias, each would be waited for.
+  constexpr bool kEarly = G::kFM == 1;
+  if constexpr (kEarly) load_row(0);
   typename G::Acc acc;
   G::clear(acc);
-  G::run(p.a, p.b, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc, p.segments, p.a_lo,
-         p.b_lo);
-  const float rho = p.rho ? *p.rho : 1.f;
-  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t v) {
-    orth_store<KIND, SPLIT>(p, rho, row, col, v);
-  });
+  G::run(p.a, p.b, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+#pragma unroll
+  for (int i = 0; i < G::kFM; ++i) {
+    if constexpr (!kEarly) load_row(i);
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+      orth_store<KIND, SPLIT>(p, rho, tm != tn, row0 + 32 * i, col0 + 32 * (q / 4) + 8 * (q % 4),
+                              G::quad(acc, i, q / 4, q % 4), before[q]);
+  }
+}
+
+// Square tiles of four sizes; a launch takes the one with the smallest estimated time: rounds of
+// tiles over the 256 units, times the steps of 64 k at the time a step takes on a full device, plus
+// a fixed time (fill of the pipeline, epilogue).  Large tiles read less per product, small ones
+// fill the device; symmetric results have only the tiles on and below the diagonal, whose number is
+// what matters: 4096 x 4096 in 256s is 136 tiles for 256 units, in 192s 253.  Measured (us for
+// five steps, symmetric products in 256 / 192 / 128 / 64, the rest alike): 4096 x 11008 4606 /
+// 4387 / 5300 / 6125, 2048 x 8192 1850 / 1574 / 1215 / 1402, 1024 x 4096 806 / 668 / 450 / 282.
+struct OrthTile {
+  int size;
+  float step_us, fixed_us;
+};
+constexpr OrthTile kOrthTiles[] = {{256, 1.85f, 11.f}, {192, 1.15f, 8.f}, {128, 0.5f, 4.5f}, {64, 0.25f, 3.5f}};
+constexpr OrthTile kOrthSplitTiles[] = {{128, 1.1f, 5.f}, {64, 0.45f, 4.f}};
+
+template <int N>
+int pick_orth_tile(const OrthTile (&tiles)[N], int64_t rows, int64_t cols, int steps, bool lower) {
+  int best = tiles[0].size;
+  double least = 1e30;
+  for (const OrthTile& t : tiles) {
+    const int64_t m = (rows + t.size - 1) / t.size, n = (cols + t.size - 1) / t.size;
+    const int64_t count = lower ? m * (m + 1) / 2 : m * n;
+    const double us = (double)((count + 255) / 256) * (steps * (double)t.step_us + t.fixed_us);
+    if (us < least) {
+      least = us;
+      best = t.size;
+    }
+  }
+  return best;
 }
 
 template <class G, int KIND, bool SPLIT>
 hipError_t launch_orth_tile(OrthArgs p, hipStream_t s) {
-  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.cols + G::kBN - 1) / G::kBN);
+  // A and B are symmetric: their tiles above the diagonal are written by those below it
+  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.cols + G::kBN - 1) / G::kBN, KIND != kUpdate);
   return G::template launch<orth_kernel<G, KIND, SPLIT>>(p, p.map, 1, s);
 }
 
 template <int KIND, bool AS, bool BS, bool SPLIT>
 hipError_t launch_orth_product(const OrthArgs& p, hipStream_t s) {
-  const int64_t big = ((p.rows + 255) / 256) * ((p.cols + 255) / 256);
-  const int64_t mid = ((p.rows + 127) / 128) * ((p.cols + 127) / 128);
-  if (big >= 128) return launch_orth_tile<Gemm<2, 4, 4, 2, AS, BS, false, true>, KIND, SPLIT>(p, s);
-  if (mid >= 128) return launch_orth_tile<Gemm<2, 2, 2, 2, AS, BS, false, true>, KIND, SPLIT>(p, s);
-  return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true>, KIND, SPLIT>(p, s);
+  constexpr bool kLower = KIND != kUpdate;
+  if constexpr (SPLIT) {
+    const int tile = pick_orth_tile(kOrthSplitTiles, p.rows, p.cols, p.steps, kLower);
+    if (tile == 128)
+      return launch_orth_tile<Gemm<2, 4, 2, 1, AS, BS, false, true, 2, 2>, KIND, true>(p, s);
+    return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 4, 2>, KIND, true>(p, s);
+  } else {
+    const int tile = pick_orth_tile(kOrthTiles, p.rows, p.cols, p.steps, kLower);
+    if (tile == 256)
+      return launch_orth_tile<Gemm<2, 4, 4, 2, AS, BS, false, true, 2>, KIND, false>(p, s);
+    if (tile == 192)
+      return launch_orth_tile<Gemm<2, 2, 3, 3, AS, BS, false, true, 3>, KIND, false>(p, s);
+    if (tile == 128)
+      return launch_orth_tile<Gemm<2, 4, 2, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
+    return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 8>, KIND, false>(p, s);
+  }
 }
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
@@ -205,7 +328,7 @@ struct OrthLayout {
   int64_t rp, kp, mp;  // padded sizes; mp: the shorter side
   bool tall, split;
   int64_t x_part, a_part;       // elements of one fp16 part
-  int64_t head, x, keep, a, b, total;
+  int64_t head, x, rest, a, b, total;
   OrthLayout(int64_t R, int64_t K, int dt) {
     rp = pad64(R);
     kp = pad64(K);
@@ -217,8 +340,8 @@ struct OrthLayout {
     const int64_t parts = split ? 2 : 1;
     head = 0;
     x = (int64_t)((sizeof(OrthHead) + 255) / 256 * 256);
-    keep = x + 2 * parts * x_part * 2;  // two buffers of X
-    a = keep + (split ? 0 : x_part * 4);
+    rest = x + 2 * parts * x_part * 2;  // after two buffers of X
+    a = rest + (split ? 0 : x_part);
     b = a + parts * a_part * 2;
     total = b + parts * a_part * 2;
   }
@@ -233,13 +356,13 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
   x[1] = x[0] + (SPLIT ? 2 : 1) * L.x_part;
   _Float16* A = reinterpret_cast<_Float16*>(ws + L.a);
   _Float16* B = reinterpret_cast<_Float16*>(ws + L.b);
-  float* keep = reinterpret_cast<float*>(ws + L.keep);
   const int64_t x_lo = SPLIT ? L.x_part : 0, a_lo = SPLIT ? L.a_part : 0;
 
   const int64_t n = R * K;
-  if (dt == kF32) norm_kernel<kF32><<<kNormBlocks, 256, 0, s>>>(G, n, head);
-  else if (dt == kF16) norm_kernel<kF16><<<kNormBlocks, 256, 0, s>>>(G, n, head);
-  else norm_kernel<kBF16><<<kNormBlocks, 256, 0, s>>>(G, n, head);
+  const unsigned blocks = (unsigned)std::min<int64_t>(kNormBlocks, (n + 2047) / 2048);
+  if (dt == kF32) norm_kernel<kF32><<<blocks, 256, 0, s>>>(G, n, head);
+  else if (dt == kF16) norm_kernel<kF16><<<blocks, 256, 0, s>>>(G, n, head);
+  else norm_kernel<kBF16><<<blocks, 256, 0, s>>>(G, n, head);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t quads = L.rp * L.kp / 4;
@@ -252,20 +375,18 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
     start_kernel<kBF16, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, head, x[0], x[0] + x_lo);
   if ((e = hipGetLastError()) != hipSuccess) return e;
 
-  auto op = [](const _Float16* p, int64_t ld, int64_t rows) {
-    return GemmOperand{reinterpret_cast<const uint16_t*>(p), ld, rows};
+  auto op = [](const _Float16* p, int64_t ld, int64_t rows, int64_t lo) {
+    return GemmOperand{reinterpret_cast<const uint16_t*>(p), ld, rows, lo};
   };
   for (int i = 0; i < steps; ++i) {
     const _Float16* from = x[i & 1];
     OrthArgs p{};
-    p.segments = SPLIT ? 3 : 1;
     p.ca = 3.4445f;
     p.cb = -4.7750f;
     p.cc = 2.0315f;
     p.rho = i == 0 ? &head->rho : nullptr;
     // A = X X^T, or X^T X (both operands then have k as their row index)
-    p.a = p.b = op(from, L.kp, L.mp);
-    p.a_lo = p.b_lo = x_lo;
+    p.a = p.b = op(from, L.kp, L.mp, x_lo);
     p.steps = (int)((L.tall ? L.rp : L.kp) / kGemmStep);
     p.rows = p.cols = L.mp;
     p.hi = A;
@@ -274,8 +395,7 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
                : launch_orth_product<kGram, false, false, SPLIT>(p, s);
     if (e != hipSuccess) return e;
     // B = b A + c A A (A is symmetric: its rows are its columns)
-    p.a = p.b = op(A, L.mp, L.mp);
-    p.a_lo = p.b_lo = a_lo;
+    p.a = p.b = op(A, L.mp, L.mp, a_lo);
     p.steps = (int)(L.mp / kGemmStep);
     p.from_hi = A;
     p.from_lo = A + a_lo;
@@ -287,10 +407,10 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
     p.cols = L.kp;
     p.from_hi = from;
     p.from_lo = from + x_lo;
-    p.from = i == 0 || SPLIT ? nullptr : keep;
+    p.rest = reinterpret_cast<uint32_t*>(ws + L.rest);
+    p.from_rest = i > 0;
     p.hi = x[(i + 1) & 1];
     p.lo = p.hi + x_lo;
-    p.keep = keep;
     if (i + 1 == steps) {
       p.out = out;
       p.out_dt = dt;
@@ -298,16 +418,12 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
       p.K = K;
     }
     if (L.tall) {
-      p.a = op(from, L.kp, L.rp);
-      p.b = op(B, L.mp, L.mp);
-      p.a_lo = x_lo;
-      p.b_lo = a_lo;
+      p.a = op(from, L.kp, L.rp, x_lo);
+      p.b = op(B, L.mp, L.mp, a_lo);
       e = launch_orth_product<kUpdate, false, false, SPLIT>(p, s);
     } else {
-      p.a = op(B, L.mp, L.mp);
-      p.b = op(from, L.kp, L.kp);
-      p.a_lo = a_lo;
-      p.b_lo = x_lo;
+      p.a = op(B, L.mp, L.mp, a_lo);
+      p.b = op(from, L.kp, L.kp, x_lo);
       e = launch_orth_product<kUpdate, false, true, SPLIT>(p, s);
     }
     if (e != hipSuccess) return e;

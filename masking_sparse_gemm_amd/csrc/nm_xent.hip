@@ -118,11 +118,22 @@ __global__ void __launch_bounds__(1024)
   const int64_t t = (int64_t)blockIdx.x * 32 + x;
   float m = -INFINITY, s = 0.f;
   if (t < T) {
-    for (int64_t i = y; i < parts; i += 32) {
-      const float mi = top[i * T + t], si = sum[i * T + t];
-      const float n = fmaxf(m, mi), sh = n == -INFINITY ? 0.f : n;
-      s = s * __builtin_amdgcn_exp2f((m - sh) * kLog2e) +
-          si * __builtin_amdgcn_exp2f((mi - sh) * kLog2e);
+    // eight loads of each kind in flight at a time
+    for (int64_t i = y; i < parts; i += 8 * 32) {
+      float mi[8], si[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool in = i + 32 * k < parts;
+        mi[k] = in ? top[(i + 32 * k) * T + t] : -INFINITY;
+        si[k] = in ? sum[(i + 32 * k) * T + t] : 0.f;
+      }
+      float n = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) n = fmaxf(n, mi[k]);
+      const float sh = n == -INFINITY ? 0.f : n;
+      s *= __builtin_amdgcn_exp2f((m - sh) * kLog2e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += si[k] * __builtin_amdgcn_exp2f((mi[k] - sh) * kLog2e);
       m = n;
     }
   }
@@ -177,11 +188,13 @@ unsigned pad_grid(int64_t chunks) { return stride_grid(chunks, 256); }
 struct TokenArgs {  // of the tokens, padded to a whole number of 64
   int* y;           // target, -1 where left out
   float* lse;
-  float* g;         // g 2^e
-  float* back;      // one number: 2^-e
+  float* g;         // g times 2^14 over the largest
+  float* back;      // one number: what brings a sum of P back
 };
 
-// One workgroup: the largest |g| of the tokens that count, then 2^e with 2^13 <= 2^e max < 2^14.
+// One workgroup: the largest |g| of the tokens that count, then all g over it, times 2^14.  A mean's
+// equal g become 2^14, so that the entries of P at the targets, just below 2^14 in size, lie where
+// 16-bit numbers are densest for their size.
 __global__ void __launch_bounds__(1024)
     tokens_kernel(const int64_t* __restrict__ target, const float* __restrict__ lse,
                   const float* __restrict__ gout, int64_t V, int64_t T, int64_t Tp, TokenArgs out) {
@@ -195,15 +208,13 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = fmaxf(top, part[i]);
-  int e = 0;
-  if (top > 0.f && top < INFINITY) frexpf(top, &e);  // top = f 2^e, f in [1/2, 1)
-  e = min(max(14 - e, -100), 100);
-  if (threadIdx.x == 0) *out.back = ldexpf(1.f, -e);
+  const bool scaled = top > 0.f && top < INFINITY;
+  if (threadIdx.x == 0) *out.back = scaled ? top * 0x1p-14f : 1.f;
   for (int64_t t = threadIdx.x; t < Tp; t += 1024) {
     const bool live = t < T && target[t] >= 0 && target[t] < V;
     out.y[t] = live ? (int)target[t] : -1;
     out.lse[t] = live ? lse[t] : 0.f;
-    out.g[t] = live ? ldexpf(gout[t], e) : 0.f;
+    out.g[t] = !live ? 0.f : scaled ? gout[t] / top * 0x1p14f : gout[t];
   }
 }
 
@@ -231,22 +242,33 @@ __global__ void __launch_bounds__(G::kThreads) prob_kernel(ProbArgs p) {
   typename G::Acc acc;
   G::clear(acc);
   G::run(p.w, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
-  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t l) {
-    if (row >= p.rows || col >= p.Tp) return;
-    const float4_t lse = *reinterpret_cast<const float4_t*>(p.tok.lse + col);
-    const float4_t g = *reinterpret_cast<const float4_t*>(p.tok.g + col);
-    const int4 y = *reinterpret_cast<const int4*>(p.tok.y + col);
-    const int v = (int)(p.v0 + row);
-    const int ys[4] = {y.x, y.y, y.z, y.w};
-    float q[4];
+  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = __builtin_amdgcn_exp2f((l[i] - lse[i]) * kLog2e);
-      q[i] = v < p.V && ys[i] >= 0 ? (e - (v == ys[i] ? 1.f : 0.f)) * g[i] : 0.f;
+  for (int j = 0; j < G::kFN; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int64_t col = col0 + 32 * j + 8 * c;
+      if (col >= p.Tp) continue;
+      const float4_t lse = *reinterpret_cast<const float4_t*>(p.tok.lse + col);
+      const float4_t g = *reinterpret_cast<const float4_t*>(p.tok.g + col);
+      const int4 y = *reinterpret_cast<const int4*>(p.tok.y + col);
+      const int ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < G::kFM; ++i) {
+        const int64_t row = row0 + 32 * i;
+        if (row >= p.rows) continue;
+        const float4_t l = G::quad(acc, i, j, c);
+        const int v = (int)(p.v0 + row);
+        float q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = __builtin_amdgcn_exp2f((l[e] - lse[e]) * kLog2e);
+          q[e] = v < p.V && ys[e] >= 0 ? (x - (v == ys[e] ? 1.f : 0.f)) * g[e] : 0.f;
+        }
+        *reinterpret_cast<u32x2_t*>(p.P + row * p.Tp + col) =
+            u32x2_t{pack2<BF16>(q[0], q[1]), pack2<BF16>(q[2], q[3])};
+      }
     }
-    *reinterpret_cast<u32x2_t*>(p.P + row * p.Tp + col) =
-        u32x2_t{pack2<BF16>(q[0], q[1]), pack2<BF16>(q[2], q[3])};
-  });
 }
 
 struct GradXArgs {
@@ -273,16 +295,28 @@ __global__ void __launch_bounds__(G::kThreads) grad_x_kernel(GradXArgs p) {
   G::clear(acc);
   if (steps > 0) G::run(w, q, m0, n0, steps, p.klen - (int64_t)s0 * kGemmStep, smem, acc);
   float* out = p.sums + (int64_t)blockIdx.y * p.K * p.Tp;
-  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t v) {
-    if (row >= p.K || col >= p.Tp) return;
-    float4_t* o = reinterpret_cast<float4_t*>(out + row * p.Tp + col);
-    if (p.add) {
-      const float4_t b = *o;
+  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += b[i];
+  for (int i = 0; i < G::kFM; ++i) {
+    const int64_t row = row0 + 32 * i;
+    float4_t before[4 * G::kFN];  // read together: between the stores each would be waited for
+    if (p.add) {
+#pragma unroll
+      for (int q = 0; q < 4 * G::kFN; ++q) {
+        const int64_t col = col0 + 32 * (q / 4) + 8 * (q % 4);
+        if (row < p.K && col < p.Tp)
+          before[q] = *reinterpret_cast<const float4_t*>(out + row * p.Tp + col);
+      }
     }
-    *o = v;
-  });
+#pragma unroll
+    for (int q = 0; q < 4 * G::kFN; ++q) {
+      const int64_t col = col0 + 32 * (q / 4) + 8 * (q % 4);
+      if (row >= p.K || col >= p.Tp) continue;
+      float4_t v = G::quad(acc, i, q / 4, q % 4);
+      if (p.add) v += before[q];
+      *reinterpret_cast<float4_t*>(out + row * p.Tp + col) = v;
+    }
+  }
 }
 
 struct GradWArgs {
@@ -305,20 +339,25 @@ __global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
   G::run(p.q, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
   const float back = *p.back;
   const bool whole = p.K % 4 == 0;
-  G::each4(acc, m0, n0, [&](int64_t row, int64_t col, float4_t v) {
-    if (row >= p.rows || col >= p.K) return;
-    uint16_t* o = p.dW + row * p.K + col;
-    const uint32_t a = pack2<BF16>(v[0] * back, v[1] * back);
-    const uint32_t b = pack2<BF16>(v[2] * back, v[3] * back);
-    if (whole) {
-      *reinterpret_cast<u32x2_t*>(o) = u32x2_t{a, b};
-    } else {
-      const uint32_t h[4] = {a & 0xFFFFu, a >> 16, b & 0xFFFFu, b >> 16};
+  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + i < p.K) o[i] = (uint16_t)h[i];
+  for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+    for (int q = 0; q < 4 * G::kFN; ++q) {
+      const int64_t row = row0 + 32 * i, col = col0 + 32 * (q / 4) + 8 * (q % 4);
+      if (row >= p.rows || col >= p.K) continue;
+      const float4_t v = G::quad(acc, i, q / 4, q % 4) * back;
+      uint16_t* o = p.dW + row * p.K + col;
+      const uint32_t a = pack2<BF16>(v[0], v[1]), b = pack2<BF16>(v[2], v[3]);
+      if (whole) {
+        *reinterpret_cast<u32x2_t*>(o) = u32x2_t{a, b};
+      } else {
+        const uint32_t h[4] = {a & 0xFFFFu, a >> 16, b & 0xFFFFu, b >> 16};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.K) o[e] = (uint16_t)h[e];
+      }
     }
-  });
 }
 
 template <bool BF16>
@@ -426,8 +465,8 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
   for (int64_t v0 = 0; v0 < V; v0 += L.piece) {
     const int64_t rows = V - v0 < L.piece ? V - v0 : L.piece, rp = pad64(rows);
     ProbArgs a{};
-    a.w = GemmOperand{Wp + v0 * ldw, ldw, rows};
-    a.x = GemmOperand{Xp, L.Tp, L.Tp};
+    a.w = GemmOperand{Wp + v0 * ldw, ldw, rows, 0};
+    a.x = GemmOperand{Xp, L.Tp, L.Tp, 0};
     a.steps = (int)(L.Kp / kGemmStep);
     a.v0 = v0;
     a.V = V;
@@ -442,8 +481,8 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     if (e != hipSuccess) return e;
 
     GradWArgs b{};
-    b.q = GemmOperand{P, L.Tp, rp};
-    b.x = GemmOperand{Xp, L.Tp, L.Kp};
+    b.q = GemmOperand{P, L.Tp, rp, 0};
+    b.x = GemmOperand{Xp, L.Tp, L.Kp, 0};
     b.steps = (int)(L.Tp / kGemmStep);
     b.rows = rows;
     b.K = K;
@@ -456,8 +495,8 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     if (e != hipSuccess) return e;
 
     GradXArgs c{};
-    c.w = GemmOperand{Wp + v0 * ldw, ldw, L.Kp};
-    c.q = GemmOperand{P, L.Tp, L.Tp};
+    c.w = GemmOperand{Wp + v0 * ldw, ldw, L.Kp, 0};
+    c.q = GemmOperand{P, L.Tp, L.Tp, 0};
     c.klen = rows;
     c.steps = (int)(rp / kGemmStep);
     c.per = (c.steps + L.splits - 1) / L.splits;
@@ -504,8 +543,8 @@ hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t 
     if ((e = hipGetLastError()) != hipSuccess) return e;
     w = c;
   }
-  p.w = GemmOperand{w, L.Kp, V};
-  p.x = GemmOperand{x, L.Tp, L.Tp};
+  p.w = GemmOperand{w, L.Kp, V, 0};
+  p.x = GemmOperand{x, L.Tp, L.Tp, 0};
   p.steps = (int)(L.Kp / kGemmStep);
   p.V = V;
   p.T = T;
