@@ -87,7 +87,7 @@ inline GemmMap make_gemm_map(int64_t tiles_m, int64_t tiles_n, bool lower = fals
 template <int WM, int WN, int FM, int FN, bool AS, bool BS, bool BF16, bool SWAP, int STAGES = 2,
           int PARTS = 1>
 struct Gemm {
-  static constexpr int kFM = FM, kFN = FN;
+  static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kBM = 32 * FM * WM, kBN = 32 * FN * WN;
   static constexpr int kABytes = kBM * 2 * kGemmStep, kBBytes = kBN * 2 * kGemmStep;
@@ -307,6 +307,51 @@ struct Gemm {
     static_assert(SWAP, "rows by lane");
     return float4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
                     acc[i][j][4 * g + 3]};
+  }
+
+  // Stores the accumulators as 16-bit numbers, element (row, col) at out[row * ld + col] for row <
+  // rows and col < cols.  Where rows of `out` are whole 16-byte pieces, each wave's 32 rows pass
+  // through its own part of smem and leave in 16-byte pieces of whole 128-byte lines: stored as
+  // the lanes hold them, 8 bytes in each of 32 rows, they take four times the requests.
+  template <bool TO_BF16>
+  static __device__ __forceinline__ void store16(const Acc& acc, int64_t m0, int64_t n0,
+                                                 uint8_t* smem, uint16_t* out, int64_t ld,
+                                                 int64_t rows, int64_t cols) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool whole = ld % 8 == 0 && cols % 8 == 0;
+    constexpr int kPitch = 64 * FN + 16, kPieces = 4 * FN;  // bytes, 16-byte pieces a row
+    static_assert(kWaves * 32 * kPitch <= kLds, "the waves' parts fit");
+    uint8_t* mine = smem + wave * 32 * kPitch;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t row = m0 + (wave / WN) * 32 * FM + 32 * i;
+      const int64_t col = n0 + (wave % WN) * 32 * FN;
+#pragma unroll
+      for (int q = 0; q < 4 * FN; ++q) {
+        const float4_t v = quad(acc, i, q / 4, q % 4);
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = TO_BF16 ? f32_to_bf16(v[e]) : f32_to_f16(v[e]);
+        const int c = 32 * (q / 4) + 8 * (q % 4) + 4 * (lane >> 5);
+        if (whole) {
+          *reinterpret_cast<u32x2_t*>(mine + (lane & 31) * kPitch + 2 * c) =
+              u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
+        } else if (row + (lane & 31) < rows) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + c + e < cols) out[(row + (lane & 31)) * ld + col + c + e] = (uint16_t)h[e];
+        }
+      }
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < 32 * kPieces / 64; ++k) {
+          const int p = k * 64 + lane, r = p / kPieces, c = p % kPieces * 8;
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * kPitch + 2 * c);
+          if (row + r < rows && col + c < cols)
+            *reinterpret_cast<u32x4_t*>(out + (row + r) * ld + col + c) = v;
+        }
+      }
+    }
   }
 };
 

@@ -25,7 +25,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int64_t kPieceBytes = 64 << 20;  // of P
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 32;
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 int64_t pad256b(int64_t n) { return (n + 255) / 256 * 256; }
@@ -51,6 +51,47 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// The products' tiles.  256 x 256 is the fastest on many large tiles; of 128 x 128 two fit a unit,
+// so that one's epilogue runs under the other's steps, and short or few sums are faster in them;
+// 128 x 64 suits few tokens.
+enum XentTile { kTile256, kTile128, kTileNarrow, kXentTiles };
+constexpr int kTileM[kXentTiles] = {256, 128, 128}, kTileN[kXentTiles] = {256, 128, 64};
+
+template <class G>
+struct TileTag {
+  typedef G type;
+};
+template <bool AS, bool BS, bool BF16, bool SWAP, typename F>
+hipError_t with_tile(int tile, F&& f) {
+  if (tile == kTile256) return f(TileTag<Gemm<2, 4, 4, 2, AS, BS, BF16, SWAP, 2>>{});
+  if (tile == kTile128) return f(TileTag<Gemm<2, 4, 2, 1, AS, BS, BF16, SWAP, 2>>{});
+  return f(TileTag<Gemm<2, 2, 2, 1, AS, BS, BF16, SWAP, 3>>{});
+}
+
+int64_t tiles_of(int tile, int64_t m, int64_t n) {
+  return ((m + kTileM[tile] - 1) / kTileM[tile]) * ((n + kTileN[tile] - 1) / kTileN[tile]);
+}
+
+// Estimated time (us) of `count` tiles of `steps` steps: whole rounds of 256 for the large tile,
+// and 512 at a time in a steady flow for the small ones, but never less than one tile alone.
+// Measured, 256 / 128 / narrow: loss 32768 x 4096, 2048 tokens 522 / 611 / 731 us; 20000 x 1024,
+// 1000 tokens 74 / 58 / 71; 12000 x 2048, 128 tokens 54 / 25 / 17; 30000 x 4096, 32 tokens
+// 99 / 62 / 41; dW of 12000 x 2048, 128 tokens 21 / 17 / 23.
+double tile_us(int tile, int64_t count, int64_t steps) {
+  if (tile == kTile256) return (double)((count + 255) / 256) * (2.0 * steps + 8.0);
+  const bool mid = tile == kTile128;
+  const double alone = mid ? 0.65 * steps + 4.0 : 0.45 * steps + 3.0;
+  const double flow = (double)count / 512 * (mid ? 1.19 * steps + 4.6 : 0.71 * steps + 3.5);
+  return alone > flow ? alone : flow;
+}
+
+int pick_tile(int64_t m, int64_t n, int64_t steps) {
+  int best = 0;
+  for (int t = 1; t < kXentTiles; ++t)
+    if (tile_us(t, tiles_of(t, m, n), steps) < tile_us(best, tiles_of(best, m, n), steps)) best = t;
+  return best;
+}
+
 // ---- loss ------------------------------------------------------------------------------
 
 struct StatsArgs {
@@ -63,8 +104,9 @@ struct StatsArgs {
   float* hit;        // [T]: the target's logit
 };
 
-template <class G, int FM, int FN, int WM, int WN>
+template <class G>
 __global__ void __launch_bounds__(G::kThreads) stats_kernel(StatsArgs p) {
+  constexpr int FM = G::kFM, FN = G::kFN, WM = G::kWM, WN = G::kWN;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   int tm, tn;
   if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
@@ -153,25 +195,18 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-template <int WM, int WN, int FM, int FN, bool BF16>
-hipError_t launch_stats(StatsArgs p, hipStream_t s) {
-  typedef Gemm<WM, WN, FM, FN, false, true, BF16, false> G;
-  p.map = make_gemm_map((p.V + G::kBM - 1) / G::kBM, (p.T + G::kBN - 1) / G::kBN);
-  return G::template launch<stats_kernel<G, FM, FN, WM, WN>>(p, p.map, 1, s);
-}
-
 struct LossLayout {
   int64_t Kp, Tp;
-  bool copy_x, copy_w, narrow;
+  bool copy_x, copy_w;
+  int tile;
   int64_t x, w, top, sum, hit, total, parts;
   LossLayout(int64_t V, int64_t K, int64_t T) {
     Kp = pad64(K);
     copy_w = K % 64 != 0;
     copy_x = copy_w || T % 8 != 0;
     Tp = copy_x ? pad64(T) : T;
-    // a narrow tile wastes less of the matrix cores on few tokens and spreads W over more units
-    narrow = T <= 64;
-    parts = narrow ? (V + 127) / 128 * 2 : (V + 255) / 256 * 2;
+    tile = pick_tile(V, T, Kp / kGemmStep);
+    parts = (V + kTileM[tile] - 1) / kTileM[tile] * 2;  // every tile has two rows of waves
     x = 0;
     w = x + (copy_x ? pad256b(Kp * Tp * 2) : 0);
     top = w + (copy_w ? pad256b(V * Kp * 2) : 0);
@@ -228,11 +263,6 @@ struct ProbArgs {
   uint16_t* P;       // rows x Tp
 };
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return BF16 ? f32_to_bf16(a) | f32_to_bf16(b) << 16 : f32_to_f16(a) | f32_to_f16(b) << 16;
-}
-
 template <class G, bool BF16>
 __global__ void __launch_bounds__(G::kThreads) prob_kernel(ProbArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -248,27 +278,26 @@ __global__ void __launch_bounds__(G::kThreads) prob_kernel(ProbArgs p) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int64_t col = col0 + 32 * j + 8 * c;
-      if (col >= p.Tp) continue;
-      const float4_t lse = *reinterpret_cast<const float4_t*>(p.tok.lse + col);
-      const float4_t g = *reinterpret_cast<const float4_t*>(p.tok.g + col);
-      const int4 y = *reinterpret_cast<const int4*>(p.tok.y + col);
+      float4_t lse{}, g{};
+      int4 y{-1, -1, -1, -1};
+      if (col < p.Tp) {
+        lse = *reinterpret_cast<const float4_t*>(p.tok.lse + col);
+        g = *reinterpret_cast<const float4_t*>(p.tok.g + col);
+        y = *reinterpret_cast<const int4*>(p.tok.y + col);
+      }
       const int ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i) {
-        const int64_t row = row0 + 32 * i;
-        if (row >= p.rows) continue;
-        const float4_t l = G::quad(acc, i, j, c);
-        const int v = (int)(p.v0 + row);
-        float q[4];
+        const int v = (int)(p.v0 + row0 + 32 * i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = __builtin_amdgcn_exp2f((l[e] - lse[e]) * kLog2e);
-          q[e] = v < p.V && ys[e] >= 0 ? (x - (v == ys[e] ? 1.f : 0.f)) * g[e] : 0.f;
+          const float x = __builtin_amdgcn_exp2f((acc[i][j][4 * c + e] - lse[e]) * kLog2e);
+          acc[i][j][4 * c + e] =
+              v < p.V && ys[e] >= 0 ? (x - (v == ys[e] ? 1.f : 0.f)) * g[e] : 0.f;
         }
-        *reinterpret_cast<u32x2_t*>(p.P + row * p.Tp + col) =
-            u32x2_t{pack2<BF16>(q[0], q[1]), pack2<BF16>(q[2], q[3])};
       }
     }
+  G::template store16<BF16>(acc, m0, n0, smem, p.P, p.Tp, p.rows, p.Tp);
 }
 
 struct GradXArgs {
@@ -338,26 +367,11 @@ __global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
   G::clear(acc);
   G::run(p.q, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
   const float back = *p.back;
-  const bool whole = p.K % 4 == 0;
-  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
 #pragma unroll
   for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-    for (int q = 0; q < 4 * G::kFN; ++q) {
-      const int64_t row = row0 + 32 * i, col = col0 + 32 * (q / 4) + 8 * (q % 4);
-      if (row >= p.rows || col >= p.K) continue;
-      const float4_t v = G::quad(acc, i, q / 4, q % 4) * back;
-      uint16_t* o = p.dW + row * p.K + col;
-      const uint32_t a = pack2<BF16>(v[0], v[1]), b = pack2<BF16>(v[2], v[3]);
-      if (whole) {
-        *reinterpret_cast<u32x2_t*>(o) = u32x2_t{a, b};
-      } else {
-        const uint32_t h[4] = {a & 0xFFFFu, a >> 16, b & 0xFFFFu, b >> 16};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < p.K) o[e] = (uint16_t)h[e];
-      }
-    }
+    for (int j = 0; j < G::kFN; ++j) acc[i][j] *= back;
+  G::template store16<BF16>(acc, m0, n0, smem, p.dW, p.K, p.rows, p.K);
 }
 
 template <bool BF16>
@@ -383,8 +397,8 @@ __global__ void __launch_bounds__(256)
 
 struct GradLayout {
   int64_t Kp, Tp, piece;  // piece: rows of W at a time
-  bool copy_w, big_x;     // big_x: 256 x 256 tiles for dX
-  int splits;
+  bool copy_w;
+  int tile_x, splits;     // of dX
   int64_t x, w, tok_y, tok_lse, tok_g, back, P, sums, total;
   GradLayout(int64_t V, int64_t K, int64_t T) {
     Kp = pad64(K);
@@ -393,15 +407,20 @@ struct GradLayout {
     piece = kPieceBytes / (2 * Tp) / 256 * 256;
     if (piece < 256) piece = 256;
     if (piece > V) piece = V;
-    const int64_t big = ((K + 255) / 256) * ((Tp + 255) / 256);
-    const int64_t mid = ((K + 127) / 128) * ((Tp + 127) / 128);
-    big_x = big * kMaxSplit >= 256;
-    const int64_t tiles = big_x ? big : mid;
-    int64_t z = (256 + tiles - 1) / tiles;
-    z = z < 1 ? 1 : z > kMaxSplit ? kMaxSplit : z;
+    // dX's sums over the piece are split where its tiles are too few; each split costs a write
+    // and a read of its sums (5 GB a ms)
     const int64_t steps = (piece + 63) / 64;
-    while (z > 1 && steps / z < 8) --z;
-    splits = (int)z;
+    double least = 1e30;
+    for (int t = 0; t < kXentTiles; ++t)
+      for (int z = 1; z <= kMaxSplit && (z == 1 || steps / z >= 4); z = z < 4 ? z + 1 : z + 2) {
+        const double us = tile_us(t, tiles_of(t, K, Tp) * z, (steps + z - 1) / z) +
+                          (double)z * K * Tp * 8 / 5e6;
+        if (us < least) {
+          least = us;
+          tile_x = t;
+          splits = z;
+        }
+      }
     x = 0;
     w = x + pad256b(Kp * Tp * 2);
     tok_y = w + (copy_w ? pad256b(V * Kp * 2) : 0);
@@ -413,22 +432,6 @@ struct GradLayout {
     total = sums + pad256b((int64_t)splits * K * Tp * 4);
   }
 };
-
-template <class G, bool BF16>
-hipError_t launch_prob(ProbArgs p, hipStream_t s) {
-  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.Tp + G::kBN - 1) / G::kBN);
-  return G::template launch<prob_kernel<G, BF16>>(p, p.map, 1, s);
-}
-template <class G>
-hipError_t launch_grad_x(GradXArgs p, int splits, hipStream_t s) {
-  p.map = make_gemm_map((p.K + G::kBM - 1) / G::kBM, (p.Tp + G::kBN - 1) / G::kBN);
-  return G::template launch<grad_x_kernel<G>>(p, p.map, splits, s);
-}
-template <class G, bool BF16>
-hipError_t launch_grad_w(GradWArgs p, hipStream_t s) {
-  p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.K + G::kBN - 1) / G::kBN);
-  return G::template launch<grad_w_kernel<G, BF16>>(p, p.map, 1, s);
-}
 
 __global__ void __launch_bounds__(256) zero_kernel(uint16_t* out, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
@@ -474,10 +477,11 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     a.Tp = L.Tp;
     a.tok = tok;
     a.P = P;
-    const int64_t big = ((rp + 255) / 256) * ((L.Tp + 255) / 256);
-    if (L.Tp > 128 && big >= 128) e = launch_prob<Gemm<2, 4, 4, 2, false, true, BF16, true>, BF16>(a, s);
-    else if (L.Tp > 64) e = launch_prob<Gemm<2, 2, 2, 2, false, true, BF16, true>, BF16>(a, s);
-    else e = launch_prob<Gemm<2, 2, 2, 1, false, true, BF16, true>, BF16>(a, s);
+    e = with_tile<false, true, BF16, true>(pick_tile(rp, L.Tp, a.steps), [&](auto tag) {
+      typedef typename decltype(tag)::type G;
+      a.map = make_gemm_map((rp + G::kBM - 1) / G::kBM, (L.Tp + G::kBN - 1) / G::kBN);
+      return G::template launch<prob_kernel<G, BF16>>(a, a.map, 1, s);
+    });
     if (e != hipSuccess) return e;
 
     GradWArgs b{};
@@ -488,10 +492,11 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     b.K = K;
     b.back = tok.back;
     b.dW = dW + v0 * K;
-    if (((rows + 255) / 256) * ((K + 255) / 256) >= 128)
-      e = launch_grad_w<Gemm<2, 4, 4, 2, false, false, BF16, true>, BF16>(b, s);
-    else
-      e = launch_grad_w<Gemm<2, 2, 2, 2, false, false, BF16, true>, BF16>(b, s);
+    e = with_tile<false, false, BF16, true>(pick_tile(rows, K, b.steps), [&](auto tag) {
+      typedef typename decltype(tag)::type G;
+      b.map = make_gemm_map((rows + G::kBM - 1) / G::kBM, (K + G::kBN - 1) / G::kBN);
+      return G::template launch<grad_w_kernel<G, BF16>>(b, b.map, 1, s);
+    });
     if (e != hipSuccess) return e;
 
     GradXArgs c{};
@@ -504,8 +509,11 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     c.Tp = L.Tp;
     c.sums = sums;
     c.add = v0 > 0;
-    e = L.big_x ? launch_grad_x<Gemm<2, 4, 4, 2, true, true, BF16, true>>(c, L.splits, s)
-                : launch_grad_x<Gemm<2, 2, 2, 2, true, true, BF16, true>>(c, L.splits, s);
+    e = with_tile<true, true, BF16, true>(L.tile_x, [&](auto tag) {
+      typedef typename decltype(tag)::type G;
+      c.map = make_gemm_map((K + G::kBM - 1) / G::kBM, (L.Tp + G::kBN - 1) / G::kBN);
+      return G::template launch<grad_x_kernel<G>>(c, c.map, L.splits, s);
+    });
     if (e != hipSuccess) return e;
   }
   finish_x_kernel<BF16><<<stride_grid(K * L.Tp / 4, 256), 256, 0, s>>>(sums, L.splits, K, T, L.Tp,
@@ -552,11 +560,13 @@ hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t 
   p.top = reinterpret_cast<float*>(ws + L.top);
   p.sum = reinterpret_cast<float*>(ws + L.sum);
   p.hit = reinterpret_cast<float*>(ws + L.hit);
-  const bool bf16 = dt == kBF16;
-  if (L.narrow)
-    e = bf16 ? launch_stats<2, 2, 2, 1, true>(p, s) : launch_stats<2, 2, 2, 1, false>(p, s);
-  else
-    e = bf16 ? launch_stats<2, 4, 4, 2, true>(p, s) : launch_stats<2, 4, 4, 2, false>(p, s);
+  const auto launch = [&](auto tag) {
+    typedef typename decltype(tag)::type G;
+    p.map = make_gemm_map((V + G::kBM - 1) / G::kBM, (T + G::kBN - 1) / G::kBN);
+    return G::template launch<stats_kernel<G>>(p, p.map, 1, s);
+  };
+  e = dt == kBF16 ? with_tile<false, true, true, false>(L.tile, launch)
+                  : with_tile<false, true, false, false>(L.tile, launch);
   if (e != hipSuccess) return e;
   join_kernel<<<(unsigned)((T + 31) / 32), 1024, 0, s>>>(p.top, p.sum, L.parts, T, V, target, p.hit,
                                                        loss, lse);
