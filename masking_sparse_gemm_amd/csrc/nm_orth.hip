@@ -135,7 +135,7 @@ __device__ __forceinline__ float4_t widen(half4_t h) {
 
 // What fp16 lacks of a number, as fp8 (E4M3) times 2^10: at most 2^7 there, and seen down to 2^-19
 // of the scaled X, whose entries are around 1.
-constexpr float kRestScale = 1024.f;
+[[maybe_unused]] constexpr float kRestScale = 1024.f;
 __device__ __forceinline__ uint32_t pack_rest(float4_t r) {
   int w = 0;
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -317,7 +317,7 @@ hipError_t launch_orth_product(const OrthArgs& p, hipStream_t s) {
       return launch_orth_tile<Gemm<2, 2, 3, 3, AS, BS, false, true, 3>, KIND, false>(p, s);
     if (tile == 128)
       return launch_orth_tile<Gemm<2, 4, 2, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
-    return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 8>, KIND, false>(p, s);
+    return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
   }
 }
 

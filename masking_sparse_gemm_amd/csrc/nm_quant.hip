@@ -10,6 +10,7 @@
 // columns lie in the low half and the odd ones in the high half, column pair p at bits 4 p and
 // 4 p + 16: one shift and one and-or turn a word into a pair of 16-bit floats.
 #include <algorithm>
+#include <type_traits>
 
 #include "nm_grid.h"
 #include "nm_launch.h"
@@ -52,106 +53,136 @@ __device__ __forceinline__ uint32_t f32_to_scale(float s) {
   else return f32_to_f16(s);
 }
 
-// Eight elements of a row from column c; zeros past column C.  kWhole: C % 8 == 0, so the
-// eight are wholly inside or outside and their address is 16-byte aligned.
-template <int DT, bool kWhole>
-__device__ __forceinline__ void load8(const typename WeightElem<DT>::type* row, int64_t c,
-                                      int64_t C, float (&v)[8]) {
-  if constexpr (kWhole) {
-    if (c >= C) {
+typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+
+// Eight elements of a row from column c, as they are stored; zeros past column C.  kWhole: C % 8
+// == 0, so the eight are wholly inside or outside and their address is 16-byte aligned.
+template <int DT>
+struct Eight {
+  static constexpr int kWords = DT == kF32 ? 8 : 4;
+  uint32_t w[kWords];
+
+  template <bool kWhole>
+  __device__ __forceinline__ void load(const typename WeightElem<DT>::type* row, int64_t c,
+                                       int64_t C) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    } else if constexpr (DT == kF32) {
-      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(row + c);
-      const u32x4_t b = *reinterpret_cast<const u32x4_t*>(row + c + 4);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+    if constexpr (kWhole) {
+      if (c >= C) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(a[i]);
-        v[4 + i] = __uint_as_float(b[i]);
+      for (int h = 0; h < kWords / 4; ++h) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + c + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * h + i] = v[i];
       }
     } else {
-      const u32x4_t a = *reinterpret_cast<const u32x4_t*>(row + c);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = to_f32<DT>((uint16_t)(a[i / 2] >> (16 * (i & 1))));
+        if (c + i < C) {
+          if constexpr (DT == kF32) w[i] = row[c + i];
+          else w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+        }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < C ? to_f32<DT>(row[c + i]) : 0.f;
   }
-}
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (DT == kF32) return __uint_as_float(w[i]);
+    else if constexpr (DT == kBF16) return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    else return f16_to_f32(w[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
+  }
+  // The largest |x| as sign-cleared bits, which order like |x| with NaN above infinity, so that a
+  // group that holds a NaN gets a NaN scale; 16-bit types: one of the even and one of the odd
+  // elements in the halves of the word.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) t = larger(t, w[i] & (DT == kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu));
+    return t;
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (DT == kF32) return max(a, b);
+    else
+      return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2_t, a),
+                                                                    __builtin_bit_cast(ushort2_t, b)));
+  }
+  static __device__ __forceinline__ float to_float(uint32_t top) {
+    if constexpr (DT == kF32) return __uint_as_float(top);
+    else return to_f32<DT>((uint16_t)max(top >> 16, top & 0xFFFFu));
+  }
+};
 
-// Bits of |x|: as unsigned numbers they order like |x|, with NaN above infinity, so a group
-// that holds a NaN gets a NaN scale.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-template <int DT, bool BF16S, bool kBlocked, bool kWhole>
+template <int DT, bool BF16S, bool kBlocked, bool kWhole, int LOG_GROUP>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const typename WeightElem<DT>::type* __restrict__ W, int64_t R, int64_t C,
-                    int64_t S, int64_t blocks, int log_group, u32x4_t* __restrict__ codes,
+                    int64_t S, int64_t blocks, u32x4_t* __restrict__ codes,
                     uint16_t* __restrict__ scales) {
+  constexpr int kWords = 1 << (LOG_GROUP - 5);  // code words of a lane that share a scale
   const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;
-  const int64_t groups = (C + (1 << log_group) - 1) >> log_group;
+  const int64_t groups = (C + (1 << LOG_GROUP) - 1) >> LOG_GROUP;
   for (int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); b < blocks;
        b += (int64_t)gridDim.x * 4) {
     const int64_t g = b / S, s = b % S, row = 16 * g + r;
-    float v[4][8];
-    uint32_t top[4];
+    Eight<DT> v[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int64_t c = kBlockCols * s + 32 * w + 8 * j;
       if constexpr (kBlocked) {  // (g, step, 16, 32): a step is one instruction's columns
         const int64_t steps = C / 32, step = 4 * s + w;
-        load8<DT, true>(W + ((g * steps + step) * 16 + r) * 32 - 32 * step,
-                        step < steps ? c : C, C, v[w]);
+        v[w].template load<true>(W + ((g * steps + step) * 16 + r) * 32 - 32 * step,
+                                 step < steps ? c : C, C);
       } else {
-        load8<DT, kWhole>(W + (row < R ? row : 0) * C, row < R ? c : C, C, v[w]);
+        v[w].template load<kWhole>(W + (row < R ? row : 0) * C, row < R ? c : C, C);
       }
-      uint32_t t = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t = max(t, abs_bits(v[w][i]));
-      t = max(t, (uint32_t)__shfl_xor((int)t, 16));
-      top[w] = max(t, (uint32_t)__shfl_xor((int)t, 32));
     }
-    if (log_group >= 6) {
-      top[0] = top[1] = max(top[0], top[1]);
-      top[2] = top[3] = max(top[2], top[3]);
-    }
-    if (log_group == 7) top[0] = top[1] = top[2] = top[3] = max(top[0], top[2]);
     u32x4_t out;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t s16 = f32_to_scale<BF16S>(__uint_as_float(top[w]) / 7.f);
+    for (int w0 = 0; w0 < 4; w0 += kWords) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int w = w0; w < w0 + kWords; ++w) top = Eight<DT>::larger(top, v[w].top());
+      top = Eight<DT>::larger(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = Eight<DT>::larger(top, (uint32_t)__shfl_xor((int)top, 32));
+      const uint32_t s16 = f32_to_scale<BF16S>(Eight<DT>::to_float(top) / 7.f);
       const float sc = scale_to_f32<BF16S>(s16);
-      uint32_t word;
       if (DT != kF32 && __all(abs_bits(sc) >= 0x0D800000u)) {  // 2^-100: 1 / sc is finite
         // Both numbers have at most 11 significant bits, so a quotient of this size is a half
         // integer or at least 2^-13 away from one, and w * (1 / sc) is within 2^-18 of it:
-        // brought to a multiple of 2^-15 (by the addition of 384), it rounds as the quotient.
+        // brought to a multiple of 2^-15 by the addition of 384 (|quotient| is below 11), it rounds
+        // as the quotient.  The four codes of a half word add up as the digits of a float.
         const float inv = 1.f / sc;
-        word = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float q = __builtin_amdgcn_fmed3f(v[w][i] * inv, -9.f, 9.f);
-          q = (q + 384.f) - 384.f;
-          q = __builtin_amdgcn_fmed3f(q, -8.f, 7.f) + 12582920.f;  // 1.5 2^23 + 8: code + 8 below
-          word |= (__float_as_uint(q) & 15u) << (4 * (i >> 1) + 16 * (i & 1));
+        for (int w = w0; w < w0 + kWords; ++w) {
+          uint32_t half[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float digits = 0.f;
+#pragma unroll
+            for (int p = 3; p >= 0; --p) {
+              const float q = rintf(__builtin_fmaf(v[w].value(2 * p + h), inv, 384.f));
+              digits = __builtin_fmaf(digits, 16.f, __builtin_amdgcn_fmed3f(q, 376.f, 391.f));
+            }
+            half[h] = (uint32_t)(digits - 376.f * 4369.f);  // 4369 = 0x1111
+          }
+          out[w] = half[0] | half[1] << 16;
+          if (abs_bits(sc) >= 0x7F800000u) out[w] = 0x88888888u;  // no numbers: codes 0
         }
-        if (abs_bits(sc) >= 0x7F800000u) word = 0x88888888u;  // no numbers: codes 0
       } else {
-        word = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float q = rintf(v[w][i] / sc);
-          // a scale of zero, and elements that are no number, take code 0
-          const int code = sc != 0.f && q == q ? (int)fminf(fmaxf(q, -8.f), 7.f) + 8 : 8;
-          word |= (uint32_t)code << (4 * (i >> 1) + 16 * (i & 1));
+        for (int w = w0; w < w0 + kWords; ++w) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float q = rintf(v[w].value(i) / sc);
+            // a scale of zero, and elements that are no number, take code 0
+            const int code = sc != 0.f && q == q ? (int)fminf(fmaxf(q, -8.f), 7.f) + 8 : 8;
+            word |= (uint32_t)code << (4 * (i >> 1) + 16 * (i & 1));
+          }
+          out[w] = word;
         }
       }
-      out[w] = word;
-      const int64_t gi = (kBlockCols * s + 32 * w) >> log_group;
-      if (((32 * w) & ((1 << log_group) - 1)) == 0 && j == 0 && gi < groups)
-        scales[(g * groups + gi) * 16 + r] = (uint16_t)s16;
+      const int64_t gi = (kBlockCols * s + 32 * w0) >> LOG_GROUP;
+      if (j == 0 && gi < groups) scales[(g * groups + gi) * 16 + r] = (uint16_t)s16;
     }
     codes[b * 64 + lane] = out;
   }
@@ -653,14 +684,19 @@ hipError_t launch_quantize_as(const void* W, int64_t R, int64_t C, bool blocked,
   const E* w = static_cast<const E*>(W);
   u32x4_t* c = static_cast<u32x4_t*>(codes);
   uint16_t* sc = static_cast<uint16_t*>(scales);
-  const int lg = log2_of(group);
-  if (blocked)
-    quantize_kernel<DT, BF16S, true, true><<<grid, 256, 0, s>>>(w, R, C, S, blocks, lg, c, sc);
-  else if (C % 8 == 0)
-    quantize_kernel<DT, BF16S, false, true><<<grid, 256, 0, s>>>(w, R, C, S, blocks, lg, c, sc);
-  else
-    quantize_kernel<DT, BF16S, false, false><<<grid, 256, 0, s>>>(w, R, C, S, blocks, lg, c, sc);
-  return hipGetLastError();
+  const auto launch = [&](auto log_group) {
+    constexpr int kLog = decltype(log_group)::value;
+    if (blocked)
+      quantize_kernel<DT, BF16S, true, true, kLog><<<grid, 256, 0, s>>>(w, R, C, S, blocks, c, sc);
+    else if (C % 8 == 0)
+      quantize_kernel<DT, BF16S, false, true, kLog><<<grid, 256, 0, s>>>(w, R, C, S, blocks, c, sc);
+    else
+      quantize_kernel<DT, BF16S, false, false, kLog><<<grid, 256, 0, s>>>(w, R, C, S, blocks, c, sc);
+    return hipGetLastError();
+  };
+  if (group == 32) return launch(std::integral_constant<int, 5>{});
+  if (group == 64) return launch(std::integral_constant<int, 6>{});
+  return launch(std::integral_constant<int, 7>{});
 }
 
 }  // namespace
