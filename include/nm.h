@@ -363,6 +363,7 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
  * one column or a few (every T is taken; beyond some tens a dequantised product is faster).
  * meta NULL: dense codes of C = K columns.  Else the metadata, in NM_LAYOUT_BLOCKED, of a 2:4
  * pair whose values the codes hold (C = K/2; K % 64 == 0, else NM_ERR_LAYOUT); it is trusted.
+ * R < 2^26, K < 2^25, T < 2^20, else NM_ERR_SHAPE.
  * dt is the type of X and of the scales, NM_F16 or NM_BF16; y_dt is dt or NM_F32.  Codes enter
  * the matrix cores exactly, sums are fp32, a group's sum is scaled in fp32 and Y is rounded once.
  * workspace: nm_matvec_workspace_bytes(R, K, T, meta != NULL) bytes of device memory (0 for
@@ -380,7 +381,7 @@ nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta,
  *   lse[t]  = log sum over v of exp L[v, t]       (of every token)
  *   loss[t] = lse[t] - L[target[t], t]
  * loss and lse are fp32; sums are fp32.  V >= 1 where T > 0, V < 2^31, K < 2^22, T < 2^22,
- * else NM_ERR_SHAPE.  Fastest where K % 64 == 0 (else W is copied, padded, into the workspace)
+ * V*K, V*T and K*T < 2^36, else NM_ERR_SHAPE.  Fastest where K % 64 == 0 (else W is copied, padded, into the workspace)
  * and T % 8 == 0. */
 size_t nm_xent_workspace_bytes(int64_t V, int64_t K, int64_t T);
 nm_status nm_xent(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,

@@ -523,7 +523,10 @@ nm_status check_xent(nm_dtype dt, int64_t V, int64_t K, int64_t T) {
   if (V < 0 || K < 0 || T < 0 || V >= (int64_t)1 << 31 || K >= kMaxSide || T >= kMaxSide ||
       (V == 0 && T > 0))
     return NM_ERR_SHAPE;
-  return check_shape(V, K, 1);
+  // below 2^36 logits and entries of X every launch has fewer than 2^32 work-items
+  nm_status st = check_shape(V, K, 1);
+  if (st == NM_OK) st = check_shape(V, T, 1);
+  return st == NM_OK ? check_shape(K, T, 1) : st;
 }
 
 nm_status check_workspace(const void* p, size_t have, size_t need) {
@@ -593,7 +596,9 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
 
 namespace {
 nm_status check_matvec(int64_t R, int64_t K, int64_t T) {
-  if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 25) return NM_ERR_SHAPE;
+  // a launch has 512 work-items for 16 rows or more, one slice for 1024 rows of X or more
+  if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 25 || R >= (int64_t)1 << 26)
+    return NM_ERR_SHAPE;
   return check_shape(R, K, 1);
 }
 }  // namespace

@@ -227,15 +227,12 @@ struct Gemm {
     };
     auto multiply = [&](const Fragments& f) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int q = 0; q < 2 * PARTS - 1; ++q)  // hi hi, hi lo, lo hi
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          acc[i][j] = mfma(f.a[0][i], f.b[0][j], acc[i][j]);
-          if constexpr (PARTS == 2) {
-            acc[i][j] = mfma(f.a[0][i], f.b[1][j], acc[i][j]);
-            acc[i][j] = mfma(f.a[1][i], f.b[0][j], acc[i][j]);
-          }
-        }
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = mfma(f.a[q >> 1][i], f.b[q & 1][j], acc[i][j]);
     };
     // Waits until all but the last `keep` steps' loads have landed (all of them where fewer steps
     // follow) and this wave's reads are done, then meets the other waves.

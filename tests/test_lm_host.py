@@ -77,6 +77,7 @@ def matvec(codes=far(1), scales=far(2), meta=None, R=16, K=128, group=64, X=far(
 
 def test_matvec_refusals():
     assert matvec(dt=nm.NM_F32, ydt=nm.NM_F32) == "dtype" and matvec(ydt=nm.NM_F16) == "dtype"
+    assert matvec(R=1 << 26, K=1) == matvec(K=1 << 25) == "shape"
     assert matvec(T=-1) == matvec(T=1 << 20) == matvec(K=-1) == "shape"
     assert matvec(group=16) == "unsupported" and matvec(meta=far(6), K=96) == "layout"
     assert matvec(codes=None) == matvec(X=None) == matvec(Y=None) == "null"
@@ -96,6 +97,7 @@ def xent(W=far(1), X=far(2), dt=nm.NM_BF16, V=100, K=64, T=8, y=far(3), loss=far
 def test_xent_refusals():
     assert xent(dt=nm.NM_F32) == "dtype"
     assert xent(V=0) == xent(V=1 << 31) == xent(K=1 << 22) == xent(T=1 << 22) == xent(T=-1) == "shape"
+    assert xent(V=1 << 20, T=1 << 16) == xent(K=1 << 18, T=1 << 18) == "shape"
     assert xent(W=None) == xent(y=None) == xent(lse=None) == xent(ws=None) == "null"
     assert xent(X=ODD) == xent(y=ODD) == xent(ws=ODD) == "align"
     assert xent(n=64) == "scratch"
