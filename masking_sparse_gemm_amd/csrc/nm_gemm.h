@@ -261,27 +261,29 @@ struct Gemm {
         multiply(f[kk & 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      const bool more = s + STAGES < steps;
       if (s + 1 < steps) {
         // step s + 1 has landed; no wave reads this step's stage any more
         meet(std::integral_constant<int, STAGES - 2>{}, s + STAGES <= steps);
-        if (s + STAGES < steps) issue(s + STAGES, stage);
         read(f[0], next, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
       multiply(f[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) issue(s + STAGES, stage);  // in the shadow of the products just queued
       __builtin_amdgcn_sched_barrier(0);
       stage = next;
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // smem may be reused
   }
 
-  // Launches kKernel, which uses this tile's LDS, on map.groups() x splits workgroups.
+  // Launches kKernel, which uses this tile's LDS, on groups x splits workgroups.
   template <auto kKernel, typename Args>
-  static hipError_t launch(const Args& args, const GemmMap& map, int splits, hipStream_t s) {
+  static hipError_t launch(const Args& args, int groups, int splits, hipStream_t s) {
     static const hipError_t attr = hipFuncSetAttribute(
         reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (attr != hipSuccess) return attr;
-    kKernel<<<dim3((unsigned)map.groups(), (unsigned)splits), kThreads, kLds, s>>>(args);
+    kKernel<<<dim3((unsigned)groups, (unsigned)splits), kThreads, kLds, s>>>(args);
     return hipGetLastError();
   }
 

@@ -298,7 +298,7 @@ template <class G, int KIND, bool SPLIT>
 hipError_t launch_orth_tile(OrthArgs p, hipStream_t s) {
   // A and B are symmetric: their tiles above the diagonal are written by those below it
   p.map = make_gemm_map((p.rows + G::kBM - 1) / G::kBM, (p.cols + G::kBN - 1) / G::kBN, KIND != kUpdate);
-  return G::template launch<orth_kernel<G, KIND, SPLIT>>(p, p.map, 1, s);
+  return G::template launch<orth_kernel<G, KIND, SPLIT>>(p, p.map.groups(), 1, s);
 }
 
 template <int KIND, bool AS, bool BS, bool SPLIT>

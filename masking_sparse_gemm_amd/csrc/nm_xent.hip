@@ -30,25 +30,106 @@ constexpr int kMaxSplit = 32;
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 int64_t pad256b(int64_t n) { return (n + 255) / 256 * 256; }
 
-// X (K x T) -> rp x cp with zeros past it, and, given targets, at the columns left out.
-// W rows -> padded rows are the same copy without targets.
-__global__ void __launch_bounds__(256)
-    pad_kernel(const uint16_t* __restrict__ in, int64_t rows, int64_t cols, int64_t rp, int64_t cp,
-               const int64_t* __restrict__ target, int64_t V, uint16_t* __restrict__ out) {
-  const int64_t chunks = cp / 8, total = rp * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks, c = i % chunks * 8;
-    uint32_t h[8];
+struct TokenArgs {  // of the tokens, padded to a whole number of 64
+  int* y;           // target, -1 where left out
+  float* lse;
+  float* g;         // g times 2^14 over the largest
+  float* back;      // one number: what brings a sum of P back
+};
+
+// One workgroup: the largest |g| of the tokens that count, then all g over it, times 2^14.  A mean's
+// equal g become 2^14, so that the entries of P at the targets, just below 2^14 in size, lie where
+// 16-bit numbers are densest for their size.
+__device__ __forceinline__ void prepare_tokens(const int64_t* __restrict__ target,
+                                               const float* __restrict__ lse,
+                                               const float* __restrict__ gout, int64_t V, int64_t T,
+                                               int64_t Tp, const TokenArgs& out) {
+  __shared__ float part[4];
+  float top = 0.f;
+#pragma unroll 4
+  for (int64_t t = threadIdx.x; t < T; t += 256)
+    if (target[t] >= 0 && target[t] < V) top = fmaxf(top, fabsf(gout[t]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      bool take = r < rows && c + e < cols;
-      if (take && target) take = target[c + e] >= 0 && target[c + e] < V;
-      h[e] = take ? in[r * cols + c + e] : 0u;
-    }
-    *reinterpret_cast<u32x4_t*>(out + r * cp + c) =
-        u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, part[i]);
+  const bool scaled = top > 0.f && top < INFINITY;
+  if (threadIdx.x == 0) *out.back = scaled ? top * 0x1p-14f : 1.f;
+#pragma unroll 4
+  for (int64_t t = threadIdx.x; t < Tp; t += 256) {
+    const bool live = t < T && target[t] >= 0 && target[t] < V;
+    out.y[t] = live ? (int)target[t] : -1;
+    out.lse[t] = live ? lse[t] : 0.f;
+    out.g[t] = !live ? 0.f : scaled ? gout[t] / top * 0x1p14f : gout[t];
   }
+}
+
+struct PadArgs {
+  const uint16_t* in;  // rows x cols
+  int64_t rows, cols;
+  uint16_t* out;       // rp x cp, zeros past the input
+  int64_t rp, cp;
+  // the gradient's copy of X: zeros at the columns of tokens left out, and the last workgroup
+  // prepares the tokens
+  const int64_t* target;
+  const float *lse, *gout;
+  int64_t V;
+  TokenArgs tok;
+};
+
+// A thread keeps its eight columns and walks down the rows.
+template <bool TOKENS>
+__global__ void __launch_bounds__(256) pad_kernel(PadArgs p) {
+  const int64_t blocks = gridDim.x - (TOKENS ? 1 : 0);
+  if (TOKENS && blockIdx.x == blocks) {
+    prepare_tokens(p.target, p.lse, p.gout, p.V, p.cols, p.cp, p.tok);
+    return;
+  }
+  const int64_t chunks = p.cp / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t stride = blocks * 256 / chunks, c = i % chunks * 8;
+  if (i / chunks >= stride) return;
+  uint32_t keep[4];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    bool take = c + e < p.cols;
+    if (TOKENS && take) take = p.target[c + e] >= 0 && p.target[c + e] < p.V;
+    const uint32_t half = take ? 0xFFFFu << (16 * (e & 1)) : 0u;
+    keep[e / 2] = e & 1 ? keep[e / 2] | half : half;
+  }
+  const bool whole = p.cols % 8 == 0;
+#pragma unroll 4
+  for (int64_t r = i / chunks; r < p.rp; r += stride) {
+    u32x4_t v{0, 0, 0, 0};
+    if (r < p.rows) {
+      const uint16_t* x = p.in + r * p.cols + c;
+      if (whole) {
+        if (c < p.cols) v = *reinterpret_cast<const u32x4_t*>(x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < p.cols) v[e / 2] |= (uint32_t)x[e] << (16 * (e & 1));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] &= keep[e];
+    *reinterpret_cast<u32x4_t*>(p.out + r * p.cp + c) = v;
+  }
+}
+
+// A chunk to a thread until two workgroups to a unit, more rows a thread from there, since each
+// thread reads its columns' targets first (4096 x 2048: 17 us with 512 workgroups, 23 with 2048);
+// and no fewer threads than a row has chunks.
+template <bool TOKENS>
+hipError_t launch_pad(const PadArgs& p, hipStream_t s) {
+  const int64_t chunks = p.cp / 8, least = (chunks + 255) / 256;
+  int64_t blocks = (p.rp * chunks + 255) / 256;
+  if (blocks > 512) blocks = 512;
+  if (blocks < least) blocks = least;
+  if (p.rp * chunks > 0 || TOKENS)
+    pad_kernel<TOKENS><<<(unsigned)(blocks + (TOKENS ? 1 : 0)), 256, 0, s>>>(p);
+  return hipGetLastError();
 }
 
 // The products' tiles.  256 x 256 is the fastest on many large tiles; of 128 x 128 two fit a unit,
@@ -216,42 +297,7 @@ struct LossLayout {
   }
 };
 
-unsigned pad_grid(int64_t chunks) { return stride_grid(chunks, 256); }
-
 // ---- gradient --------------------------------------------------------------------------
-
-struct TokenArgs {  // of the tokens, padded to a whole number of 64
-  int* y;           // target, -1 where left out
-  float* lse;
-  float* g;         // g times 2^14 over the largest
-  float* back;      // one number: what brings a sum of P back
-};
-
-// One workgroup: the largest |g| of the tokens that count, then all g over it, times 2^14.  A mean's
-// equal g become 2^14, so that the entries of P at the targets, just below 2^14 in size, lie where
-// 16-bit numbers are densest for their size.
-__global__ void __launch_bounds__(1024)
-    tokens_kernel(const int64_t* __restrict__ target, const float* __restrict__ lse,
-                  const float* __restrict__ gout, int64_t V, int64_t T, int64_t Tp, TokenArgs out) {
-  __shared__ float part[16];
-  float top = 0.f;
-  for (int64_t t = threadIdx.x; t < T; t += 1024)
-    if (target[t] >= 0 && target[t] < V) top = fmaxf(top, fabsf(gout[t]));
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, part[i]);
-  const bool scaled = top > 0.f && top < INFINITY;
-  if (threadIdx.x == 0) *out.back = scaled ? top * 0x1p-14f : 1.f;
-  for (int64_t t = threadIdx.x; t < Tp; t += 1024) {
-    const bool live = t < T && target[t] >= 0 && target[t] < V;
-    out.y[t] = live ? (int)target[t] : -1;
-    out.lse[t] = live ? lse[t] : 0.f;
-    out.g[t] = !live ? 0.f : scaled ? gout[t] / top * 0x1p14f : gout[t];
-  }
-}
 
 struct ProbArgs {
   GemmOperand w, x;  // w from the piece's first row on
@@ -311,19 +357,19 @@ struct GradXArgs {
 };
 
 template <class G>
-__global__ void __launch_bounds__(G::kThreads) grad_x_kernel(GradXArgs p) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+__device__ __forceinline__ void grad_x_tile(const GradXArgs& p, int group, int split,
+                                            uint8_t* smem) {
   int tm, tn;
-  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  if (!p.map.tile_of(group, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
-  const int s0 = blockIdx.y * p.per, steps = min(p.per, p.steps - s0);
+  const int s0 = split * p.per, steps = min(p.per, p.steps - s0);
   GemmOperand w = p.w, q = p.q;
   w.p += (int64_t)s0 * kGemmStep * w.ld;
   q.p += (int64_t)s0 * kGemmStep * q.ld;
   typename G::Acc acc;
   G::clear(acc);
   if (steps > 0) G::run(w, q, m0, n0, steps, p.klen - (int64_t)s0 * kGemmStep, smem, acc);
-  float* out = p.sums + (int64_t)blockIdx.y * p.K * p.Tp;
+  float* out = p.sums + (int64_t)split * p.K * p.Tp;
   const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
 #pragma unroll
   for (int i = 0; i < G::kFM; ++i) {
@@ -358,10 +404,9 @@ struct GradWArgs {
 };
 
 template <class G, bool BF16>
-__global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+__device__ __forceinline__ void grad_w_tile(const GradWArgs& p, int group, uint8_t* smem) {
   int tm, tn;
-  if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
+  if (!p.map.tile_of(group, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
   typename G::Acc acc;
   G::clear(acc);
@@ -372,6 +417,33 @@ __global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) acc[i][j] *= back;
   G::template store16<BF16>(acc, m0, n0, smem, p.dW, p.K, p.rows, p.K);
+}
+
+template <class G>
+__global__ void __launch_bounds__(G::kThreads) grad_x_kernel(GradXArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  grad_x_tile<G>(p, blockIdx.x, blockIdx.y, smem);
+}
+template <class G, bool BF16>
+__global__ void __launch_bounds__(G::kThreads) grad_w_kernel(GradWArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  grad_w_tile<G, BF16>(p, blockIdx.x, smem);
+}
+
+// Both in one launch, dX's longer sums first: where each alone has few tiles, the units that one
+// leaves idle take the other's.
+struct GradArgs {
+  GradXArgs x;
+  GradWArgs w;
+  int groups_x, splits;  // workgroups for each split of dX
+};
+template <class GX, class GW, bool BF16>
+__global__ void __launch_bounds__(GX::kThreads) grad_kernel(GradArgs p) {
+  static_assert(GX::kThreads == GW::kThreads && GX::kLds == GW::kLds, "one launch for both");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int b = blockIdx.x, first_w = p.groups_x * p.splits;
+  if (b < first_w) grad_x_tile<GX>(p.x, b % p.groups_x, b / p.groups_x, smem);
+  else grad_w_tile<GW, BF16>(p.w, b - first_w, smem);
 }
 
 template <bool BF16>
@@ -453,15 +525,13 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
   const TokenArgs tok{reinterpret_cast<int*>(ws + L.tok_y), reinterpret_cast<float*>(ws + L.tok_lse),
                       reinterpret_cast<float*>(ws + L.tok_g), reinterpret_cast<float*>(ws + L.back)};
   hipError_t e;
-  tokens_kernel<<<1, 1024, 0, s>>>(target, lse, gout, V, T, L.Tp, tok);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  pad_kernel<<<pad_grid(L.Kp * L.Tp / 8), 256, 0, s>>>(X, K, T, L.Kp, L.Tp, target, V, Xp);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if ((e = launch_pad<true>(PadArgs{X, K, T, Xp, L.Kp, L.Tp, target, lse, gout, V, tok}, s)) !=
+      hipSuccess)
+    return e;
   const uint16_t* Wp = W;
   if (L.copy_w) {
     uint16_t* w = reinterpret_cast<uint16_t*>(ws + L.w);
-    pad_kernel<<<pad_grid(V * L.Kp / 8), 256, 0, s>>>(W, V, K, V, L.Kp, nullptr, 0, w);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_pad<false>(PadArgs{W, V, K, w, V, L.Kp}, s)) != hipSuccess) return e;
     Wp = w;
   }
   const int64_t ldw = L.Kp;
@@ -480,7 +550,7 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     e = with_tile<false, true, BF16, true>(pick_tile(rp, L.Tp, a.steps), [&](auto tag) {
       typedef typename decltype(tag)::type G;
       a.map = make_gemm_map((rp + G::kBM - 1) / G::kBM, (L.Tp + G::kBN - 1) / G::kBN);
-      return G::template launch<prob_kernel<G, BF16>>(a, a.map, 1, s);
+      return G::template launch<prob_kernel<G, BF16>>(a, a.map.groups(), 1, s);
     });
     if (e != hipSuccess) return e;
 
@@ -492,13 +562,6 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     b.K = K;
     b.back = tok.back;
     b.dW = dW + v0 * K;
-    e = with_tile<false, false, BF16, true>(pick_tile(rows, K, b.steps), [&](auto tag) {
-      typedef typename decltype(tag)::type G;
-      b.map = make_gemm_map((rows + G::kBM - 1) / G::kBM, (K + G::kBN - 1) / G::kBN);
-      return G::template launch<grad_w_kernel<G, BF16>>(b, b.map, 1, s);
-    });
-    if (e != hipSuccess) return e;
-
     GradXArgs c{};
     c.w = GemmOperand{Wp + v0 * ldw, ldw, L.Kp, 0};
     c.q = GemmOperand{P, L.Tp, L.Tp, 0};
@@ -509,10 +572,29 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     c.Tp = L.Tp;
     c.sums = sums;
     c.add = v0 > 0;
+    const int tile_w = pick_tile(rows, K, b.steps);
+    if (tile_w == kTile128 && L.tile_x == kTile128) {
+      typedef Gemm<2, 4, 2, 1, true, true, BF16, true, 2> GX;
+      typedef Gemm<2, 4, 2, 1, false, false, BF16, true, 2> GW;
+      GradArgs both{c, b, 0, L.splits};
+      both.x.map = make_gemm_map((K + 127) / 128, (L.Tp + 127) / 128);
+      both.w.map = make_gemm_map((rows + 127) / 128, (K + 127) / 128);
+      both.groups_x = both.x.map.groups();
+      e = GX::template launch<grad_kernel<GX, GW, BF16>>(
+          both, both.groups_x * L.splits + both.w.map.groups(), 1, s);
+      if (e != hipSuccess) return e;
+      continue;
+    }
     e = with_tile<true, true, BF16, true>(L.tile_x, [&](auto tag) {
       typedef typename decltype(tag)::type G;
       c.map = make_gemm_map((K + G::kBM - 1) / G::kBM, (L.Tp + G::kBN - 1) / G::kBN);
-      return G::template launch<grad_x_kernel<G>>(c, c.map, L.splits, s);
+      return G::template launch<grad_x_kernel<G>>(c, c.map.groups(), L.splits, s);
+    });
+    if (e != hipSuccess) return e;
+    e = with_tile<false, false, BF16, true>(tile_w, [&](auto tag) {
+      typedef typename decltype(tag)::type G;
+      b.map = make_gemm_map((rows + G::kBM - 1) / G::kBM, (K + G::kBN - 1) / G::kBN);
+      return G::template launch<grad_w_kernel<G, BF16>>(b, b.map.groups(), 1, s);
     });
     if (e != hipSuccess) return e;
   }
@@ -541,14 +623,12 @@ hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t 
   hipError_t e;
   if (L.copy_x) {
     uint16_t* c = reinterpret_cast<uint16_t*>(ws + L.x);
-    pad_kernel<<<pad_grid(L.Kp * L.Tp / 8), 256, 0, s>>>(x, K, T, L.Kp, L.Tp, nullptr, 0, c);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_pad<false>(PadArgs{x, K, T, c, L.Kp, L.Tp}, s)) != hipSuccess) return e;
     x = c;
   }
   if (L.copy_w) {
     uint16_t* c = reinterpret_cast<uint16_t*>(ws + L.w);
-    pad_kernel<<<pad_grid(V * L.Kp / 8), 256, 0, s>>>(w, V, K, V, L.Kp, nullptr, 0, c);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if ((e = launch_pad<false>(PadArgs{w, V, K, c, V, L.Kp}, s)) != hipSuccess) return e;
     w = c;
   }
   p.w = GemmOperand{w, L.Kp, V, 0};
@@ -563,7 +643,7 @@ hipError_t launch_xent(const void* W, const void* X, int dt, int64_t V, int64_t 
   const auto launch = [&](auto tag) {
     typedef typename decltype(tag)::type G;
     p.map = make_gemm_map((V + G::kBM - 1) / G::kBM, (T + G::kBN - 1) / G::kBN);
-    return G::template launch<stats_kernel<G>>(p, p.map, 1, s);
+    return G::template launch<stats_kernel<G>>(p, p.map.groups(), 1, s);
   };
   e = dt == kBF16 ? with_tile<false, true, true, false>(L.tile, launch)
                   : with_tile<false, true, false, false>(L.tile, launch);
