@@ -32,6 +32,10 @@ namespace {
 
 constexpr int kGemmStep = 64;  // k per step
 
+// Between a wave's writes to LDS and its other lanes' reads of them, both ways round: LDS serves a
+// wave's accesses in order, so only the compiler has to keep it.
+__device__ __forceinline__ void keep_lds_order() { asm volatile("" ::: "memory"); }
+
 // One operand: element (row, k) at p[row * ld + k], or at p[k * ld + row] if strided.  rows:
 // rows of the whole matrix from p on (loads past them read the last one).
 struct GemmOperand {
@@ -342,6 +346,7 @@ struct Gemm {
         }
       }
       if (whole) {
+        keep_lds_order();
 #pragma unroll
         for (int k = 0; k < 32 * kPieces / 64; ++k) {
           const int p = k * 64 + lane, r = p / kPieces, c = p % kPieces * 8;
@@ -349,6 +354,7 @@ struct Gemm {
           if (row + r < rows && col + c < cols)
             *reinterpret_cast<u32x4_t*>(out + (row + r) * ld + col + c) = v;
         }
+        keep_lds_order();
       }
     }
   }

@@ -23,6 +23,8 @@
 namespace nm {
 namespace {
 
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kNormBlocks = 1024;
 constexpr float kOrthScale = 256.f;
 
@@ -103,7 +105,6 @@ __global__ void __launch_bounds__(256)
       h[j] = (_Float16)x;
       l[j] = (_Float16)(x - (float)h[j]);
     }
-    typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
     *reinterpret_cast<half4_t*>(hi + 4 * i) = half4_t{h[0], h[1], h[2], h[3]};
     if constexpr (SPLIT) *reinterpret_cast<half4_t*>(lo + 4 * i) = half4_t{l[0], l[1], l[2], l[3]};
   }
@@ -120,14 +121,13 @@ struct OrthArgs {
   const float* rho;            // the first step's factor, else null
   const _Float16 *from_hi, *from_lo;  // square: A; update: the X before
   _Float16 *hi, *lo;           // result (lo only with two parts)
-  uint32_t* rest;              // one part: what hi lacks of X, four fp8 numbers a word
+  uint8_t* rest;               // one part: what hi lacks of X in fp8
   bool from_rest;              // whether the X before has any
   void* out;                   // the last update: the caller's result (R x K), else null
   int out_dt;
   int64_t R, K;
 };
 
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float4_t widen(half4_t h) {
   return float4_t{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
@@ -154,113 +154,195 @@ __device__ __forceinline__ float4_t unpack_rest(uint32_t w) {
 #endif
 }
 
-// What the epilogue reads of A (square) or of the X before (update) at four columns of a row.
-template <bool SPLIT>
-struct OrthBefore {
-  half4_t hi;
-  half4_t lo;     // two parts
-  uint32_t rest;  // one part
+// The epilogue works on 32 rows of a wave's part of the tile at a time, which pass through LDS in
+// both directions, so that device memory sees 16-byte pieces of whole lines: as the lanes hold
+// them, 8 bytes in each of 32 rows, they take four times the requests (4096 x 11008, one update:
+// 445 us so, MEASURED staged).
+template <class G, int KIND, bool SPLIT>
+struct OrthEpilogue {
+  static constexpr int kFN = G::kFN, kCols = 32 * kFN;
+  static constexpr bool kReads = KIND != kGram, kMirrors = KIND != kUpdate;
+  static constexpr bool kRest = KIND == kUpdate && !SPLIT;
+  static constexpr bool kSecond = SPLIT || kRest;         // a second plane: lo or rest
+  static constexpr int kSecondBytes = SPLIT ? 2 : 1;      // of an entry of it
+  static constexpr int kPieces = 2 * kFN, kSecondPieces = kSecondBytes * kFN;  // a lane
+  static constexpr int kPitch = 2 * kCols + 16, kSecondPitch = kSecondBytes * kCols + 16;
+  static constexpr int kTurned = 64 + 16;                 // pitch of 32 rows of a column
+  static constexpr int kSecondAt = 32 * kPitch;
+  static constexpr int kTurnedAt = kSecondAt + (kSecond ? 32 * kSecondPitch : 0);
+  static constexpr int kWaveBytes = kTurnedAt + (kMirrors ? (SPLIT ? 2 : 1) * kCols * kTurned : 0);
+  static_assert(G::kWaves * kWaveBytes <= G::kLds, "the waves' parts fit");
 
-  template <int KIND>
-  __device__ __forceinline__ void load(const OrthArgs& p, int64_t row, int64_t col) {
-    if (row >= p.rows || col >= p.cols) return;
-    const int64_t at = row * p.cols + col;
-    hi = *reinterpret_cast<const half4_t*>(p.from_hi + at);
-    if constexpr (SPLIT) lo = *reinterpret_cast<const half4_t*>(p.from_lo + at);
-    else if (KIND == kUpdate && p.from_rest) rest = p.rest[at / 4];
-  }
-  template <int KIND>
-  __device__ __forceinline__ float4_t value(const OrthArgs& p) const {
-    const float4_t x = widen(hi);
-    if constexpr (SPLIT) return x + widen(lo);
-    return KIND == kUpdate && p.from_rest ? x + unpack_rest(rest) : x;
-  }
-};
+  // What is read of A (square) or of the X before (update).
+  struct Before {
+    u32x4_t first[kPieces], second[kSecondPieces];
+  };
 
-template <int KIND, bool SPLIT>
-__device__ __forceinline__ void orth_store(const OrthArgs& p, float rho, bool mirror, int64_t row,
-                                           int64_t col, float4_t v, const OrthBefore<SPLIT>& before) {
-  if (row >= p.rows || col >= p.cols) return;
-  const int64_t at = row * p.cols + col;
-  float4_t r;
-  if constexpr (KIND == kGram) {
-    r = v * (rho * rho / kOrthScale);
-  } else {
-    const float4_t x = before.template value<KIND>(p);
-    if constexpr (KIND == kSquare) r = p.cb * x + (p.cc / kOrthScale) * v;
-    else r = rho * (p.ca * x + (1.f / kOrthScale) * v);
-  }
-  if (KIND == kUpdate && p.out) {
-    if (row >= p.R) return;
-    const int64_t o = row * p.K + col;
-    r *= 1.f / kOrthScale;
-    if (p.out_dt != kF32 && p.K % 4 == 0) {
-      uint32_t h[4];
+  const OrthArgs& p;
+  uint8_t* mine;
+  int lane;
+  int64_t row, col;  // of the wave's part
+  float rho;
+  bool mirror;
+
+  // f(k, row, column, 16-byte column) for each 16-byte piece of the lane in a plane of BYTES an
+  // entry that lies in the result.
+  template <int BYTES, typename F>
+  __device__ __forceinline__ void pieces(int i, int64_t rows, int64_t cols, F f) const {
+    constexpr int kRow = BYTES * kCols / 16;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = p.out_dt == kF16 ? f32_to_f16(r[i]) : f32_to_bf16(r[i]);
-      if (col < p.K)
-        *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.out) + o) =
-            u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
+    for (int k = 0; k < BYTES * kFN; ++k) {
+      const int at = k * 64 + lane, r = at / kRow, c = at % kRow;
+      if (row + 32 * i + r < rows && col + c * (16 / BYTES) < cols)
+        f(k, row + 32 * i + r, col + c * (16 / BYTES), r, 16 * c);
+    }
+  }
+
+  __device__ __forceinline__ void load(int i, Before& b) const {
+    if constexpr (kReads) {
+      pieces<2>(i, p.rows, p.cols, [&](int k, int64_t r, int64_t c, int, int) {
+        b.first[k] = *reinterpret_cast<const u32x4_t*>(p.from_hi + r * p.cols + c);
+      });
+      if constexpr (SPLIT)
+        pieces<2>(i, p.rows, p.cols, [&](int k, int64_t r, int64_t c, int, int) {
+          b.second[k] = *reinterpret_cast<const u32x4_t*>(p.from_lo + r * p.cols + c);
+        });
+      else if constexpr (kRest)
+        if (p.from_rest)
+          pieces<1>(i, p.rows, p.cols, [&](int k, int64_t r, int64_t c, int, int) {
+            b.second[k] = *reinterpret_cast<const u32x4_t*>(p.rest + r * p.cols + c);
+          });
+    }
+  }
+
+  __device__ __forceinline__ void store(int i, const typename G::Acc& acc, const Before& b) const {
+    uint8_t* const first = mine;
+    uint8_t* const second = mine + kSecondAt;
+    uint8_t* const turned = mine + kTurnedAt;
+    if constexpr (kReads) {
+      pieces<2>(i, p.rows, p.cols, [&](int k, int64_t, int64_t, int r, int c) {
+        *reinterpret_cast<u32x4_t*>(first + r * kPitch + c) = b.first[k];
+      });
+      if constexpr (kSecond)
+        pieces<kSecondBytes>(i, p.rows, p.cols, [&](int k, int64_t, int64_t, int r, int c) {
+          *reinterpret_cast<u32x4_t*>(second + r * kSecondPitch + c) = b.second[k];
+        });
+    }
+    keep_lds_order();
+    const bool last = KIND == kUpdate && p.out;
+    const bool staged = !last || (p.out_dt != kF32 && p.K % 8 == 0);
+#pragma unroll
+    for (int q = 0; q < 4 * kFN; ++q) {
+      const float4_t v = G::quad(acc, i, q / 4, q % 4);
+      const int r = lane & 31, c = 32 * (q / 4) + 8 * (q % 4) + 4 * (lane >> 5);
+      half4_t* const at = reinterpret_cast<half4_t*>(first + r * kPitch + 2 * c);
+      uint8_t* const at2 = second + r * kSecondPitch + kSecondBytes * c;
+      float4_t y;
+      if constexpr (KIND == kGram) {
+        y = v * (rho * rho / kOrthScale);
+      } else {
+        float4_t x = widen(*at);
+        if constexpr (SPLIT) x += widen(*reinterpret_cast<const half4_t*>(at2));
+        else if (kRest && p.from_rest) x += unpack_rest(*reinterpret_cast<const uint32_t*>(at2));
+        if constexpr (KIND == kSquare) y = p.cb * x + (p.cc / kOrthScale) * v;
+        else y = rho * (p.ca * x + (1.f / kOrthScale) * v);
+      }
+      if (last) {
+        y *= 1.f / kOrthScale;
+        if (staged) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = p.out_dt == kF16 ? f32_to_f16(y[e]) : f32_to_bf16(y[e]);
+          *reinterpret_cast<u32x2_t*>(at) = u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
+          continue;
+        }
+        const int64_t to_row = row + 32 * i + r, to = to_row * p.K + col + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (to_row >= p.R || col + c + e >= p.K) continue;
+          if (p.out_dt == kF32) store_from_f32<kF32>(p.out, to + e, y[e]);
+          else if (p.out_dt == kF16) store_from_f32<kF16>(p.out, to + e, y[e]);
+          else store_from_f32<kBF16>(p.out, to + e, y[e]);
+        }
+        continue;
+      }
+      half4_t h, l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = (_Float16)y[e];
+        l[e] = (_Float16)(y[e] - (float)h[e]);
+      }
+      *at = h;
+      if constexpr (SPLIT) *reinterpret_cast<half4_t*>(at2) = l;
+      else if constexpr (kRest) *reinterpret_cast<uint32_t*>(at2) = pack_rest(y - widen(h));
+      if (kMirrors && mirror) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          *reinterpret_cast<_Float16*>(turned + (c + e) * kTurned + 2 * r) = h[e];
+          if constexpr (SPLIT)
+            *reinterpret_cast<_Float16*>(turned + (kCols + c + e) * kTurned + 2 * r) = l[e];
+        }
+      }
+    }
+    keep_lds_order();
+    if (!staged) return;
+    if (last) {
+      pieces<2>(i, p.R, p.K, [&](int, int64_t r, int64_t c, int lr, int lc) {
+        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + r * p.K + c) =
+            *reinterpret_cast<const u32x4_t*>(first + lr * kPitch + lc);
+      });
       return;
     }
+    pieces<2>(i, p.rows, p.cols, [&](int, int64_t r, int64_t c, int lr, int lc) {
+      *reinterpret_cast<u32x4_t*>(p.hi + r * p.cols + c) =
+          *reinterpret_cast<const u32x4_t*>(first + lr * kPitch + lc);
+    });
+    if constexpr (kSecond)
+      pieces<kSecondBytes>(i, p.rows, p.cols, [&](int, int64_t r, int64_t c, int lr, int lc) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(second + lr * kSecondPitch + lc);
+        if constexpr (SPLIT) *reinterpret_cast<u32x4_t*>(p.lo + r * p.cols + c) = v;
+        else *reinterpret_cast<u32x4_t*>(p.rest + r * p.cols + c) = v;
+      });
+    if (kMirrors && mirror) {  // the same numbers above the diagonal, 32 of a row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (col + i >= p.K) continue;
-      if (p.out_dt == kF32) store_from_f32<kF32>(p.out, o + i, r[i]);
-      else if (p.out_dt == kF16) store_from_f32<kF16>(p.out, o + i, r[i]);
-      else store_from_f32<kBF16>(p.out, o + i, r[i]);
+      for (int k = 0; k < kPieces; ++k) {
+        const int c = (k * 64 + lane) / 4, r = (k * 64 + lane) % 4 * 8;
+        if (col + c >= p.cols || row + 32 * i + r >= p.rows) continue;
+        const int64_t to = (col + c) * p.cols + row + 32 * i + r;
+        *reinterpret_cast<u32x4_t*>(p.hi + to) =
+            *reinterpret_cast<const u32x4_t*>(turned + c * kTurned + 2 * r);
+        if constexpr (SPLIT)
+          *reinterpret_cast<u32x4_t*>(p.lo + to) =
+              *reinterpret_cast<const u32x4_t*>(turned + (kCols + c) * kTurned + 2 * r);
+      }
     }
-    return;
   }
-  half4_t h, l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = (_Float16)r[i];
-    l[i] = (_Float16)(r[i] - (float)h[i]);
-  }
-  *reinterpret_cast<half4_t*>(p.hi + at) = h;
-  if constexpr (SPLIT) *reinterpret_cast<half4_t*>(p.lo + at) = l;
-  else if (KIND == kUpdate) p.rest[at / 4] = pack_rest(r - widen(h));
-  if (KIND != kUpdate && mirror) {  // the same numbers above the diagonal, 32 lanes a row
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p.hi[(col + i) * p.cols + row] = h[i];
-      if constexpr (SPLIT) p.lo[(col + i) * p.cols + row] = l[i];
-    }
-  }
-}
+};
 
 template <class G, int KIND, bool SPLIT>
 __global__ void __launch_bounds__(G::kThreads) orth_kernel(OrthArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  typedef OrthEpilogue<G, KIND, SPLIT> Epilogue;
   int tm, tn;
   if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
-  const int64_t row0 = G::row0(m0), col0 = G::col0(n0);
-  const float rho = p.rho ? *p.rho : 1.f;
-  constexpr int kQuads = 4 * G::kFN;  // of a row of fragments
-  OrthBefore<SPLIT> before[kQuads];
-  auto load_row = [&](int i) {
-    if constexpr (KIND != kGram) {
-#pragma unroll
-      for (int q = 0; q < kQuads; ++q)
-        before[q].template load<KIND>(p, row0 + 32 * i, col0 + 32 * (q / 4) + 8 * (q % 4));
-    }
-  };
-  // A small tile's epilogue reads come ahead of its few steps, a large one's a row of fragments
-  // at a time: one by one, between stores that might alias, each would be waited for.
+  const int wave = threadIdx.x >> 6;
+  const Epilogue epilogue{p, smem + wave * Epilogue::kWaveBytes, (int)threadIdx.x & 63,
+                          m0 + wave / G::kWN * 32 * G::kFM, n0 + wave % G::kWN * 32 * G::kFN,
+                          p.rho ? *p.rho : 1.f, tm != tn};
+  // A small tile's epilogue reads come ahead of its few steps, a large one's 32 rows ahead.
   constexpr bool kEarly = G::kFM == 1;
-  if constexpr (kEarly) load_row(0);
+  typename Epilogue::Before before[2];
+  if constexpr (kEarly) epilogue.load(0, before[0]);
   typename G::Acc acc;
   G::clear(acc);
   G::run(p.a, p.b, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+  if constexpr (!kEarly) epilogue.load(0, before[0]);
 #pragma unroll
   for (int i = 0; i < G::kFM; ++i) {
-    if constexpr (!kEarly) load_row(i);
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q)
-      orth_store<KIND, SPLIT>(p, rho, tm != tn, row0 + 32 * i, col0 + 32 * (q / 4) + 8 * (q % 4),
-                              G::quad(acc, i, q / 4, q % 4), before[q]);
+    if (i + 1 < G::kFM) epilogue.load(i + 1, before[(i + 1) & 1]);
+    epilogue.store(i, acc, before[i & 1]);
+    keep_lds_order();
   }
 }
 
@@ -407,7 +489,7 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
     p.cols = L.kp;
     p.from_hi = from;
     p.from_lo = from + x_lo;
-    p.rest = reinterpret_cast<uint32_t*>(ws + L.rest);
+    p.rest = ws + L.rest;
     p.from_rest = i > 0;
     p.hi = x[(i + 1) & 1];
     p.lo = p.hi + x_lo;
