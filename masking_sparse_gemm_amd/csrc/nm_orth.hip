@@ -157,7 +157,7 @@ __device__ __forceinline__ float4_t unpack_rest(uint32_t w) {
 // The epilogue works on 32 rows of a wave's part of the tile at a time, which pass through LDS in
 // both directions, so that device memory sees 16-byte pieces of whole lines: as the lanes hold
 // them, 8 bytes in each of 32 rows, they take four times the requests (4096 x 11008, one update:
-// 445 us so, MEASURED staged).
+// 445 us so, 392 staged).
 template <class G, int KIND, bool SPLIT>
 struct OrthEpilogue {
   static constexpr int kFN = G::kFN, kCols = 32 * kFN;
@@ -349,16 +349,20 @@ __global__ void __launch_bounds__(G::kThreads) orth_kernel(OrthArgs p) {
 // Square tiles of four sizes; a launch takes the one with the smallest estimated time: rounds of
 // tiles over the 256 units, times the steps of 64 k at the time a step takes on a full device, plus
 // a fixed time (fill of the pipeline, epilogue).  Large tiles read less per product, small ones
-// fill the device; symmetric results have only the tiles on and below the diagonal, whose number is
-// what matters: 4096 x 4096 in 256s is 136 tiles for 256 units, in 192s 253.  Measured (us for
-// five steps, symmetric products in 256 / 192 / 128 / 64, the rest alike): 4096 x 11008 4606 /
-// 4387 / 5300 / 6125, 2048 x 8192 1850 / 1574 / 1215 / 1402, 1024 x 4096 806 / 668 / 450 / 282.
+// fill the device, and the smallest fits on a unit twice; symmetric results have only the tiles on
+// and below the diagonal, whose number is what matters: 4096 x 4096 in 256s is 136 tiles for 256
+// units, in 192s 253.  Measured (us for five steps with the symmetric products in 256 / 192 / 128
+// / 64, the update in its pick): 4096 x 11008 3566 / 3324 / 4002 / 4944, 2048 x 8192 1456 / 1106 /
+// 874 / 955, 1536 x 6144 1020 / 750 / 556 / 480, 1024 x 4096 680 / 482 / 345 / 241.  With the
+// update in each, the symmetric ones in their pick: 3315 / 3556 / 3818 / 4488, 868 / 931 / 1004 /
+// 1094, 583 / 552 / 656 / 638, 337 / 276 / 244 / 262.
 struct OrthTile {
-  int size;
+  int size, per_unit;
   float step_us, fixed_us;
 };
-constexpr OrthTile kOrthTiles[] = {{256, 1.85f, 11.f}, {192, 1.15f, 8.f}, {128, 0.5f, 4.5f}, {64, 0.25f, 3.5f}};
-constexpr OrthTile kOrthSplitTiles[] = {{128, 1.1f, 5.f}, {64, 0.45f, 4.f}};
+constexpr OrthTile kOrthTiles[] = {
+    {256, 1, 1.85f, 11.f}, {192, 1, 1.15f, 8.f}, {128, 1, 0.5f, 4.5f}, {64, 2, 0.25f, 3.5f}};
+constexpr OrthTile kOrthSplitTiles[] = {{128, 1, 1.1f, 5.f}, {64, 1, 0.45f, 4.f}};
 
 template <int N>
 int pick_orth_tile(const OrthTile (&tiles)[N], int64_t rows, int64_t cols, int steps, bool lower) {
@@ -367,7 +371,8 @@ int pick_orth_tile(const OrthTile (&tiles)[N], int64_t rows, int64_t cols, int s
   for (const OrthTile& t : tiles) {
     const int64_t m = (rows + t.size - 1) / t.size, n = (cols + t.size - 1) / t.size;
     const int64_t count = lower ? m * (m + 1) / 2 : m * n;
-    const double us = (double)((count + 255) / 256) * (steps * (double)t.step_us + t.fixed_us);
+    const double rounds = (double)((count * t.per_unit + 255) / 256) / t.per_unit;
+    const double us = (rounds < 1 ? 1 : rounds) * (steps * (double)t.step_us + t.fixed_us);
     if (us < least) {
       least = us;
       best = t.size;
@@ -396,7 +401,7 @@ hipError_t launch_orth_product(const OrthArgs& p, hipStream_t s) {
     if (tile == 256)
       return launch_orth_tile<Gemm<2, 4, 4, 2, AS, BS, false, true, 2>, KIND, false>(p, s);
     if (tile == 192)
-      return launch_orth_tile<Gemm<2, 2, 3, 3, AS, BS, false, true, 3>, KIND, false>(p, s);
+      return launch_orth_tile<Gemm<2, 6, 3, 1, AS, BS, false, true, 3>, KIND, false>(p, s);
     if (tile == 128)
       return launch_orth_tile<Gemm<2, 4, 2, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
     return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
