@@ -230,26 +230,59 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------------------
 // nm_matvec.  y[r, t] = sum over groups of s[r, g] * (sum over the group of q x).
 //
-// A code becomes a 16-bit float by bit patterns alone: 16 + u for the stored u = q + 8 (for
-// bf16 u goes to mantissa bits 3 .. 6 under the exponent of 16, for fp16 to bits 6 .. 9), and
-// the matrix cores take off the 24 again with a second instruction whose A operand is the
-// constant -24 at every stored place (for 2:4, under the same positions).  Products are exact,
-// sums fp32; the group's sum is scaled in fp32.
+// A code becomes the 16-bit float that it is, exactly, so the matrix cores' products are exact and
+// an infinite x gives what it gives in q x; sums are fp32; the group's sum is scaled in fp32.
 // ---------------------------------------------------------------------------------------
 
-// Four pairs of eight codes as 16-bit floats 16 + u: a shift and an and-or each.  The masks come
-// in registers (mask_of), for an instruction takes only one constant of 32 bits.
-template <bool BF16>
-__device__ __forceinline__ u32x4_t codes_to_float(uint32_t w, uint32_t mask, uint32_t sixteen) {
-  constexpr int kUp = BF16 ? 3 : 6;  // to the mantissa's places under the exponent of 16
-  return u32x4_t{((w << kUp) & mask) | sixteen,
-                 (kUp > 4 ? (w << (kUp - 4)) & mask : (w >> (4 - kUp)) & mask) | sixteen,
-                 ((w >> (8 - kUp)) & mask) | sixteen, ((w >> (12 - kUp)) & mask) | sixteen};
-}
 __device__ __forceinline__ uint32_t in_register(uint32_t c) {
   asm volatile("" : "+v"(c));
   return c;
 }
+
+// Eight codes as four pairs of 16-bit floats.
+template <bool BF16>
+struct Codes;
+
+// bf16: the stored u = q + 8 of a pair, masked where they stand, are subnormal fp16 numbers, u
+// 2^-24 or u 2^-20; one mixed-precision multiply-add each makes them q in fp32, whose upper halves
+// are bf16.  17 instructions a word.
+template <>
+struct Codes<true> {
+  uint32_t low = in_register(0x000F000Fu), high = in_register(0x00F000F0u);
+  float low_scale = __uint_as_float(in_register(0x4B800000u));   // 2^24
+  float high_scale = __uint_as_float(in_register(0x49800000u));  // 2^20
+  float minus8 = __uint_as_float(in_register(0xC1000000u));
+
+  __device__ __forceinline__ uint32_t pair(uint32_t u, float scale) const {
+    float even, odd;
+    asm("v_fma_mix_f32 %0, %1, %2, %3 op_sel_hi:[1,0,0]" : "=v"(even) : "v"(u), "v"(scale), "v"(minus8));
+    asm("v_fma_mix_f32 %0, %1, %2, %3 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+        : "=v"(odd) : "v"(u), "v"(scale), "v"(minus8));
+    return __builtin_amdgcn_perm(__float_as_uint(odd), __float_as_uint(even), 0x07060302u);
+  }
+  __device__ __forceinline__ u32x4_t floats(uint32_t w) const {
+    const uint32_t v = w >> 8;
+    return u32x4_t{pair(w & low, low_scale), pair(w & high, high_scale), pair(v & low, low_scale),
+                   pair(v & high, high_scale)};
+  }
+};
+
+// fp16: u goes to the mantissa's upper bits under the exponent of 16, and 24 is taken off again.
+// 12 instructions a word.
+template <>
+struct Codes<false> {
+  uint32_t mask = in_register(0x03C003C0u), sixteen = in_register(0x4C004C00u);
+  uint32_t minus24 = in_register(0xCE00CE00u);
+
+  __device__ __forceinline__ uint32_t pair(uint32_t u) const {
+    typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, (u & mask) | sixteen) +
+                                            __builtin_bit_cast(half2_t, minus24));
+  }
+  __device__ __forceinline__ u32x4_t floats(uint32_t w) const {
+    return u32x4_t{pair(w << 6), pair(w << 2), pair(w >> 2), pair(w >> 6)};
+  }
+};
 
 template <bool BF16>
 __device__ __forceinline__ float4_t mfma_dense(const u32x4_t& a, const u32x4_t& b,
@@ -326,10 +359,8 @@ struct CodeBlock {
   // total[t] += this block times the B operands operand(w, half, t): for step w 32 rows of X (of
   // the two halves of 64, for 2:4), 16 columns.
   template <bool BF16, int NT, typename F>
-  __device__ __forceinline__ void multiply(float4_t (&total)[NT], uint32_t mask, uint32_t sixteen,
+  __device__ __forceinline__ void multiply(float4_t (&total)[NT], const Codes<BF16>& convert,
                                            F&& operand) const {
-    constexpr uint32_t off = BF16 ? 0xC1C0C1C0u : 0xCE00CE00u;  // -24, -24
-    const u32x4_t offs{off, off, off, off};
     float4_t acc[NT];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -337,17 +368,15 @@ struct CodeBlock {
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[t] = float4_t{0.f, 0.f, 0.f, 0.f};
       }
-      const u32x4_t wf = codes_to_float<BF16>(codes[w], mask, sixteen);
+      const u32x4_t wf = convert.floats(codes[w]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const u32x4_t b0 = operand(w, 0, t);
         if constexpr (SPARSE) {
           const u32x4_t b1 = operand(w, 1, t);
           acc[t] = mfma_sparse<BF16>(wf, b0, b1, acc[t], meta[w]);
-          acc[t] = mfma_sparse<BF16>(offs, b0, b1, acc[t], meta[w]);
         } else {
           acc[t] = mfma_dense<BF16>(wf, b0, acc[t]);
-          acc[t] = mfma_dense<BF16>(offs, b0, acc[t]);
         }
       }
       if (((32 * (w + 1)) & ((1 << LOG_GROUP) - 1)) == 0) {
@@ -372,8 +401,7 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & 63, j = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t mask = in_register(BF16 ? 0x00780078u : 0x03C003C0u);
-  const uint32_t sixteen = in_register(BF16 ? 0x41804180u : 0x4C004C00u);
+  const Codes<BF16> convert;
   const int64_t g = blockIdx.x;
   CodeBlock<SPARSE, LOG_GROUP> next;
   if (wave < a.S) next.load(a, g, wave, lane);
@@ -397,7 +425,7 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
     const CodeBlock<SPARSE, LOG_GROUP> cur = next;
     if (s + WAVES < a.S) next.load(a, g, s + WAVES, lane);
     const u32x4_t* x = reinterpret_cast<const u32x4_t*>(smem) + 4 * s * kEights + j;
-    cur.template multiply<BF16, 1>(total, mask, sixteen, [&](int w, int half, int) {
+    cur.template multiply<BF16, 1>(total, convert, [&](int w, int half, int) {
       return x[w * kEights + 4 * half];
     });
   }
@@ -431,8 +459,7 @@ __global__ void __launch_bounds__(64 * kSliceWaves) matvec_slice_kernel(MatvecAr
   const int lane = threadIdx.x & 63, n = lane & 15, j = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int along = 1 << a.log_along, first = wave & (along - 1);
-  const uint32_t mask = in_register(BF16 ? 0x00780078u : 0x03C003C0u);
-  const uint32_t sixteen = in_register(BF16 ? 0x41804180u : 0x4C004C00u);
+  const Codes<BF16> convert;
   const int64_t last = (a.R + 15) / 16 - 1;
   const int64_t mine = (int64_t)blockIdx.x * (kSliceWaves >> a.log_along) + (wave >> a.log_along);
   const int64_t g = mine < last ? mine : last;  // rows past the matrix: dropped below
@@ -525,7 +552,7 @@ __global__ void __launch_bounds__(64 * kSliceWaves) matvec_slice_kernel(MatvecAr
     const Block cur = next;
     next.load(a, g, s0 + min(s + along, blocks - 1), lane);
     const uint8_t* x = smem + s * kBlockRows * 32;
-    cur.template multiply<BF16, NT>(total, mask, sixteen, [&](int w, int half, int t) {
+    cur.template multiply<BF16, NT>(total, convert, [&](int w, int half, int t) {
       return *reinterpret_cast<const u32x4_t*>(x + t * tile_bytes +
                                                (w * (kBlockRows / 128) + half) * 1024 + lane * 16);
     });

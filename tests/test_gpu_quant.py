@@ -212,6 +212,28 @@ def test_matvec_columns_do_not_mix():
         assert y[:, 1].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_matvec_infinities_and_the_largest_numbers(dtype, T):
+    """Codes multiply as what they are: an infinity in X gives the infinities and NaN of the plain
+    product, and numbers whose products with the codes are finite give finite sums."""
+    R, K, group = 40, 256, 64
+    gen = torch.Generator().manual_seed(5)
+    q = torch.randint(-7, 8, (R, K), generator=gen)
+    q[:, ::group] = 7  # every group's scale is 1
+    q[0] = 0
+    codes, scales = nm.quantize(q.to(dtype).cuda(), group)
+    x = torch.zeros(K, T, dtype=dtype)
+    x[5] = torch.finfo(dtype).max / 16
+    y = nm.matvec(codes, scales, x.cuda(), group, rows=R, out_dtype=torch.float32).cpu()
+    assert torch.equal(y.double(), q.double() @ x.double())
+    x[5] = float("inf")
+    y = nm.matvec(codes, scales, x.cuda(), group, rows=R, out_dtype=torch.float32).cpu()
+    want = q.double()[:, 5:6] * torch.full((1, T), float("inf"), dtype=torch.float64)
+    assert torch.equal(y.double().nan_to_num(1.0), want.nan_to_num(1.0))
+    assert torch.equal(y.isnan(), want.isnan())
+
+
 def test_matvec_is_repeatable_and_uses_the_current_stream():
     R, K, T = 1000, 4096, 5
     w = weights(R, K, torch.bfloat16).cuda()
