@@ -14,7 +14,7 @@
 // as many as fit for the small ones, whose whole sum may then be in flight at once.  A wave owns
 // 32 FM x 32 FN of the tile and uses v_mfma_f32_32x32x16.  LDS layouts of a stage, both free of
 // bank conflicts for their reads:
-//   k contiguous: 128 bytes a row of the tile, 16-byte chunk c at c ^ (row & 7); a fragment is
+//   k contiguous: 128 bytes a row of the tile, 16-byte chunk c at c ^ (row / 2 & 7); a fragment is
 //     one 16-byte read per lane;
 //   strided: a row of the tile's columns for each k, 32-byte pair p at p ^ 2 (k & 3); a
 //     fragment is two transposing reads (ds_read_b64_tr_b16).
@@ -99,6 +99,7 @@ struct Gemm {
   static constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
   static constexpr int kLoads = PARTS * (kALoads + kBLoads);  // of a wave and step
   static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "whole loads");
+  static constexpr int kProducts = FM * FN * (2 * PARTS - 1);  // of a wave and 16 k
   static_assert(kLds <= 160 * 1024, "LDS");
   static_assert(STAGES >= 2 && (STAGES - 1) * kLoads <= 63, "vmcnt");
 
@@ -111,7 +112,7 @@ struct Gemm {
                                                     int64_t left, int64_t kleft) {
     const int slot = (j * kWaves + wave) * 64 + lane;  // 16-byte slot of the tile
     if constexpr (!STRIDED) {
-      const int r = slot >> 3, c = (slot & 7) ^ (r & 7);
+      const int r = slot >> 3, c = (slot & 7) ^ ((r >> 1) & 7);
       const int64_t row = r < left ? r : left - 1;
       return (uint32_t)(row * ld * 2 + 16 * c);
     } else {
@@ -132,7 +133,7 @@ struct Gemm {
     const int q = lane >> 5;
     if constexpr (!STRIDED) {
       const int r = w0 + 32 * f + (lane & 31);
-      return *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((2 * kk + q) ^ (r & 7)) << 4));
+      return *reinterpret_cast<const u32x4_t*>(tile + r * 128 + (((2 * kk + q) ^ ((r >> 1) & 7)) << 4));
     } else {
       [[maybe_unused]] constexpr int kPairs = ROWS / 16;
       const int l16 = lane & 15, half = (lane >> 4) & 1;
@@ -229,6 +230,33 @@ struct Gemm {
           f.b[q][j] = fragment<BS, kBN>(tb + q * kBBytes, wn * 32 * FN, j, kk, lane);
       }
     };
+    // Reads the fragments due after product m of kProducts: those that the next products need first
+    // come first, and the last is read two products ahead where there are enough.
+    auto read_after = [&](Fragments& f, int stage, int kk, int m) {
+      constexpr int kAll = PARTS * (FM + FN), kOver = kProducts > kAll ? kProducts - 2 : kProducts;
+      const uint8_t* ta = smem + stage * kStage;
+      const uint8_t* tb = ta + PARTS * kABytes;
+#pragma unroll
+      for (int x = 0; x < kAll; ++x) {
+        if (x * kOver / kAll != m) continue;
+        const int q = x / (FM + FN), y = x % (FM + FN);  // a[0], all of b, the rest of a
+        if (y > 0 && y <= FN)
+          f.b[q][(y - 1) % FN] = fragment<BS, kBN>(tb + q * kBBytes, wn * 32 * FN, y - 1, kk, lane);
+        else
+          f.a[q][y == 0 ? 0 : (y - FN) % FM] =
+              fragment<AS, kBM>(ta + q * kABytes, wm * 32 * FM, y == 0 ? 0 : y - FN, kk, lane);
+      }
+    };
+    auto multiply_and_read = [&](const Fragments& f, Fragments& next, int stage, int kk) {
+#pragma unroll
+      for (int m = 0; m < kProducts; ++m) {
+        const int q = m / (FM * FN), i = m / FN % FM, j = m % FN;
+        acc[i][j] = mfma(f.a[q >> 1][i], f.b[q & 1][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        read_after(next, stage, kk, m);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
     auto multiply = [&](const Fragments& f) {
 #pragma unroll
       for (int q = 0; q < 2 * PARTS - 1; ++q)  // hi hi, hi lo, lo hi
@@ -255,29 +283,37 @@ struct Gemm {
     Fragments f[2];
     read(f[0], 0, 0);
     int stage = 0;
-    for (int s = 0; s < steps; ++s) {
+    // inner: a step with at least STAGES + 1 more behind it, which needs no tests.
+    auto step = [&](int s, auto inner) {
+      constexpr bool kInner = decltype(inner)::value;
       const int next = stage + 1 == STAGES ? 0 : stage + 1;
       // the next 16 k's fragments are read while the matrix cores work on these
 #pragma unroll
       for (int kk = 0; kk < 3; ++kk) {
-        read(f[(kk + 1) & 1], stage, kk + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(f[kk & 1]);
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kProducts >= 3) {
+          multiply_and_read(f[kk & 1], f[(kk + 1) & 1], stage, kk + 1);
+        } else {
+          read(f[(kk + 1) & 1], stage, kk + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(f[kk & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      const bool more = s + STAGES < steps;
-      if (s + 1 < steps) {
+      if (kInner || s + 1 < steps) {
         // step s + 1 has landed; no wave reads this step's stage any more
-        meet(std::integral_constant<int, STAGES - 2>{}, s + STAGES <= steps);
+        meet(std::integral_constant<int, STAGES - 2>{}, kInner || s + STAGES <= steps);
         read(f[0], next, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
       multiply(f[1]);
       __builtin_amdgcn_sched_barrier(0);
-      if (more) issue(s + STAGES, stage);  // in the shadow of the products just queued
+      if (kInner || s + STAGES < steps) issue(s + STAGES, stage);  // behind the products just queued
       __builtin_amdgcn_sched_barrier(0);
       stage = next;
-    }
+    };
+    int s = 0;
+    for (; s < steps - STAGES - 1; ++s) step(s, std::true_type{});
+    for (; s < steps; ++s) step(s, std::false_type{});
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // smem may be reused
   }
 
