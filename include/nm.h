@@ -367,7 +367,7 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
  * dt is the type of X and of the scales, NM_F16 or NM_BF16; y_dt is dt or NM_F32.  Codes enter
  * the matrix cores exactly, sums are fp32, a group's sum is scaled in fp32 and Y is rounded once.
  * workspace: nm_matvec_workspace_bytes(R, K, T, meta != NULL) bytes of device memory (0 for
- * T = 1 and K <= 32768), whose contents do not matter. */
+ * T = 1 and K <= 32768, and for some small T), whose contents do not matter. */
 size_t nm_matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, int sparse);
 nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
                     int64_t K, int group, const void* X, int64_t T, nm_dtype dt, void* Y,

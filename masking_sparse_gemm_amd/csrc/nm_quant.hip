@@ -8,7 +8,7 @@
 // word w, the eight columns 32 w + 8 j .. + 7 of row r -- its share of the A operand of the
 // 16 x 16 matrix-core instruction for columns 32 w .. 32 w + 31.  Inside a word the even
 // columns lie in the low half and the odd ones in the high half, column pair p at bits 4 p and
-// 4 p + 16: one shift and one and-or turn a word into a pair of 16-bit floats.
+// 4 p + 16: a mask takes a pair out of a word, a code in each half.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,7 +23,9 @@ constexpr int kBlockCols = 128;       // stored columns of a block of codes
 
 // ---------------------------------------------------------------------------------------
 // nm_quantize: one wave per block of 16 rows x 128 columns; lane 16 j + r reads its 32
-// elements, the four lanes of a row share the group maxima by lane exchange.
+// elements, the four lanes of a row share the group maxima by lane exchange.  One pass, bound by
+// memory: 11008 x 2048 kept values of bf16 take 11.6 us (57 MB, 4.9 TB/s; a large copy reaches
+// 5.2), 768 x 768 4.3 us, which is a launch.
 // ---------------------------------------------------------------------------------------
 
 template <int DT>
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------------------
 // nm_dequantize: the same assignment of columns to lanes, s q rounded once to the scales' type.
+// Bound by memory: 11008 x 2048 values of bf16 in 11.6 us (57 MB, 4.9 TB/s).
 // ---------------------------------------------------------------------------------------
 template <bool BF16S, bool kBlocked, bool kWhole>
 __global__ void __launch_bounds__(256)
@@ -313,6 +316,8 @@ __device__ __forceinline__ float4_t mfma_sparse(const u32x4_t& a, const u32x4_t&
                                                     0, 0);
 }
 
+constexpr int kColumnPad = 64;  // bytes: four columns of X apart are on all banks of LDS
+
 struct MatvecArgs {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -391,11 +396,15 @@ struct CodeBlock {
   }
 };
 
-// One column.  A workgroup has 16 rows; its waves take the blocks of 128 stored columns in turn,
-// each with the next one's loads in flight, and add their sums in wave order at the end.  X lies
-// in LDS whole; every column of the instruction holds it, and only the first is kept.  Blocks
-// past the matrix's last columns hold code 0 against zeros of X, so there are no ends to treat.
-template <bool BF16, bool SPARSE, int LOG_GROUP, int WAVES, int YT>
+// Few columns, with X whole in LDS, a run of its rows for each column; FEW: more than one.  A
+// workgroup has 16 rows; its waves take the blocks of 128 stored columns in turn, each with the next
+// one's loads in flight, and add their sums in wave order at the end.  The instruction's columns
+// past the last hold the last again and are dropped.  Blocks past the matrix's last columns hold
+// code 0 against zeros of X, so there are no ends to treat.
+// Bound by the first loads' latency on small matrices, from there by the few loads that a unit keeps
+// in flight: one column 4096 x 4096 4.9 us (1.8 TB/s), 4096 x 11008 8.9 (2.7), 16384 x 12288
+// 27.3 (3.9); two columns of 4096 x 4096 4.7 us with the codes in cache.
+template <bool BF16, bool SPARSE, int LOG_GROUP, int WAVES, bool FEW, int YT>
 __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
   constexpr int kEights = SPARSE ? 8 : 4;  // eights of X's rows to a step
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -403,28 +412,45 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Codes<BF16> convert;
   const int64_t g = blockIdx.x;
+  const int T = FEW ? (int)a.T : 1;
   CodeBlock<SPARSE, LOG_GROUP> next;
   if (wave < a.S) next.load(a, g, wave, lane);
   const int chunks = a.S * 4 * kEights;  // X and the zeros after it, to whole blocks
-  for (int c = threadIdx.x; c < chunks; c += 64 * WAVES) {
-    const int64_t k = 8 * (int64_t)c;
+  const int pitch = 16 * chunks + kColumnPad;
+  const int64_t have = a.K * T;
+  for (int c = threadIdx.x; c < chunks * T; c += 64 * WAVES) {
+    const int64_t at = 8 * (int64_t)c;
     u32x4_t v;
-    if (k + 8 <= a.K) {
-      v = *reinterpret_cast<const u32x4_t*>(a.x + k);
+    if (at + 8 <= have) {
+      v = *reinterpret_cast<const u32x4_t*>(a.x + at);
     } else {
       uint32_t h[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = k + e < a.K ? a.x[k + e] : 0u;
+      for (int e = 0; e < 8; ++e) h[e] = at + e < have ? a.x[at + e] : 0u;
       v = u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
     }
-    reinterpret_cast<u32x4_t*>(smem)[c] = v;
+    if constexpr (FEW) {
+      int k = 8 * c / T, t = 8 * c - k * T;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        *reinterpret_cast<uint16_t*>(smem + t * pitch + 2 * k) = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+        if (++t == T) {
+          t = 0;
+          ++k;
+        }
+      }
+    } else {
+      reinterpret_cast<u32x4_t*>(smem)[c] = v;
+    }
   }
   __syncthreads();
   float4_t total[1] = {float4_t{0.f, 0.f, 0.f, 0.f}};
+  const int col = (lane & 15) < T ? lane & 15 : T - 1;
   for (int s = wave; s < a.S; s += WAVES) {
     const CodeBlock<SPARSE, LOG_GROUP> cur = next;
     if (s + WAVES < a.S) next.load(a, g, s + WAVES, lane);
-    const u32x4_t* x = reinterpret_cast<const u32x4_t*>(smem) + 4 * s * kEights + j;
+    const u32x4_t* x =
+        reinterpret_cast<const u32x4_t*>(smem + (FEW ? col * pitch : 0)) + 4 * s * kEights + j;
     cur.template multiply<BF16, 1>(total, convert, [&](int w, int half, int) {
       return x[w * kEights + 4 * half];
     });
@@ -433,12 +459,12 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
   float4_t* part = reinterpret_cast<float4_t*>(smem);
   part[wave * 64 + lane] = total[0];
   __syncthreads();
-  if (threadIdx.x < 16) {  // rows 4 j + i of column 0
-    const int row = threadIdx.x;
+  if ((int)threadIdx.x < 16 * T) {  // lane 16 j + t holds rows 4 j + i of column t
+    const int row = threadIdx.x / T, t = threadIdx.x - row * T;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) y += part[w * 64 + 16 * (row / 4)][row % 4];
-    if (16 * g + row < a.R) store_from_f32<YT>(a.y, 16 * g + row, y);
+    for (int w = 0; w < WAVES; ++w) y += part[w * 64 + 16 * (row / 4) + t][row % 4];
+    if (16 * g + row < a.R) store_from_f32<YT>(a.y, (16 * g + row) * T + t, y);
   }
 }
 
@@ -449,6 +475,9 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
 // The waves that share rows take the slice's blocks in turn and add their sums in wave order.
 // With more than one slice the sums go to the workspace, where join_slices_kernel adds them in
 // slice order.
+// Bound by laying out X, which every workgroup does for its slice, and by the launch of the second
+// kernel (3.8 us): 2:4 4096 x 11008 with 32 columns 13.2 us and the join, 5003 x 11007 with 5 columns
+// 14.2 us and the join, 16384 x 8192 with 32 columns 34.5 us in all (2.1 TB/s).
 constexpr int kSliceWaves = 8;
 
 template <bool BF16, bool SPARSE, int LOG_GROUP, int NT, int YT>
@@ -613,9 +642,22 @@ __global__ void __launch_bounds__(256)
     if (row + i < R) store_from_f32<YT>(y, (row + i) * T + col, total[i]);
 }
 
-constexpr int64_t kColumnLds = 64 << 10;  // most of it that a single column may take
-int64_t column_bytes(int64_t K) { return (K + 255) / 256 * 512; }
-bool one_column(int64_t K, int64_t T) { return T == 1 && column_bytes(K) <= kColumnLds; }
+// Bytes of LDS that X's columns take in matvec_kernel, 0 where slices of them are better.  Every
+// workgroup lays out all of X, at a cost of K T for each that a unit gets (two at a time where they
+// fit), so rows and columns are bounded together.  Measured, us, whole / slices: 4096 x 4096, 2
+// columns 4.7 / 10.0, 5 5.5 / 9.6, 8 6.4 / 7.1; 2:4 4096 x 11008, 5 columns 9.4 / 12.0; 2:4 11008 x
+// 4096, 7 columns 11.4 / 13.2, 8 12.2 / 9.5; 16384 x 8192, 2 columns 19.7 / 23.9, 3 20.5 / 21.7, 5
+// 34.5 / 21.8; 5003 x 11007, 2 columns 13.1 / 15.8, 4 21.1 / 15.6.
+constexpr int kFewColumns = 8;
+constexpr int64_t kFewLds = 128 << 10;
+int64_t column_lds(int64_t R, int64_t K, int64_t T) {
+  const int64_t column = std::max<int64_t>(1, (K + 255) / 256) * 512;
+  if (T == 1) return column <= 64 << 10 ? column : 0;
+  const int64_t groups = (R + 15) / 16, all = T * (column + kColumnPad);
+  if (T > kFewColumns || all > kFewLds) return 0;
+  const double rounds = all <= 80 << 10 ? std::max(1.0, groups / 256.0) : (double)((groups + 255) / 256);
+  return rounds * (double)(K * T) <= 80 << 10 ? all : 0;
+}
 
 // How several columns are cut.  Each workgroup reads X's rows of its slice, so rows are shared by
 // few waves where that leaves workgroups for all 256 units, and one slice is taken where X fits the
@@ -669,17 +711,34 @@ hipError_t launch_matvec_slices(const MatvecArgs& a, const MatvecPlan& p, hipStr
   return hipGetLastError();
 }
 
+// Eight waves to 16 rows fill the device where rows are many, sixteen where they are few.
+template <bool BF16, bool SPARSE, int LOG_GROUP, bool FEW, int YT>
+hipError_t launch_matvec_whole(const MatvecArgs& a, size_t lds, hipStream_t s) {
+  const unsigned groups = (unsigned)((a.R + 15) / 16);
+  const int waves = groups > 256 ? 8 : 16;
+  const auto kernel = waves == 8 ? matvec_kernel<BF16, SPARSE, LOG_GROUP, 8, FEW, YT>
+                                 : matvec_kernel<BF16, SPARSE, LOG_GROUP, 16, FEW, YT>;
+  if constexpr (FEW) {
+    static const hipError_t attr8 = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(matvec_kernel<BF16, SPARSE, LOG_GROUP, 8, true, YT>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewLds);
+    static const hipError_t attr16 = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(matvec_kernel<BF16, SPARSE, LOG_GROUP, 16, true, YT>),
+        hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFewLds);
+    if (attr8 != hipSuccess) return attr8;
+    if (attr16 != hipSuccess) return attr16;
+  }
+  kernel<<<groups, 64 * waves, lds, s>>>(a);
+  return hipGetLastError();
+}
+
 template <bool BF16, bool SPARSE, int LOG_GROUP, int YT>
 hipError_t launch_matvec_cols(const MatvecArgs& a, const MatvecPlan& p, hipStream_t s) {
-  if (one_column(a.K, a.T)) {
-    // eight waves to 16 rows fill the device where rows are many, sixteen where they are few
-    const size_t lds = std::max((size_t)column_bytes(a.K), (size_t)16 * 1024);
-    const unsigned groups = (unsigned)((a.R + 15) / 16);
-    if (groups > 256)
-      matvec_kernel<BF16, SPARSE, LOG_GROUP, 8, YT><<<groups, 512, lds, s>>>(a);
-    else
-      matvec_kernel<BF16, SPARSE, LOG_GROUP, 16, YT><<<groups, 1024, lds, s>>>(a);
-    return hipGetLastError();
+  const int64_t whole = column_lds(a.R, a.K, a.T);
+  if (whole) {
+    const size_t lds = std::max((size_t)whole, (size_t)16 * 1024);
+    return a.T == 1 ? launch_matvec_whole<BF16, SPARSE, LOG_GROUP, false, YT>(a, lds, s)
+                    : launch_matvec_whole<BF16, SPARSE, LOG_GROUP, true, YT>(a, lds, s);
   }
   return p.nt == 1 ? launch_matvec_slices<BF16, SPARSE, LOG_GROUP, 1, YT>(a, p, s)
                    : launch_matvec_slices<BF16, SPARSE, LOG_GROUP, 2, YT>(a, p, s);
@@ -761,7 +820,7 @@ hipError_t launch_dequantize(const void* codes, const void* scales, int scale_dt
 }
 
 size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse) {
-  return one_column(K, T) ? 0 : (size_t)MatvecPlan(R, K, T, sparse).bytes;
+  return column_lds(R, K, T) ? 0 : (size_t)MatvecPlan(R, K, T, sparse).bytes;
 }
 
 hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,

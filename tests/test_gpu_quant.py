@@ -140,13 +140,11 @@ def check_product(y, q, s, x, group, at=None):
     R, C = q.shape
     sr = s.double().repeat_interleave(group, 1)[:, :C]
     xd = x.double()
-    w, m = q.double() * sr, (q.double() + 8 + 16 + 24) * sr
+    w = q.double() * sr
     if at is not None:
-        K = x.shape[0]
-        w = torch.zeros(R, K, dtype=torch.float64).scatter_(1, at, w)
-        m = torch.zeros(R, K, dtype=torch.float64).scatter_(1, at, m)
+        w = torch.zeros(R, x.shape[0], dtype=torch.float64).scatter_(1, at, w)
     want = w @ xd
-    tol = ROUND[y.dtype] * want.abs() + (C + 2) * 2.0 ** -24 * (m @ xd.abs()) + 1e-30
+    tol = ROUND[y.dtype] * want.abs() + 2 * (C + 2) * 2.0 ** -24 * (w.abs() @ xd.abs()) + 1e-30
     if y.dtype == torch.float16:
         tol = tol + 2.0 ** -25
     assert (((y.double() - want).abs() <= tol)).all(), float(((y.double() - want).abs() / tol).max())
@@ -181,6 +179,27 @@ def test_matvec_compressed(R, K, T, group, dtype):
     for out_dtype in (dtype, torch.float32):
         y = nm.matvec(codes, scales, x.cuda(), group, rows=R, meta=meta, out_dtype=out_dtype)
         check_product(y.cpu(), q, s, x, group, at)
+
+
+@pytest.mark.parametrize("R,K,T,sparse", [(40, 40001, 1, False), (40, 21001, 5, False),
+                                          (17, 30000, 8, False), (40, 24576, 3, True),
+                                          (4200, 2048, 8, True), (9000, 5000, 3, False)])
+def test_matvec_few_columns_of_long_or_many_rows(R, K, T, sparse):
+    """Few columns that are too long to be held whole, or held whole by too many rows' workgroups."""
+    dtype, group = torch.bfloat16, 64
+    w, x = weights(R, K, dtype), weights(K, T, torch.float64, 5).mul(50).to(dtype)
+    at = meta = None
+    if sparse:
+        at = nm.mask(w.cuda(), 2, 4).cpu().nonzero()[:, 1].view(R, K // 2)
+        values, meta = nm.compress(w.cuda(), 2, 4, layout="blocked")
+        codes, scales = nm.quantize(values, group, layout="blocked", rows=R)
+    else:
+        codes, scales = nm.quantize(w.cuda(), group)
+    y = nm.matvec(codes, scales, x.cuda(), group, rows=R, meta=meta, out_dtype=torch.float32).cpu()
+    some = torch.arange(0, R, max(1, R // 40))  # whole rows, every few
+    rows = w[some]
+    q, s = plain_quantize(rows if at is None else rows.gather(1, at[some]), group, dtype)
+    check_product(y[some], q, s, x, group, None if at is None else at[some])
 
 
 def test_matvec_agrees_with_the_products_it_stands_for():

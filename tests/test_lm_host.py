@@ -32,7 +32,7 @@ def test_sizes():
     assert L.nm_scales_bytes(17, 129, 48) == 0
     assert L.nm_matvec_workspace_bytes(4096, 4096, 1, 0) == 0
     assert L.nm_matvec_workspace_bytes(-1, 4096, 2, 0) == 0
-    assert L.nm_matvec_workspace_bytes(128, 16384, 2, 1) > 0    # X beyond the LDS: slices to be joined
+    assert L.nm_matvec_workspace_bytes(128, 65536, 2, 1) > 0    # X beyond the LDS: slices to be joined
     assert L.nm_matvec_workspace_bytes(128, 4096, 16, 0) == 0
     assert L.nm_xent_workspace_bytes(0, 8, 1) == 0
     assert L.nm_xent_grad_workspace_bytes(1 << 31, 8, 1) == 0
@@ -81,10 +81,10 @@ def test_matvec_refusals():
     assert matvec(T=-1) == matvec(T=1 << 20) == matvec(K=-1) == "shape"
     assert matvec(group=16) == "unsupported" and matvec(meta=far(6), K=96) == "layout"
     assert matvec(codes=None) == matvec(X=None) == matvec(Y=None) == "null"
-    assert matvec(ws=None, K=8192) == "null"
+    assert matvec(ws=None, K=65536) == "null"
     assert matvec(X=ODD) == matvec(ws=ODD) == matvec(meta=ODD) == "align"
-    assert matvec(n=100, K=8192) == "scratch"
-    assert matvec(Y=far(3)) == matvec(Y=far(5), K=8192) == matvec(ws=far(1), K=8192) == "alias"
+    assert matvec(n=100, K=65536) == "scratch"
+    assert matvec(Y=far(3)) == matvec(Y=far(5), K=65536) == matvec(ws=far(1), K=65536) == "alias"
     assert matvec(meta=far(4)) == "alias"
     assert matvec(R=0) == matvec(T=0) == "ok"
 
