@@ -42,6 +42,18 @@ constexpr int kGemmStep = 64;  // k per step
 // wave's accesses in order, so only the compiler has to keep it.
 __device__ __forceinline__ void keep_lds_order() { asm volatile("" ::: "memory"); }
 
+// The first `left` of eight 16-bit numbers in LDS to memory at any 2-byte address.
+__device__ __forceinline__ void store_piece(uint16_t* to, const uint8_t* lds, int64_t left) {
+  const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds);
+  if (left >= 8) {
+    *reinterpret_cast<u32x4_any_t*>(to) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+  }
+}
+
 // One operand: element (row, k) at p[row * ld + k], or at p[k * ld + row] if strided.  rows:
 // rows of the whole matrix from p on (loads past them read the last one).
 struct GemmOperand {
@@ -355,15 +367,15 @@ struct Gemm {
   }
 
   // Stores the accumulators as 16-bit numbers, element (row, col) at out[row * ld + col] for row <
-  // rows and col < cols.  Where rows of `out` are whole 16-byte pieces, each wave's 32 rows pass
-  // through its own part of smem and leave in 16-byte pieces of whole 128-byte lines: stored as
-  // the lanes hold them, 8 bytes in each of 32 rows, they take four times the requests.
+  // rows and col < cols.  Each wave's 32 rows pass through its own part of smem and leave in
+  // 16-byte pieces of whole 128-byte lines (a row's last ones by element where `cols` ends inside a
+  // piece): stored as the lanes hold them, 8 bytes in each of 32 rows, they take four times the
+  // requests.
   template <bool TO_BF16>
   static __device__ __forceinline__ void store16(const Acc& acc, int64_t m0, int64_t n0,
                                                  uint8_t* smem, uint16_t* out, int64_t ld,
                                                  int64_t rows, int64_t cols) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool whole = ld % 8 == 0 && cols % 8 == 0;
     constexpr int kPitch = 64 * FN + 16, kPieces = 4 * FN;  // bytes, 16-byte pieces a row
     static_assert(kWaves * 32 * kPitch <= kLds, "the waves' parts fit");
     uint8_t* mine = smem + wave * 32 * kPitch;
@@ -378,26 +390,17 @@ struct Gemm {
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = TO_BF16 ? f32_to_bf16(v[e]) : f32_to_f16(v[e]);
         const int c = 32 * (q / 4) + 8 * (q % 4) + 4 * (lane >> 5);
-        if (whole) {
-          *reinterpret_cast<u32x2_t*>(mine + (lane & 31) * kPitch + 2 * c) =
-              u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
-        } else if (row + (lane & 31) < rows) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + c + e < cols) out[(row + (lane & 31)) * ld + col + c + e] = (uint16_t)h[e];
-        }
+        *reinterpret_cast<u32x2_t*>(mine + (lane & 31) * kPitch + 2 * c) =
+            u32x2_t{h[0] | h[1] << 16, h[2] | h[3] << 16};
       }
-      if (whole) {
-        keep_lds_order();
+      keep_lds_order();
 #pragma unroll
-        for (int k = 0; k < 32 * kPieces / 64; ++k) {
-          const int p = k * 64 + lane, r = p / kPieces, c = p % kPieces * 8;
-          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + r * kPitch + 2 * c);
-          if (row + r < rows && col + c < cols)
-            *reinterpret_cast<u32x4_t*>(out + (row + r) * ld + col + c) = v;
-        }
-        keep_lds_order();
+      for (int k = 0; k < 32 * kPieces / 64; ++k) {
+        const int p = k * 64 + lane, r = p / kPieces, c = p % kPieces * 8;
+        if (row + r < rows)
+          store_piece(out + (row + r) * ld + col + c, mine + r * kPitch + 2 * c, cols - col - c);
       }
+      keep_lds_order();
     }
   }
 };

@@ -5,6 +5,9 @@
 
 namespace nm {
 
+// 16 bytes at any 2-byte address, in one access.
+typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+
 // `blocked` selects NM_LAYOUT_BLOCKED for the compressed pair (K % 64 == 0 checked).
 
 // Mask and/or compress: mask may be null (compress only); values/meta may be null (mask only).

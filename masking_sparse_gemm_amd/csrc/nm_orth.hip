@@ -235,7 +235,7 @@ struct OrthEpilogue {
     }
     keep_lds_order();
     const bool last = KIND == kUpdate && p.out;
-    const bool staged = !last || (p.out_dt != kF32 && p.K % 8 == 0);
+    const bool staged = !last || p.out_dt != kF32;
 #pragma unroll
     for (int q = 0; q < 4 * kFN; ++q) {
       const float4_t v = G::quad(acc, i, q / 4, q % 4);
@@ -263,12 +263,8 @@ struct OrthEpilogue {
         }
         const int64_t to_row = row + 32 * i + r, to = to_row * p.K + col + c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (to_row >= p.R || col + c + e >= p.K) continue;
-          if (p.out_dt == kF32) store_from_f32<kF32>(p.out, to + e, y[e]);
-          else if (p.out_dt == kF16) store_from_f32<kF16>(p.out, to + e, y[e]);
-          else store_from_f32<kBF16>(p.out, to + e, y[e]);
-        }
+        for (int e = 0; e < 4; ++e)
+          if (to_row < p.R && col + c + e < p.K) store_from_f32<kF32>(p.out, to + e, y[e]);
         continue;
       }
       half4_t h, l;
@@ -293,8 +289,7 @@ struct OrthEpilogue {
     if (!staged) return;
     if (last) {
       pieces<2>(i, p.R, p.K, [&](int, int64_t r, int64_t c, int lr, int lc) {
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + r * p.K + c) =
-            *reinterpret_cast<const u32x4_t*>(first + lr * kPitch + lc);
+        store_piece(static_cast<uint16_t*>(p.out) + r * p.K + c, first + lr * kPitch + lc, p.K - c);
       });
       return;
     }

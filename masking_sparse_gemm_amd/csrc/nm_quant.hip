@@ -58,7 +58,9 @@ __device__ __forceinline__ uint32_t f32_to_scale(float s) {
 typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
 
 // Eight elements of a row from column c, as they are stored; zeros past column C.  kWhole: C % 8
-// == 0, so the eight are wholly inside or outside and their address is 16-byte aligned.
+// == 0, so the eight are wholly inside or outside and their address is 16-byte aligned; else eight
+// that lie inside are read as they stand and only a row's last ones one by one (quantize and
+// dequantize of 4096 x 4100 bf16: 11.5 and 13.2 us, 27.1 and 40.3 with all one by one).
 template <int DT>
 struct Eight {
   static constexpr int kWords = DT == kF32 ? 8 : 4;
@@ -74,6 +76,13 @@ struct Eight {
 #pragma unroll
       for (int h = 0; h < kWords / 4; ++h) {
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + c + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * h + i] = v[i];
+      }
+    } else if (c + 8 <= C) {
+#pragma unroll
+      for (int h = 0; h < kWords / 4; ++h) {
+        const u32x4_any_t v = *reinterpret_cast<const u32x4_any_t*>(row + c + 4 * h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[4 * h + i] = v[i];
       }
@@ -221,6 +230,9 @@ __global__ void __launch_bounds__(256)
         const int64_t at = kBlocked ? ((g * (C / 32) + 4 * s + w) * 16 + r) * 32 + 8 * j : row * C + c;
         *reinterpret_cast<u32x4_t*>(W + at) =
             u32x4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+      } else if (c + 8 <= C) {
+        *reinterpret_cast<u32x4_any_t*>(W + row * C + c) =
+            u32x4_any_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)

@@ -103,14 +103,13 @@ __global__ void __launch_bounds__(256) pad_kernel(PadArgs p) {
     const uint32_t half = take ? 0xFFFFu << (16 * (e & 1)) : 0u;
     keep[e / 2] = e & 1 ? keep[e / 2] | half : half;
   }
-  const bool whole = p.cols % 8 == 0;
 #pragma unroll 4
   for (int64_t r = i / chunks; r < p.rp; r += stride) {
     u32x4_t v{0, 0, 0, 0};
     if (r < p.rows) {
       const uint16_t* x = p.in + r * p.cols + c;
-      if (whole) {
-        if (c < p.cols) v = *reinterpret_cast<const u32x4_t*>(x);
+      if (c + 8 <= p.cols) {
+        v = *reinterpret_cast<const u32x4_any_t*>(x);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
