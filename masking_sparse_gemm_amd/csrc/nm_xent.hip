@@ -189,6 +189,10 @@ struct StatsArgs {
   float* hit;        // [T]: the target's logit
 };
 
+// What exponents are taken relative to: the maximum, or 0 where that is an infinity, so that logits
+// of -infinity add 0 and one of +infinity makes the sum and its logarithm +infinity.
+__device__ __forceinline__ float base_of(float top) { return fabsf(top) < INFINITY ? top : 0.f; }
+
 template <class G>
 __global__ void __launch_bounds__(G::kThreads) stats_kernel(StatsArgs p) {
   constexpr int FM = G::kFM, FN = G::kFN, WM = G::kWM, WN = G::kWN;
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(G::kThreads) stats_kernel(StatsArgs p) {
         m = fmaxf(m, acc[i][j][r]);
       }
     m = fmaxf(m, __shfl_xor(m, 32));
-    const float shift = m == -INFINITY ? 0.f : m * kLog2e;
+    const float shift = base_of(m) * kLog2e;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(1024)
       float n = m;
 #pragma unroll
       for (int k = 0; k < 8; ++k) n = fmaxf(n, mi[k]);
-      const float sh = n == -INFINITY ? 0.f : n;
+      const float sh = base_of(n);
       s *= __builtin_amdgcn_exp2f((m - sh) * kLog2e);
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += si[k] * __builtin_amdgcn_exp2f((mi[k] - sh) * kLog2e);
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(1024)
   if (y == 0 && t < T) {
     float top_all = -INFINITY;
     for (int i = 0; i < 32; ++i) top_all = fmaxf(top_all, ms[i][x]);
-    const float sh = top_all == -INFINITY ? 0.f : top_all;
+    const float sh = base_of(top_all);
     float total = 0.f;
     for (int i = 0; i < 32; ++i) total += ss[i][x] * __builtin_amdgcn_exp2f((ms[i][x] - sh) * kLog2e);
     const float l = sh + __builtin_amdgcn_logf(total) * kLn2;
