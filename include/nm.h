@@ -377,7 +377,8 @@ nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta,
  *
  * Logits L = W X of W (V x K) and X (K x T, one column a token), dt NM_F16 or NM_BF16 for both;
  * L is never stored.  target: T entries; a token whose target is outside 0 .. V-1 is left out
- * (its loss is 0 and it adds nothing to the gradient, whatever its column of X holds).
+ * (its loss and its column of dX are 0 and it adds nothing to dW, whatever its column of X, or W,
+ * holds).
  *   lse[t]  = log sum over v of exp L[v, t]       (of every token; +infinity where a logit is)
  *   loss[t] = lse[t] - L[target[t], t]
  * loss and lse are fp32; sums are fp32.  V >= 1 where T > 0, V < 2^31, K < 2^22, T < 2^22,

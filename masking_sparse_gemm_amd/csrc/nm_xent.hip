@@ -454,10 +454,13 @@ __global__ void __launch_bounds__(GX::kThreads) grad_kernel(GradArgs p) {
   else grad_w_tile<GW, BF16>(p.w, b - first_w, smem);
 }
 
+// dX from its sums; zeros at the tokens left out, also where a word's row of W is not finite and made
+// NaN of their P of zeros.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     finish_x_kernel(const float* __restrict__ sums, int splits, int64_t K, int64_t T, int64_t Tp,
-                    const float* __restrict__ back, uint16_t* __restrict__ dX) {
+                    const float* __restrict__ back, const int* __restrict__ y,
+                    uint16_t* __restrict__ dX) {
   const float f = *back;
   const int64_t total = K * Tp / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
@@ -469,9 +472,12 @@ __global__ void __launch_bounds__(256)
       for (int e = 0; e < 4; ++e) v[e] += b[e];
     }
     const int64_t k = 4 * i / Tp, t = 4 * i % Tp;
+    const int4 y4 = *reinterpret_cast<const int4*>(y + t);
+    const int ys[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (t + e < T) store_from_f32<BF16 ? kBF16 : kF16>(dX, k * T + t + e, v[e] * f);
+      if (t + e < T)
+        store_from_f32<BF16 ? kBF16 : kF16>(dX, k * T + t + e, ys[e] >= 0 ? v[e] * f : 0.f);
   }
 }
 
@@ -607,7 +613,7 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     if (e != hipSuccess) return e;
   }
   finish_x_kernel<BF16><<<stride_grid(K * L.Tp / 4, 256), 256, 0, s>>>(sums, L.splits, K, T, L.Tp,
-                                                                     tok.back, dX);
+                                                                     tok.back, tok.y, dX);
   return hipGetLastError();
 }
 

@@ -45,3 +45,17 @@ def test_infinite_logits(V, up, dtype):
         want = plain(W, X, y, g)
         assert torch.equal(dW.isnan(), want["dW"].isnan())
         assert torch.equal(dX.isnan(), want["dX"].isnan())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_left_out_tokens_have_no_gradient_whatever_W_holds(dtype, bad):
+    """A word whose row of W is not finite spoils the live tokens, not those that are left out."""
+    W, X, y, g = problem(300, 64, 40, dtype, 11)
+    W[7] = bad
+    y[5], y[30] = -100, 300
+    loss, lse = nm.xent(W.cuda(), X.cuda(), y.cuda())
+    _, dX = nm.xent_grad(W.cuda(), X.cuda(), y.cuda(), lse, g.cuda())
+    left = (y < 0) | (y >= 300)
+    assert (loss.cpu()[left] == 0).all() and (dX.cpu()[:, left] == 0).all()
+    assert dX.cpu()[:, ~left].isnan().any()
