@@ -392,7 +392,9 @@ nm_status nm_xent(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t 
 /* The gradient of sum over t of gout[t] * loss[t] (gout: T fp32 numbers; 1 / tokens for a mean):
  *   dW (V x K) = P X^T,  dX (K x T) = W^T P,  P[v, t] = (exp(L[v, t] - lse[t]) - [v = target[t]]) gout[t]
  * with lse from nm_xent, in dt.  The logits are computed again, a piece of the vocabulary at a
- * time; P of a piece is rounded to dt, sums are fp32, results are rounded once. */
+ * time; P of a piece is rounded to dt, sums are fp32, results are rounded once.  P is scaled by g
+ * for that; in NM_F16 a token whose g is below 2^-14 of the largest is scaled by its own (dW then
+ * takes the rest of it on X's column), so its column of dX keeps probabilities down to 2^-24. */
 size_t nm_xent_grad_workspace_bytes(int64_t V, int64_t K, int64_t T);
 nm_status nm_xent_grad(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
                        const int64_t* target, const float* lse, const float* gout, void* dW,

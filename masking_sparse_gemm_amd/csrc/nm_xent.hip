@@ -10,9 +10,11 @@
 // Gradient: the vocabulary is taken in pieces whose P fits a bounded workspace.  For each piece
 // the logits are multiplied again and leave the epilogue as P in 16 bits (the operand the next
 // two products need; the rounding is the same relative size as that of dW and dX themselves), then
-// dW of the piece is one product, and W^T P is added to fp32 sums of dX.  g is brought to a
-// power-of-two multiple that fits 16-bit numbers before the rounding, and the products are scaled
-// back in fp32, so fp16 loses no small probabilities to underflow whatever g's size.
+// dW of the piece is one product, and W^T P is added to fp32 sums of dX.  g is taken over its largest,
+// times 2^14, before the rounding, and the products are scaled back in fp32.  fp16: a token whose g
+// is below 2^-14 of the largest keeps its P at 2^0 for a probability of 1, so that its column of dX
+// loses no more to underflow than any other's, and brings the rest of its g to dW as a power of two
+// on its column of X.
 //
 // Bound by the matrix cores where tokens are many: 32768 x 4096 with 2048 tokens in bf16 takes 474
 // us for the loss's product (1160 TFLOP/s), and for the gradient's three, in two pieces, 478, 476 and
@@ -21,6 +23,8 @@
 //
 // Tokens with a target outside 0 .. V - 1 are left out: their loss is 0 and their column of X
 // is read as zeros in the gradient, so that not even infinities or NaN in it reach dW.
+#include <algorithm>
+
 #include "nm_gemm.h"
 #include "nm_grid.h"
 
@@ -38,36 +42,71 @@ int64_t pad256b(int64_t n) { return (n + 255) / 256 * 256; }
 struct TokenArgs {  // of the tokens, padded to a whole number of 64
   int* y;           // target, -1 where left out
   float* lse;
-  float* g;         // g times 2^14 over the largest
-  float* back;      // one number: what brings a sum of P back
+  float* g;         // what P's column is times: g times 2^14 over the largest, over `down`
+  float* down;      // fp16: what X's column is times for dW, a power of two up to 1
+  float* back;      // what brings dX's column back
+  float* all_back;  // one number: what brings dW back
+  int* any_down;    // one number: whether a token's `down` is below 1
 };
 
-// One workgroup: the largest |g| of the tokens that count, then all g over it, times 2^14.  A mean's
-// equal g become 2^14, so that the entries of P at the targets, just below 2^14 in size, lie where
-// 16-bit numbers are densest for their size.
+// One workgroup: the largest finite |g| of the tokens that count, then all g over it, times 2^14.  A
+// mean's equal g become 2^14, so that the entries of P at the targets, just below 2^14 in size, lie
+// where 16-bit numbers are densest for their size.  DOWN (fp16, whose normal numbers end at 2^-14): a
+// smaller g keeps its P between 2^0 and 2^1 at least.
+template <bool DOWN>
 __device__ __forceinline__ void prepare_tokens(const int64_t* __restrict__ target,
                                                const float* __restrict__ lse,
                                                const float* __restrict__ gout, int64_t V, int64_t T,
                                                int64_t Tp, const TokenArgs& out) {
   __shared__ float part[4];
+  __shared__ int any;
+  if (threadIdx.x == 0) any = 0;
   float top = 0.f;
 #pragma unroll 4
   for (int64_t t = threadIdx.x; t < T; t += 256)
-    if (target[t] >= 0 && target[t] < V) top = fmaxf(top, fabsf(gout[t]));
+    if (target[t] >= 0 && target[t] < V && fabsf(gout[t]) < INFINITY) top = fmaxf(top, fabsf(gout[t]));
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) top = fmaxf(top, part[i]);
-  const bool scaled = top > 0.f && top < INFINITY;
-  if (threadIdx.x == 0) *out.back = scaled ? top * 0x1p-14f : 1.f;
+  const bool scaled = top > 0.f;
+  const float back = scaled ? top * 0x1p-14f : 1.f;
+  int top_e;
+  const float top_m = frexpf(top, &top_e);
+  bool mine = false;
 #pragma unroll 4
   for (int64_t t = threadIdx.x; t < Tp; t += 256) {
     const bool live = t < T && target[t] >= 0 && target[t] < V;
+    const float g = live ? gout[t] : 0.f;
+    float p = scaled ? g / top * 0x1p14f : g;
     out.y[t] = live ? (int)target[t] : -1;
     out.lse[t] = live ? lse[t] : 0.f;
-    out.g[t] = !live ? 0.f : scaled ? gout[t] / top * 0x1p14f : gout[t];
+    if constexpr (DOWN) {
+      int e = 0;
+      if (g != 0.f && fabsf(p) < 1.f) {  // g = m 2^e with m in [1/2, 1)
+        const float m = frexpf(g, &e);
+        p = m / top_m;
+        e -= top_e - 14;
+        if (fabsf(p) < 1.f) {
+          p *= 2.f;
+          --e;
+        }
+        mine |= e < 0;
+      }
+      out.down[t] = ldexpf(1.f, e > -100 ? e : -100);  // of fp16 nothing is left there
+      out.back[t] = ldexpf(back, e);
+    } else {
+      out.back[t] = back;
+    }
+    out.g[t] = p;
+  }
+  if (threadIdx.x == 0) *out.all_back = back;
+  if constexpr (DOWN) {
+    if (mine) atomicOr(&any, 1);
+    __syncthreads();
+    if (threadIdx.x == 0) *out.any_down = any;
   }
 }
 
@@ -85,11 +124,11 @@ struct PadArgs {
 };
 
 // A thread keeps its eight columns and walks down the rows.
-template <bool TOKENS>
+template <bool TOKENS, bool DOWN = false>
 __global__ void __launch_bounds__(256) pad_kernel(PadArgs p) {
   const int64_t blocks = gridDim.x - (TOKENS ? 1 : 0);
   if (TOKENS && blockIdx.x == blocks) {
-    prepare_tokens(p.target, p.lse, p.gout, p.V, p.cols, p.cp, p.tok);
+    prepare_tokens<DOWN>(p.target, p.lse, p.gout, p.V, p.cols, p.cp, p.tok);
     return;
   }
   const int64_t chunks = p.cp / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -125,14 +164,14 @@ __global__ void __launch_bounds__(256) pad_kernel(PadArgs p) {
 // A chunk to a thread until two workgroups to a unit, more rows a thread from there, since each
 // thread reads its columns' targets first (4096 x 2048: 17 us with 512 workgroups, 23 with 2048);
 // and no fewer threads than a row has chunks.
-template <bool TOKENS>
+template <bool TOKENS, bool DOWN = false>
 hipError_t launch_pad(const PadArgs& p, hipStream_t s) {
   const int64_t chunks = p.cp / 8, least = (chunks + 255) / 256;
   int64_t blocks = (p.rp * chunks + 255) / 256;
   if (blocks > 512) blocks = 512;
   if (blocks < least) blocks = least;
   if (p.rp * chunks > 0 || TOKENS)
-    pad_kernel<TOKENS><<<(unsigned)(blocks + (TOKENS ? 1 : 0)), 256, 0, s>>>(p);
+    pad_kernel<TOKENS, DOWN><<<(unsigned)(blocks + (TOKENS ? 1 : 0)), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -307,6 +346,27 @@ struct LossLayout {
 
 // ---- gradient --------------------------------------------------------------------------
 
+// fp16: the X that dW is formed from where a token's column is brought down, rows x Tp.
+struct DownArgs {
+  const uint16_t* x;
+  int64_t rows, Tp;
+  const float* down;
+  const int* any;    // without any, X itself is used
+  uint16_t* out;
+};
+__device__ __forceinline__ void bring_down(const DownArgs& p, int64_t first, int64_t stride) {
+  if (*p.any == 0) return;
+  for (int64_t i = first; i < p.rows * p.Tp / 8; i += stride) {
+    const int64_t t = 8 * i % p.Tp;
+    u32x4_t v = reinterpret_cast<const u32x4_t*>(p.x)[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = f32_to_f16(f16_to_f32(v[e] & 0xFFFFu) * p.down[t + 2 * e]) |
+             f32_to_f16(f16_to_f32(v[e] >> 16) * p.down[t + 2 * e + 1]) << 16;
+    reinterpret_cast<u32x4_t*>(p.out)[i] = v;
+  }
+}
+
 struct ProbArgs {
   GemmOperand w, x;  // w from the piece's first row on
   int steps;
@@ -315,11 +375,18 @@ struct ProbArgs {
   int64_t rows, Tp;  // of P, padded
   TokenArgs tok;
   uint16_t* P;       // rows x Tp
+  int groups;        // workgroups of the product; those past them (fp16, first piece) bring X down
+  DownArgs down;
 };
 
 template <class G, bool BF16>
 __global__ void __launch_bounds__(G::kThreads) prob_kernel(ProbArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  if (!BF16 && (int)blockIdx.x >= p.groups) {
+    bring_down(p.down, (int64_t)(blockIdx.x - p.groups) * G::kThreads + threadIdx.x,
+               (int64_t)(gridDim.x - p.groups) * G::kThreads);
+    return;
+  }
   int tm, tn;
   if (!p.map.tile_of(blockIdx.x, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
@@ -408,6 +475,8 @@ struct GradWArgs {
   GemmMap map;
   int64_t rows, K;  // rows of W in the piece
   const float* back;
+  const uint16_t* x_down;  // fp16: the X to use if *any_down
+  const int* any_down;
   uint16_t* dW;     // from the piece's first row on
 };
 
@@ -418,7 +487,9 @@ __device__ __forceinline__ void grad_w_tile(const GradWArgs& p, int group, uint8
   const int64_t m0 = (int64_t)tm * G::kBM, n0 = (int64_t)tn * G::kBN;
   typename G::Acc acc;
   G::clear(acc);
-  G::run(p.q, p.x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
+  GemmOperand x = p.x;
+  if (!BF16 && __builtin_amdgcn_readfirstlane(*p.any_down)) x.p = p.x_down;
+  G::run(p.q, x, m0, n0, p.steps, (int64_t)p.steps * kGemmStep, smem, acc);
   const float back = *p.back;
 #pragma unroll
   for (int i = 0; i < G::kFM; ++i)
@@ -461,7 +532,6 @@ __global__ void __launch_bounds__(256)
     finish_x_kernel(const float* __restrict__ sums, int splits, int64_t K, int64_t T, int64_t Tp,
                     const float* __restrict__ back, const int* __restrict__ y,
                     uint16_t* __restrict__ dX) {
-  const float f = *back;
   const int64_t total = K * Tp / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
@@ -473,11 +543,12 @@ __global__ void __launch_bounds__(256)
     }
     const int64_t k = 4 * i / Tp, t = 4 * i % Tp;
     const int4 y4 = *reinterpret_cast<const int4*>(y + t);
+    const float4_t f = *reinterpret_cast<const float4_t*>(back + t);
     const int ys[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (t + e < T)
-        store_from_f32<BF16 ? kBF16 : kF16>(dX, k * T + t + e, ys[e] >= 0 ? v[e] * f : 0.f);
+        store_from_f32<BF16 ? kBF16 : kF16>(dX, k * T + t + e, ys[e] >= 0 ? v[e] * f[e] : 0.f);
   }
 }
 
@@ -485,7 +556,7 @@ struct GradLayout {
   int64_t Kp, Tp, piece;  // piece: rows of W at a time
   bool copy_w;
   int tile_x, splits;     // of dX
-  int64_t x, w, tok_y, tok_lse, tok_g, back, P, sums, total;
+  int64_t x, x_down, w, tok_y, tok_lse, tok_g, tok_down, tok_back, all_back, P, sums, total;
   GradLayout(int64_t V, int64_t K, int64_t T) {
     Kp = pad64(K);
     Tp = pad64(T);
@@ -508,12 +579,15 @@ struct GradLayout {
         }
       }
     x = 0;
-    w = x + pad256b(Kp * Tp * 2);
+    x_down = x + pad256b(Kp * Tp * 2);
+    w = x_down + pad256b(Kp * Tp * 2);
     tok_y = w + (copy_w ? pad256b(V * Kp * 2) : 0);
     tok_lse = tok_y + pad256b(Tp * 4);
     tok_g = tok_lse + pad256b(Tp * 4);
-    back = tok_g + pad256b(Tp * 4);
-    P = back + 256;
+    tok_down = tok_g + pad256b(Tp * 4);
+    tok_back = tok_down + pad256b(Tp * 4);
+    all_back = tok_back + pad256b(Tp * 4);  // and any_down
+    P = all_back + 256;
     sums = P + pad256b(pad64(piece) * Tp * 2);
     total = sums + pad256b((int64_t)splits * K * Tp * 4);
   }
@@ -536,12 +610,17 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
   uint16_t* Xp = reinterpret_cast<uint16_t*>(ws + L.x);
   uint16_t* P = reinterpret_cast<uint16_t*>(ws + L.P);
   float* sums = reinterpret_cast<float*>(ws + L.sums);
-  const TokenArgs tok{reinterpret_cast<int*>(ws + L.tok_y), reinterpret_cast<float*>(ws + L.tok_lse),
-                      reinterpret_cast<float*>(ws + L.tok_g), reinterpret_cast<float*>(ws + L.back)};
+  uint16_t* x_down = reinterpret_cast<uint16_t*>(ws + L.x_down);
+  const TokenArgs tok{reinterpret_cast<int*>(ws + L.tok_y),
+                      reinterpret_cast<float*>(ws + L.tok_lse),
+                      reinterpret_cast<float*>(ws + L.tok_g),
+                      reinterpret_cast<float*>(ws + L.tok_down),
+                      reinterpret_cast<float*>(ws + L.tok_back),
+                      reinterpret_cast<float*>(ws + L.all_back),
+                      reinterpret_cast<int*>(ws + L.all_back) + 1};
+  const PadArgs pad_x{X, K, T, Xp, L.Kp, L.Tp, target, lse, gout, V, tok};
   hipError_t e;
-  if ((e = launch_pad<true>(PadArgs{X, K, T, Xp, L.Kp, L.Tp, target, lse, gout, V, tok}, s)) !=
-      hipSuccess)
-    return e;
+  if ((e = launch_pad<true, !BF16>(pad_x, s)) != hipSuccess) return e;
   const uint16_t* Wp = W;
   if (L.copy_w) {
     uint16_t* w = reinterpret_cast<uint16_t*>(ws + L.w);
@@ -561,10 +640,13 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     a.Tp = L.Tp;
     a.tok = tok;
     a.P = P;
+    a.down = DownArgs{Xp, L.Kp, L.Tp, tok.down, tok.any_down, x_down};
+    const int down = BF16 || v0 > 0 ? 0 : (int)std::min<int64_t>(L.Kp * L.Tp / 8 / 256, 256);
     e = with_tile<false, true, BF16, true>(pick_tile(rp, L.Tp, a.steps), [&](auto tag) {
       typedef typename decltype(tag)::type G;
       a.map = make_gemm_map((rp + G::kBM - 1) / G::kBM, (L.Tp + G::kBN - 1) / G::kBN);
-      return G::template launch<prob_kernel<G, BF16>>(a, a.map.groups(), 1, s);
+      a.groups = a.map.groups();
+      return G::template launch<prob_kernel<G, BF16>>(a, a.groups + down, 1, s);
     });
     if (e != hipSuccess) return e;
 
@@ -574,7 +656,9 @@ hipError_t run_grad(const uint16_t* W, const uint16_t* X, int64_t V, int64_t K, 
     b.steps = (int)(L.Tp / kGemmStep);
     b.rows = rows;
     b.K = K;
-    b.back = tok.back;
+    b.back = tok.all_back;
+    b.x_down = x_down;
+    b.any_down = tok.any_down;
     b.dW = dW + v0 * K;
     GradXArgs c{};
     c.w = GemmOperand{Wp + v0 * ldw, ldw, L.Kp, 0};
