@@ -9,7 +9,10 @@
 // at most about 3, so the wide exponent of bf16 buys nothing and its 8 bits cost a percent of
 // the result.  All three are held times 2^8, which keeps entries of 2^-22 in fp16's normal
 // range.  G itself is only scaled by a power of two (exact for bf16); the rest of its norm, a
-// factor rho in fp32, goes into the first step's epilogues.
+// factor in fp32, goes into the first step's epilogues.  Where eps makes X far smaller than 1, each
+// step multiplies it by about a until it is near 1; the X that is stored is kept at its first size
+// meanwhile and a factor is carried beside it, since fp16 would lose it.  A is stored as it is: what
+// it loses below 2^-33 is nothing beside the a of a X.
 //   bf16 G: operands are one fp16, and the X that a X is formed from has the next four bits
 //     beside it (one fp8 an entry): without them the small singular values lose most.
 //   fp16 and fp32 G: each operand is two fp16, hi + lo (22 bits), and a product is hi hi +
@@ -32,10 +35,13 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kNormBlocks = 1024;
 constexpr float kOrthScale = 256.f;
+constexpr int kMaxSteps = 100;
+constexpr float kCoefA = 3.4445f, kCoefB = -4.7750f, kCoefC = 2.0315f;
 
 struct OrthHead {  // first bytes of the workspace
   double partial[kNormBlocks];
-  float rho;
+  float size[kMaxSteps];  // X of a step is `size` times the stored one
+  float grow[kMaxSteps];  // this step's size over the next one's (1 for the result)
 };
 
 template <int DT>
@@ -85,7 +91,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const void* __restrict__ G, i
 template <int DT, bool SPLIT>
 __global__ void __launch_bounds__(256)
     start_kernel(const void* __restrict__ G, int64_t R, int64_t K, int64_t rp, int64_t kp, float eps,
-                 OrthHead* head, _Float16* __restrict__ hi, _Float16* __restrict__ lo) {
+                 int steps, OrthHead* head, _Float16* __restrict__ hi, _Float16* __restrict__ lo) {
   __shared__ double part[4];
   double sum = 0;
 #pragma unroll
@@ -98,8 +104,14 @@ __global__ void __launch_bounds__(256)
   int e = 0;
   if (norm > 0 && norm < INFINITY) frexp(norm, &e);  // norm = f 2^e, f in [1/2, 1)
   const int k = 8 - e;
-  if (blockIdx.x == 0 && threadIdx.x == 0)
-    head->rho = norm > 0 ? (float)(ldexp(256.0, -k) / (norm + (double)eps)) : 1.f;
+  if (blockIdx.x == 0 && (int)threadIdx.x < steps) {  // a thread a step
+    const int i = threadIdx.x;
+    const auto after = [](double size) { return size > 0 ? fmin(1.0, size * kCoefA) : 1.0; };
+    double size = norm > 0 ? ldexp(256.0, -k) / (norm + (double)eps) : 1.0;
+    for (int j = 0; j < i && size != 1.0; ++j) size = after(size);
+    head->size[i] = (float)size;
+    head->grow[i] = (float)(i + 1 < steps ? size / after(size) : size);
+  }
   const int64_t total = rp * kp / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t r = 4 * i / kp, c = 4 * i % kp;
@@ -122,8 +134,7 @@ struct OrthArgs {
   int steps;
   GemmMap map;
   int64_t rows, cols;  // of the result, whole multiples of 64; its rows are `cols` apart
-  float ca, cb, cc;
-  const float* rho;            // the first step's factor, else null
+  const float *size, *grow;    // the step's (OrthHead)
   const _Float16 *from_hi, *from_lo;  // square: A; update: the X before
   _Float16 *hi, *lo;           // result (lo only with two parts)
   uint8_t* rest;               // one part: what hi lacks of X in fp8
@@ -187,7 +198,7 @@ struct OrthEpilogue {
   uint8_t* mine;
   int lane;
   int64_t row, col;  // of the wave's part
-  float rho;
+  float factor;      // size of X (gram), its growth (update)
   bool mirror;
 
   // f(k, row, column, 16-byte column) for each 16-byte piece of the lane in a plane of BYTES an
@@ -244,13 +255,13 @@ struct OrthEpilogue {
       uint8_t* const at2 = second + r * kSecondPitch + kSecondBytes * c;
       float4_t y;
       if constexpr (KIND == kGram) {
-        y = v * (rho * rho / kOrthScale);
+        y = v * (factor * factor / kOrthScale);
       } else {
         float4_t x = widen(*at);
         if constexpr (SPLIT) x += widen(*reinterpret_cast<const half4_t*>(at2));
         else if (kRest && p.from_rest) x += unpack_rest(*reinterpret_cast<const uint32_t*>(at2));
-        if constexpr (KIND == kSquare) y = p.cb * x + (p.cc / kOrthScale) * v;
-        else y = rho * (p.ca * x + (1.f / kOrthScale) * v);
+        if constexpr (KIND == kSquare) y = kCoefB * x + (kCoefC / kOrthScale) * v;
+        else y = factor * (kCoefA * x + (1.f / kOrthScale) * v);
       }
       if (last) {
         y *= 1.f / kOrthScale;
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(G::kThreads) orth_kernel(OrthArgs p) {
   const int wave = threadIdx.x >> 6;
   const Epilogue epilogue{p, smem + wave * Epilogue::kWaveBytes, (int)threadIdx.x & 63,
                           m0 + wave / G::kWN * 32 * G::kFM, n0 + wave % G::kWN * 32 * G::kFN,
-                          p.rho ? *p.rho : 1.f, tm != tn};
+                          KIND == kGram ? *p.size : KIND == kUpdate ? *p.grow : 1.f, tm != tn};
   // A small tile's epilogue reads come ahead of its few steps, a large one's 32 rows ahead.
   constexpr bool kEarly = G::kFM == 1;
   typename Epilogue::Before before[2];
@@ -455,11 +466,14 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
   const int64_t quads = L.rp * L.kp / 4;
   const unsigned grid = (unsigned)(quads / 256 < 2048 ? (quads + 255) / 256 : 2048);
   if (dt == kF32)
-    start_kernel<kF32, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, head, x[0], x[0] + x_lo);
+    start_kernel<kF32, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, steps, head, x[0],
+                                                     x[0] + x_lo);
   else if (dt == kF16)
-    start_kernel<kF16, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, head, x[0], x[0] + x_lo);
+    start_kernel<kF16, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, steps, head, x[0],
+                                                     x[0] + x_lo);
   else
-    start_kernel<kBF16, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, head, x[0], x[0] + x_lo);
+    start_kernel<kBF16, SPLIT><<<grid, 256, 0, s>>>(G, R, K, L.rp, L.kp, eps, steps, head, x[0],
+                                                     x[0] + x_lo);
   if ((e = hipGetLastError()) != hipSuccess) return e;
 
   auto op = [](const _Float16* p, int64_t ld, int64_t rows, int64_t lo) {
@@ -468,10 +482,8 @@ hipError_t run_orth(const void* G, int dt, int64_t R, int64_t K, int steps, floa
   for (int i = 0; i < steps; ++i) {
     const _Float16* from = x[i & 1];
     OrthArgs p{};
-    p.ca = 3.4445f;
-    p.cb = -4.7750f;
-    p.cc = 2.0315f;
-    p.rho = i == 0 ? &head->rho : nullptr;
+    p.size = &head->size[i];
+    p.grow = &head->grow[i];
     // A = X X^T, or X^T X (both operands then have k as their row index)
     p.a = p.b = op(from, L.kp, L.mp, x_lo);
     p.steps = (int)((L.tall ? L.rp : L.kp) / kGemmStep);
