@@ -628,11 +628,18 @@ def _xent_inputs(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor):
     return dt, V, K, T
 
 
+def _token_numbers(t: torch.Tensor) -> torch.Tensor:
+    """t, or its copy where it is a view that starts off 16 bytes (target = tokens[1:]), which the
+    library does not take."""
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def xent(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor):
     """(loss, lse), float32 (T,): softmax cross entropy of the logits W X -- W (V, K), X (K, T),
     bfloat16 or float16, a column a token -- at target (int64), and the logits' log sum exp.  A
     target outside 0 .. V - 1 leaves its token out: loss 0.  The logits are not stored."""
     dt, V, K, T = _xent_inputs(W, X, target)
+    target = _token_numbers(target)
     loss = W.new_empty((T,), dtype=torch.float32)
     lse = W.new_empty((T,), dtype=torch.float32)
     L = lib()
@@ -652,6 +659,7 @@ def xent_grad(W: torch.Tensor, X: torch.Tensor, target: torch.Tensor, lse: torch
         if t.dtype != torch.float32 or tuple(t.shape) != (T,) or not t.is_contiguous() or \
                 t.device != W.device:
             raise ValueError(f"{name} must be a contiguous float32 ({T},) tensor on W's device")
+    target, lse, gout = _token_numbers(target), _token_numbers(lse), _token_numbers(gout)
     dW, dX = torch.empty_like(W), torch.empty_like(X)
     L = lib()
     ws, ws_ptr = _workspace(W, L.nm_xent_grad_workspace_bytes(V, K, T))

@@ -121,3 +121,17 @@ def test_not_finite_gout_stays_with_its_token():
     # W = 2^-11 g, and the result's rounding, 2^-11 of it or 2^-25
     assert (off <= 2.0 ** -8 * gout[keep].double() + 2.0 ** -10 * clean[:, keep].double().abs()
             + 2.0 ** -24).all()
+
+
+def test_shifted_targets():
+    """A view that starts at any entry (target = tokens[1:]) is taken as it stands."""
+    W, X, y, g = (t.cuda() for t in problem(300, 64, 40, torch.bfloat16, 13))
+    loss, lse = nm.xent(W, X, y)
+    want = nm.xent_grad(W, X, y, lse, g)
+    tokens = torch.cat([y[:1], y])
+    lse1, g1 = (torch.cat([t.new_zeros(3), t])[3:] for t in (lse, g))
+    assert tokens[1:].data_ptr() % 16 and lse1.data_ptr() % 16 and g1.data_ptr() % 16
+    again = nm.xent(W, X, tokens[1:])
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    for a, b in zip(nm.xent_grad(W, X, tokens[1:], lse1, g1), want):
+        assert torch.equal(a, b)
