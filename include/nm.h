@@ -363,7 +363,8 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
  * one column or a few (every T is taken; beyond some tens a dequantised product is faster).
  * meta NULL: dense codes of C = K columns.  Else the metadata, in NM_LAYOUT_BLOCKED, of a 2:4
  * pair whose values the codes hold (C = K/2; K % 64 == 0, else NM_ERR_LAYOUT); it is trusted.
- * R < 2^26, K < 2^25, T < 2^20, else NM_ERR_SHAPE.
+ * R < 2^26, K < 2^25, T < 2^20, and where a workspace is needed R T < 2^34 (whole 16 rows and 16
+ * or 32 columns), else NM_ERR_SHAPE.
  * dt is the type of X and of the scales, NM_F16 or NM_BF16; y_dt is dt or NM_F32.  Codes enter
  * the matrix cores exactly, sums are fp32, a group's sum is scaled in fp32 and Y is rounded once.
  * workspace: nm_matvec_workspace_bytes(R, K, T, meta != NULL) bytes of device memory (0 for

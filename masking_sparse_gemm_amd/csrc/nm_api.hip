@@ -595,16 +595,19 @@ nm_status nm_dequantize(const void* codes, const void* scales, nm_dtype scale_dt
 }
 
 namespace {
-nm_status check_matvec(int64_t R, int64_t K, int64_t T) {
-  // a launch has 512 work-items for 16 rows or more, one slice for 1024 rows of X or more
+nm_status check_matvec(int64_t R, int64_t K, int64_t T, bool sparse) {
+  // the products' launches have at most 512 work-items for 16 rows along x, a slice for 1024 rows of X
+  // or more along y and a workgroup for 16 columns or more along z; the slices' join is checked apart
   if (T < 0 || T >= kMaxSide / 4 || K >= (int64_t)1 << 25 || R >= (int64_t)1 << 26)
     return NM_ERR_SHAPE;
-  return check_shape(R, K, 1);
+  const nm_status st = check_shape(R, K, 1);
+  const bool small = (R + 15) * (T + 31) < (int64_t)1 << 34;
+  return st != NM_OK || small || nm::matvec_fits(R, K, T, sparse) ? st : NM_ERR_SHAPE;
 }
 }  // namespace
 
 size_t nm_matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, int sparse) {
-  if (check_matvec(R, K, T) != NM_OK || R * T == 0) return 0;
+  if (check_matvec(R, K, T, sparse != 0) != NM_OK || R * T == 0) return 0;
   return nm::matvec_workspace_bytes(R, K, T, sparse != 0);
 }
 
@@ -612,7 +615,7 @@ nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta,
                     int64_t K, int group, const void* X, int64_t T, nm_dtype dt, void* Y,
                     nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
   if (!half_dtype(dt) || (y_dt != dt && y_dt != NM_F32)) return NM_ERR_DTYPE;
-  nm_status st = check_matvec(R, K, T);
+  nm_status st = check_matvec(R, K, T, meta != nullptr);
   if (st != NM_OK) return st;
   if (!group_ok(group)) return NM_ERR_UNSUPPORTED;
   if (meta != nullptr && K % 64 != 0) return NM_ERR_LAYOUT;

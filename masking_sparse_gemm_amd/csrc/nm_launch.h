@@ -75,6 +75,9 @@ hipError_t launch_quantize(const void* W, int dt, int64_t R, int64_t C, bool blo
                            void* codes, void* scales, int scale_dt, hipStream_t s);
 hipError_t launch_dequantize(const void* codes, const void* scales, int scale_dt, int64_t R,
                              int64_t C, bool blocked, int group, void* W, hipStream_t s);
+// Whether every launch of the product has fewer than 2^32 work-items in a dimension, for sizes within
+// the call's own limits.
+bool matvec_fits(int64_t R, int64_t K, int64_t T, bool sparse);
 size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse);
 hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
                          int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,

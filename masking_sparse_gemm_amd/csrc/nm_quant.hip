@@ -677,6 +677,7 @@ int64_t column_lds(int64_t R, int64_t K, int64_t T) {
 struct MatvecPlan {
   int nt, log_along, slice, slices;
   int64_t groups, tiles;  // workgroups along rows, along columns of X
+  int64_t pieces;         // work-items that join the slices: one for four rows of a column
   int64_t bytes;          // of workspace
   MatvecPlan(int64_t R, int64_t K, int64_t T, bool sparse) {
     const int64_t block_rows = sparse ? 256 : 128, S = (K + block_rows - 1) / block_rows;
@@ -701,7 +702,8 @@ struct MatvecPlan {
     slice = (int)std::max<int64_t>(1, (S + slices - 1) / slices);
     slices = (int)std::max<int64_t>(1, (S + slice - 1) / slice);
     groups = groups_of(log_along);
-    bytes = slices > 1 ? slices * ((R + 15) / 16) * tiles * nt * 1024 : 0;
+    pieces = slices > 1 ? (R + 15) / 16 * tiles * nt * 64 : 0;
+    bytes = slices * pieces * 16;
   }
 };
 
@@ -717,9 +719,8 @@ hipError_t launch_matvec_slices(const MatvecArgs& a, const MatvecPlan& p, hipStr
            s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.slices == 1) return e;
-  const int64_t tiles = p.tiles * NT, pieces = (a.R + 15) / 16 * tiles * 64;
-  join_slices_kernel<YT><<<(unsigned)((pieces + 255) / 256), 256, 0, s>>>(a.part, p.slices, pieces,
-                                                                        tiles, a.R, a.T, a.y);
+  join_slices_kernel<YT><<<(unsigned)((p.pieces + 255) / 256), 256, 0, s>>>(
+      a.part, p.slices, p.pieces, p.tiles * NT, a.R, a.T, a.y);
   return hipGetLastError();
 }
 
@@ -829,6 +830,10 @@ hipError_t launch_dequantize(const void* codes, const void* scales, int scale_dt
   else NM_DEQ(false, false);
 #undef NM_DEQ
   return hipGetLastError();
+}
+
+bool matvec_fits(int64_t R, int64_t K, int64_t T, bool sparse) {
+  return column_lds(R, K, T) || MatvecPlan(R, K, T, sparse).pieces < (int64_t)1 << 32;
 }
 
 size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse) {
