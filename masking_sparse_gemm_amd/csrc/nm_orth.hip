@@ -27,6 +27,7 @@
 #include <cmath>
 
 #include "nm_gemm.h"
+#include "nm_tiles.h"
 
 namespace nm {
 namespace {
@@ -357,41 +358,6 @@ __global__ void __launch_bounds__(G::kThreads) orth_kernel(OrthArgs p) {
   }
 }
 
-// Square tiles of four sizes; a launch takes the one with the smallest estimated time: rounds of
-// tiles over the 256 units, times the steps of 64 k at the time a step takes on a full device, plus
-// a fixed time (fill of the pipeline, epilogue).  Large tiles read less per product, small ones
-// fill the device, and the smallest fits on a unit twice; symmetric results have only the tiles on
-// and below the diagonal, whose number is what matters: 4096 x 4096 in 256s is 136 tiles for 256
-// units, in 192s 253.  Measured (us for five steps with the symmetric products in 256 / 192 / 128
-// / 64, the update in its pick): 4096 x 11008 3566 / 3324 / 4002 / 4944, 2048 x 8192 1456 / 1106 /
-// 874 / 955, 1536 x 6144 1020 / 750 / 556 / 480, 1024 x 4096 680 / 482 / 345 / 241.  With the
-// update in each, the symmetric ones in their pick: 3315 / 3556 / 3818 / 4488, 868 / 931 / 1004 /
-// 1094, 583 / 552 / 656 / 638, 337 / 276 / 244 / 262.
-struct OrthTile {
-  int size, per_unit;
-  float step_us, fixed_us;
-};
-constexpr OrthTile kOrthTiles[] = {
-    {256, 1, 1.85f, 11.f}, {192, 1, 1.15f, 8.f}, {128, 1, 0.5f, 4.5f}, {64, 2, 0.25f, 3.5f}};
-constexpr OrthTile kOrthSplitTiles[] = {{128, 1, 1.1f, 5.f}, {64, 1, 0.45f, 4.f}};
-
-template <int N>
-int pick_orth_tile(const OrthTile (&tiles)[N], int64_t rows, int64_t cols, int steps, bool lower) {
-  int best = tiles[0].size;
-  double least = 1e30;
-  for (const OrthTile& t : tiles) {
-    const int64_t m = (rows + t.size - 1) / t.size, n = (cols + t.size - 1) / t.size;
-    const int64_t count = lower ? m * (m + 1) / 2 : m * n;
-    const double rounds = (double)((count * t.per_unit + 255) / 256) / t.per_unit;
-    const double us = (rounds < 1 ? 1 : rounds) * (steps * (double)t.step_us + t.fixed_us);
-    if (us < least) {
-      least = us;
-      best = t.size;
-    }
-  }
-  return best;
-}
-
 template <class G, int KIND, bool SPLIT>
 hipError_t launch_orth_tile(OrthArgs p, hipStream_t s) {
   // A and B are symmetric: their tiles above the diagonal are written by those below it
@@ -418,8 +384,6 @@ hipError_t launch_orth_product(const OrthArgs& p, hipStream_t s) {
     return launch_orth_tile<Gemm<2, 2, 1, 1, AS, BS, false, true, 4>, KIND, false>(p, s);
   }
 }
-
-int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
 // Workspace parts, in bytes.
 struct OrthLayout {

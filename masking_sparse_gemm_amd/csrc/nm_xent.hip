@@ -27,16 +27,13 @@
 
 #include "nm_gemm.h"
 #include "nm_grid.h"
+#include "nm_tiles.h"
 
 namespace nm {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int64_t kPieceBytes = 64 << 20;  // of P
-constexpr int kMaxSplit = 32;
-
-int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 int64_t pad256b(int64_t n) { return (n + 255) / 256 * 256; }
 
 struct TokenArgs {  // of the tokens, padded to a whole number of 64
@@ -175,12 +172,6 @@ hipError_t launch_pad(const PadArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The products' tiles.  256 x 256 is the fastest on many large tiles; of 128 x 128 two fit a unit,
-// so that one's epilogue runs under the other's steps, and short or few sums are faster in them;
-// 128 x 64 suits few tokens.
-enum XentTile { kTile256, kTile128, kTileNarrow, kXentTiles };
-constexpr int kTileM[kXentTiles] = {256, 128, 128}, kTileN[kXentTiles] = {256, 128, 64};
-
 template <class G>
 struct TileTag {
   typedef G type;
@@ -190,30 +181,6 @@ hipError_t with_tile(int tile, F&& f) {
   if (tile == kTile256) return f(TileTag<Gemm<2, 4, 4, 2, AS, BS, BF16, SWAP, 2>>{});
   if (tile == kTile128) return f(TileTag<Gemm<2, 4, 2, 1, AS, BS, BF16, SWAP, 2>>{});
   return f(TileTag<Gemm<2, 2, 2, 1, AS, BS, BF16, SWAP, 3>>{});
-}
-
-int64_t tiles_of(int tile, int64_t m, int64_t n) {
-  return ((m + kTileM[tile] - 1) / kTileM[tile]) * ((n + kTileN[tile] - 1) / kTileN[tile]);
-}
-
-// Estimated time (us) of `count` tiles of `steps` steps: whole rounds of 256 for the large tile,
-// and 512 at a time in a steady flow for the small ones, but never less than one tile alone.
-// Measured, 256 / 128 / narrow: loss 32768 x 4096, 2048 tokens 522 / 611 / 731 us; 20000 x 1024,
-// 1000 tokens 74 / 58 / 71; 12000 x 2048, 128 tokens 54 / 25 / 17; 30000 x 4096, 32 tokens
-// 99 / 62 / 41; dW of 12000 x 2048, 128 tokens 21 / 17 / 23.
-double tile_us(int tile, int64_t count, int64_t steps) {
-  if (tile == kTile256) return (double)((count + 255) / 256) * (2.0 * steps + 8.0);
-  const bool mid = tile == kTile128;
-  const double alone = mid ? 0.65 * steps + 4.0 : 0.45 * steps + 3.0;
-  const double flow = (double)count / 512 * (mid ? 1.19 * steps + 4.6 : 0.71 * steps + 3.5);
-  return alone > flow ? alone : flow;
-}
-
-int pick_tile(int64_t m, int64_t n, int64_t steps) {
-  int best = 0;
-  for (int t = 1; t < kXentTiles; ++t)
-    if (tile_us(t, tiles_of(t, m, n), steps) < tile_us(best, tiles_of(best, m, n), steps)) best = t;
-  return best;
 }
 
 // ---- loss ------------------------------------------------------------------------------
@@ -561,23 +528,10 @@ struct GradLayout {
     Kp = pad64(K);
     Tp = pad64(T);
     copy_w = K % 64 != 0;
-    piece = kPieceBytes / (2 * Tp) / 256 * 256;
-    if (piece < 256) piece = 256;
-    if (piece > V) piece = V;
-    // dX's sums over the piece are split where its tiles are too few; each split costs a write
-    // and a read of its sums (5 GB a ms)
-    const int64_t steps = (piece + 63) / 64;
-    double least = 1e30;
-    for (int t = 0; t < kXentTiles; ++t)
-      for (int z = 1; z <= kMaxSplit && (z == 1 || steps / z >= 4); z = z < 4 ? z + 1 : z + 2) {
-        const double us = tile_us(t, tiles_of(t, K, Tp) * z, (steps + z - 1) / z) +
-                          (double)z * K * Tp * 8 / 5e6;
-        if (us < least) {
-          least = us;
-          tile_x = t;
-          splits = z;
-        }
-      }
+    const XentGradCut cut(V, K, T);
+    piece = cut.piece;
+    tile_x = cut.tile_x;
+    splits = cut.splits;
     x = 0;
     x_down = x + pad256b(Kp * Tp * 2);
     w = x_down + pad256b(Kp * Tp * 2);
