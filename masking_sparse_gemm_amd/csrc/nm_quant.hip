@@ -15,6 +15,7 @@
 #include "nm_grid.h"
 #include "nm_launch.h"
 #include "nm_mfma.h"
+#include "nm_tiles.h"
 
 namespace nm {
 namespace {
@@ -327,8 +328,6 @@ __device__ __forceinline__ float4_t mfma_sparse(const u32x4_t& a, const u32x4_t&
                                                     __builtin_bit_cast(f16x16_t, b), c, (int)idx,
                                                     0, 0);
 }
-
-constexpr int kColumnPad = 64;  // bytes: four columns of X apart are on all banks of LDS
 
 struct MatvecArgs {
   const uint8_t* codes;
@@ -652,23 +651,6 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (row + i < R) store_from_f32<YT>(y, (row + i) * T + col, total[i]);
-}
-
-// Bytes of LDS that X's columns take in matvec_kernel, 0 where slices of them are better.  Every
-// workgroup lays out all of X, at a cost of K T for each that a unit gets (two at a time where they
-// fit), so rows and columns are bounded together.  Measured, us, whole / slices: 4096 x 4096, 2
-// columns 4.7 / 10.0, 5 5.5 / 9.6, 8 6.4 / 7.1; 2:4 4096 x 11008, 5 columns 9.4 / 12.0; 2:4 11008 x
-// 4096, 7 columns 11.4 / 13.2, 8 12.2 / 9.5; 16384 x 8192, 2 columns 19.7 / 23.9, 3 20.5 / 21.7, 5
-// 34.5 / 21.8; 5003 x 11007, 2 columns 13.1 / 15.8, 4 21.1 / 15.6.
-constexpr int kFewColumns = 8;
-constexpr int64_t kFewLds = 128 << 10;
-int64_t column_lds(int64_t R, int64_t K, int64_t T) {
-  const int64_t column = std::max<int64_t>(1, (K + 255) / 256) * 512;
-  if (T == 1) return column <= 64 << 10 ? column : 0;
-  const int64_t groups = (R + 15) / 16, all = T * (column + kColumnPad);
-  if (T > kFewColumns || all > kFewLds) return 0;
-  const double rounds = all <= 80 << 10 ? std::max(1.0, groups / 256.0) : (double)((groups + 255) / 256);
-  return rounds * (double)(K * T) <= 80 << 10 ? all : 0;
 }
 
 // How several columns are cut.  Each workgroup reads X's rows of its slice, so rows are shared by

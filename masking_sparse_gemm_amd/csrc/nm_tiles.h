@@ -1,14 +1,40 @@
-// nm_tiles.h -- which tile a dense product of the cross entropy or of the orthogonalised update
-// takes, and how the cross entropy's gradient is cut.  Plain C++ with no HIP types, so that a host-only
-// test can compile it and say which kernels a size runs.
+// nm_tiles.h -- which kernel a 4-bit product takes, which tile a dense product of the cross entropy or
+// of the orthogonalised update takes, and how the cross entropy's gradient is cut.  Plain C++ with no
+// HIP types, so that a host-only test can compile it and say which kernels a size runs.
 #ifndef NM_TILES_H
 #define NM_TILES_H
 
+#include <algorithm>
 #include <cstdint>
 
 namespace nm {
 
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
+
+// ---- 4-bit products ------------------------------------------------------------------------------
+
+// Bytes of LDS that X's columns take in matvec_kernel, 0 where slices of them are better.  Every
+// workgroup lays out all of X, at a cost of K T for each that a unit gets (two at a time where they
+// fit), so rows and columns are bounded together; eight columns, of which the slices lay out whole
+// 16-byte pieces, at less.  Measured with weights out of cache, us, whole / slices: 4096 x 4096, 2
+// columns 5.4 / 11.2, 5 6.2 / 10.8; 2:4 4096 x 11008, 5 columns 11.2 / 14.6; 2:4 11008 x 4096, 7 columns
+// 14.4 / 16.2; 16384 x 8192, 2 columns 22.8 / 29.6, 3 24.3 / 25.9, 5 40.5 / 26.1; 5003 x 11007, 2
+// columns 16.7 / 18.4, 3 17.6 / 16.2, 4 24.4 / 17.9.  Eight columns, one round: 4096 x 4096 7.1 / 8.8,
+// 4096 x 6144 9.3 / 12.0, 64 x 6144 7.8 / 7.1, 1024 x 7168 9.5 / 7.6, 4096 x 7168 10.4 / 11.5; more: 2:4
+// 8192 x 2048 7.0 / 7.8, 12288 x 2048 9.4 / 9.2, 2:4 4608 x 4096 10.8 / 9.4, 2:4 8192 x 4096 11.1 / 9.6,
+// 2:4 11008 x 4096 15.2 / 12.8, 24576 x 1024 9.4 / 8.0.
+constexpr int kColumnPad = 64;  // bytes: four columns of X apart are on all banks of LDS
+constexpr int kFewColumns = 8;
+constexpr int64_t kFewLds = 128 << 10;
+inline int64_t column_lds(int64_t R, int64_t K, int64_t T) {
+  const int64_t column = std::max<int64_t>(1, (K + 255) / 256) * 512;
+  if (T == 1) return column <= 64 << 10 ? column : 0;
+  const int64_t groups = (R + 15) / 16, all = T * (column + kColumnPad);
+  if (T > kFewColumns || all > kFewLds) return 0;
+  const double rounds = all <= 80 << 10 ? std::max(1.0, groups / 256.0) : (double)((groups + 255) / 256);
+  const int most = T % 8 != 0 ? 80 << 10 : rounds > 1 ? 32 << 10 : 48 << 10;
+  return rounds * (double)(K * T) <= most ? all : 0;
+}
 
 // ---- cross entropy ---------------------------------------------------------------------------
 

@@ -60,3 +60,29 @@ def test_sums_of_long_rows(R, K, T, group, sparse, dtype):
                 bound = bound + 2.0 ** -25
         off = (y.double() - want).abs()
         assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("R,K,sparse", [(4700, 4096, True), (4700, 4096, False), (16400, 2048, True),
+                                        (100, 7168, True), (200, 6144, False)])
+def test_eight_columns_whole_and_in_slices(R, K, sparse):
+    """Eight columns on both sides of the rule that parts them; some rows of each."""
+    dtype, group = torch.bfloat16, 64
+    w, x = weights(R, K, dtype), weights(K, 8, torch.float64, 5).mul(50).to(dtype)
+    at, meta = None, None
+    some = torch.arange(0, R, max(1, R // 40))
+    if sparse:
+        at = nm.mask(w.cuda(), 2, 4).cpu().nonzero()[:, 1].view(R, K // 2)
+        values, meta = nm.compress(w.cuda(), 2, 4, layout="blocked")
+        codes, scales = nm.quantize(values, group, layout="blocked", rows=R)
+    else:
+        codes, scales = nm.quantize(w.cuda(), group)
+    y = nm.matvec(codes, scales, x.cuda(), group, rows=R, meta=meta, out_dtype=torch.float32).cpu()
+    stored = w[some] if at is None else w[some].gather(1, at[some])
+    q, s = plain_quantize(stored, group, dtype)
+    C = q.shape[1]
+    v = q.double() * s.double().repeat_interleave(group, 1)[:, :C]
+    if sparse:
+        v = torch.zeros(len(some), K, dtype=torch.float64).scatter_(1, at[some], v)
+    n = 32 + group // 32 + 1 + -(-C // group) + 16 + -(-K // 2048)
+    off = (y[some].double() - v @ x.double()).abs()
+    assert (off <= n * 2.0 ** -23 * (v.abs() @ x.double().abs())).all()

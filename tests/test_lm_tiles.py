@@ -32,6 +32,8 @@ int main() {
       const bool both = dw == kTile128 && cut.tile_x == kTile128;
       std::printf("%s %s %s %s %d %ld\n", names[loss], names[prob], both ? "both" : names[dw],
                   both ? "both" : names[cut.tile_x], cut.splits, (R + cut.piece - 1) / cut.piece);
+    } else if (op == 'm') {  // R, K, T
+      std::printf("%s\n", column_lds(R, K, n) ? "whole" : "slices");
     } else {  // R, K, one part or two
       const long rp = pad64(R), kp = pad64(K), mp = R > K ? kp : rp, sum = R > K ? rp : kp;
       const auto pick = [&](long rows, long cols, long k, bool lower) {
@@ -76,3 +78,16 @@ def test_orthogonalize_sizes_take_their_tiles(tmp_path):
         assert {128, 192, 256} <= {w[2] for w in one}
         two = [w for (R, K, dt), w in ORTH.items() if dt != torch.bfloat16 and (R > K) == tall]
         assert (128, 128, 128) in two
+
+
+# what measured faster: X's columns whole in LDS, or slices of them
+MATVEC = {(4096, 4096, 1): "whole", (4096, 4096, 8): "whole", (8192, 2048, 8): "whole",
+          (4096, 6144, 8): "whole", (1024, 7168, 8): "slices",
+          (4608, 4096, 8): "slices", (8192, 4096, 8): "slices", (24576, 1024, 8): "slices",
+          (11008, 4096, 7): "whole", (11008, 4096, 8): "slices", (16384, 8192, 2): "whole",
+          (16384, 8192, 5): "slices", (4096, 4096, 9): "slices", (40, 40001, 1): "slices"}
+
+
+def test_few_columns_go_the_faster_way(tmp_path):
+    got = answers(tmp_path, ["m %d %d %d" % size for size in MATVEC])
+    assert {size: a for size, (a,) in zip(MATVEC, got)} == MATVEC
