@@ -95,7 +95,8 @@ extern "C" {
 typedef enum NM_INT_ENUM {
   NM_OK = 0,
   NM_ERR_NULL = 1,        /* a required pointer is NULL                              */
-  NM_ERR_SHAPE = 2,       /* negative size, K not a multiple of M, or R*K >= 2^36    */
+  NM_ERR_SHAPE = 2,       /* negative size, K not a multiple of M, R*K >= 2^36, or a
+                             size or number past the limits that a call states       */
   NM_ERR_PATTERN = 3,     /* N:M outside 1 <= N <= M, M in {2, 4, 8}                 */
   NM_ERR_DTYPE = 4,       /* unknown dtype, y_dt not allowed for dt, or int8 where a
                              floating-point weight is required                       */
@@ -335,7 +336,8 @@ nm_status nm_perm_search(const void* W, nm_dtype dt, int64_t R, int64_t K, int n
  *   scale = max |w| / 7 over the group, rounded to the scales' type;
  *   code  = w / scale rounded to an integer (ties to even), held within -8 .. 7;
  * and a code stands for scale * code.  A group of zeros (or whose scale rounds to 0) has scale 0
- * and codes 0; a group that holds a NaN or an infinity has that as its scale, and stands for NaN.
+ * and codes 0; a group that holds a NaN or an infinity has that as its scale, and stands for NaN, as
+ * does one whose scale rounds to infinity (NM_F16 scales of |w| past 458,000).
  *
  *   codes   nm_codes_bytes(R, C) bytes.  Blocks of 16 rows x 128 columns, row after row of
  *           blocks, 1 KB each (S = ceil(C / 128) blocks to 16 rows): 32-bit word
@@ -383,8 +385,8 @@ nm_status nm_matvec(const void* codes, const void* scales, const uint32_t* meta,
  *   lse[t]  = log sum over v of exp L[v, t]       (of every token; +infinity where a logit is)
  *   loss[t] = lse[t] - L[target[t], t]
  * loss and lse are fp32; sums are fp32.  V >= 1 where T > 0, V < 2^31, K < 2^22, T < 2^22,
- * V*K, V*T and K*T < 2^36, else NM_ERR_SHAPE.  Fastest where K % 64 == 0 (else W is copied, padded, into the workspace)
- * and T % 8 == 0. */
+ * V*K, V*T and K*T < 2^36, else NM_ERR_SHAPE.  Fastest where K % 64 == 0 (else W is copied, padded,
+ * into the workspace) and T % 8 == 0. */
 size_t nm_xent_workspace_bytes(int64_t V, int64_t K, int64_t T);
 nm_status nm_xent(const void* W, const void* X, nm_dtype dt, int64_t V, int64_t K, int64_t T,
                   const int64_t* target, float* loss, float* lse, void* workspace,

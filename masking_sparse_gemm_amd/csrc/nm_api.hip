@@ -101,7 +101,7 @@ const char* nm_status_str(nm_status s) {
   switch (s) {
     case NM_OK: return "ok";
     case NM_ERR_NULL: return "null pointer";
-    case NM_ERR_SHAPE: return "bad shape (negative size, K not a multiple of M, or R*K >= 2^36)";
+    case NM_ERR_SHAPE: return "bad shape (negative size, K not a multiple of M, R*K >= 2^36 or past the call's limits)";
     case NM_ERR_PATTERN: return "bad N:M pattern (need 1 <= N <= M, M in {2,4,8})";
     case NM_ERR_DTYPE: return "bad dtype (unknown, or output neither input dtype nor fp32)";
     case NM_ERR_ALIGN: return "pointer not 16-byte aligned";
@@ -109,7 +109,7 @@ const char* nm_status_str(nm_status s) {
     case NM_ERR_DEVICE: return "device error (no gfx950 device, or launch failed)";
     case NM_ERR_LAYOUT: return "bad layout (unknown, or blocked layout with K not a multiple of 64)";
     case NM_ERR_ALIAS: return "an output overlaps an input it may not replace";
-    case NM_ERR_SCRATCH: return "the call needs more than the library's static scratch buffer";
+    case NM_ERR_SCRATCH: return "the call needs more scratch than the static buffer or the given workspace";
   }
   return "unknown status";
 }
