@@ -19,8 +19,8 @@
 //   strided: a row of the tile's columns for each k, 32-byte pair p at p ^ 2 (k & 3); a
 //     fragment is two transposing reads (ds_read_b64_tr_b16).
 // Bound, large tiles: the power that the matrix cores draw and the waits at a step's end; 256 x 256
-// tiles keep them busy 57 to 60 % of the time at a clock that the load pulls down to 1.9 GHz (32768 x
-// 4096 x 2048 bf16 in 478 us, 1150 TFLOP/s).  Small tiles: the barrier and the LDS latency of each
+// tiles keep them busy 58 to 62 % of the time at a clock that the load pulls down to 1.8 to 1.9 GHz
+// (32768 x 4096 x 2048 bf16 in 466 us, 1180 TFLOP/s).  Small tiles: the barrier and the LDS latency of each
 // 16 k, 0.25 us a step of 64 x 64 against 0.06 of products.  Measured on the way: more stages than
 // these change nothing, four waves on 128 x 128 and sixteen on 256 x 256 are 2 to 10 % slower, fewer
 // bank conflicts and reads between products gave 5 %, the loop's inner steps without tests up to 8 %.

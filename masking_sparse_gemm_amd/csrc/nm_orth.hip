@@ -19,10 +19,10 @@
 //     hi lo + lo hi in the same accumulators, as exact as fp32 products.
 // The norm is summed in fp64, so no finite G overflows or vanishes in it.
 //
-// Bound by the matrix cores on large G: a step of 4096 x 11008 in bf16 is 196 us of X X^T (940
-// TFLOP/s of the half that is computed), 81 of A A and 388 of the update (950; its 688 tiles are
+// Bound by the matrix cores on large G: a step of 4096 x 11008 in bf16 is 191 us of X X^T (970
+// TFLOP/s of the half that is computed), 79 of A A and 356 of the update (1040; its 688 tiles are
 // three rounds of 256 units for 2.7).  On small G by the chain of 3 launches a step: 256 x 384 takes
-// 5.0 to 5.8 us for each, of which a launch after another is 1.6 and the rest one tile's latency.
+// 4.8 to 5.7 us for each, of which a launch after another is 1.6 and the rest one tile's latency.
 #include <algorithm>
 #include <cmath>
 

@@ -25,8 +25,8 @@ constexpr int kBlockCols = 128;       // stored columns of a block of codes
 // ---------------------------------------------------------------------------------------
 // nm_quantize: one wave per block of 16 rows x 128 columns; lane 16 j + r reads its 32
 // elements, the four lanes of a row share the group maxima by lane exchange.  One pass, bound by
-// memory: 11008 x 2048 kept values of bf16 take 11.6 us (57 MB, 4.9 TB/s; a large copy reaches
-// 5.2), 768 x 768 4.3 us, which is a launch.
+// memory: 11008 x 2048 kept values of bf16 take 10.8 us (57 MB, 5.3 TB/s; a large copy reaches
+// 5.2), 768 x 768 4.0 us, which is a launch.
 // ---------------------------------------------------------------------------------------
 
 template <int DT>
@@ -61,7 +61,7 @@ typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
 // Eight elements of a row from column c, as they are stored; zeros past column C.  kWhole: C % 8
 // == 0, so the eight are wholly inside or outside and their address is 16-byte aligned; else eight
 // that lie inside are read as they stand and only a row's last ones one by one (quantize and
-// dequantize of 4096 x 4100 bf16: 11.5 and 13.2 us, 27.1 and 40.3 with all one by one).
+// dequantize of 4096 x 4100 bf16: 11.6 and 13.0 us, 27.1 and 40.3 with all one by one).
 template <int DT>
 struct Eight {
   static constexpr int kWords = DT == kF32 ? 8 : 4;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------------------
 // nm_dequantize: the same assignment of columns to lanes, s q rounded once to the scales' type.
-// Bound by memory: 11008 x 2048 values of bf16 in 11.6 us (57 MB, 4.9 TB/s).
+// Bound by memory: 11008 x 2048 values of bf16 in 11.2 us (57 MB, 5.1 TB/s).
 // ---------------------------------------------------------------------------------------
 template <bool BF16S, bool kBlocked, bool kWhole>
 __global__ void __launch_bounds__(256)
@@ -413,8 +413,8 @@ struct CodeBlock {
 // past the last hold the last again and are dropped.  Blocks past the matrix's last columns hold
 // code 0 against zeros of X, so there are no ends to treat.
 // Bound by the first loads' latency on small matrices, from there by the few loads that a unit keeps
-// in flight: one column 4096 x 4096 4.9 us (1.8 TB/s), 4096 x 11008 8.9 (2.7), 16384 x 12288
-// 27.3 (3.9); two columns of 4096 x 4096 4.7 us with the codes in cache.
+// in flight: one column 4096 x 4096 4.7 us (1.9 TB/s), 4096 x 11008 8.0 (3.0), 16384 x 12288
+// 23.2 (4.6); two columns of 4096 x 4096 5.4; the smaller ones' codes are in cache.
 template <bool BF16, bool SPARSE, int LOG_GROUP, int WAVES, bool FEW, int YT>
 __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
   constexpr int kEights = SPARSE ? 8 : 4;  // eights of X's rows to a step
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
 // With more than one slice the sums go to the workspace, where join_slices_kernel adds them in
 // slice order.
 // Bound by laying out X, which every workgroup does for its slice, and by the launch of the second
-// kernel (3.8 us): 2:4 4096 x 11008 with 32 columns 13.2 us and the join, 5003 x 11007 with 5 columns
-// 14.2 us and the join, 16384 x 8192 with 32 columns 34.5 us in all (2.1 TB/s).
+// kernel (4 us): 2:4 4096 x 11008 with 32 columns 13.0 us and the join, 5003 x 11007 with 5 columns
+// 13.8 us and the join, 16384 x 8192 with 32 columns 26.1 us and the join (2.4 TB/s in all).
 constexpr int kSliceWaves = 8;
 
 template <bool BF16, bool SPARSE, int LOG_GROUP, int NT, int YT>

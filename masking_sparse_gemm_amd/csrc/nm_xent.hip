@@ -16,10 +16,10 @@
 // loses no more to underflow than any other's, and brings the rest of its g to dW as a power of two
 // on its column of X.
 //
-// Bound by the matrix cores where tokens are many: 32768 x 4096 with 2048 tokens in bf16 takes 474
-// us for the loss's product (1160 TFLOP/s), and for the gradient's three, in two pieces, 478, 476 and
-// 482 us (1150), with 41 us of copies and joins beside them.  With few tokens the loss is bound by the
-// read of W (32000 x 768, 61 tokens: 13.6 us, 3.6 TB/s) and the launches.
+// Bound by the matrix cores where tokens are many: 32768 x 4096 with 2048 tokens in bf16 takes 469
+// us for the loss's product (1170 TFLOP/s), and for the gradient's three, in two pieces, 464, 467 and
+// 466 us (1180), with 43 us of copies and joins beside them.  With few tokens the loss is bound by the
+// read of W (32000 x 768, 61 tokens: 13.8 us, 3.6 TB/s) and the launches.
 //
 // Tokens with a target outside 0 .. V - 1 are left out: their loss is 0 and their column of X
 // is read as zeros in the gradient, so that not even infinities or NaN in it reach dW.
