@@ -415,6 +415,108 @@ size_t nm_orthogonalize_workspace_bytes(int64_t R, int64_t K, nm_dtype dt);
 nm_status nm_orthogonalize(const void* G, nm_dtype dt, int64_t R, int64_t K, int steps, float eps,
                            void* out, void* workspace, size_t workspace_bytes, nm_stream_t stream);
 
+/* ---- a product with its epilogue, and the gradient ------------------------------------------
+ *
+ * Z = s (W_sparse X) + b,  Y = act(Z) + residual: nm_spmm with what a layer does to its result, on the
+ * product's fp32 sums (int32 for NM_I8), each of Z and Y rounded once.  The activations:
+ *   NM_ACT_RELU      max(Z, 0)                NM_ACT_RELU2      max(Z, 0)^2
+ *   NM_ACT_SILU      Z / (1 + e^-Z)           NM_ACT_GELU       Z Phi(Z), Phi the normal distribution's
+ *   NM_ACT_GELU_TANH Z (1 + tanh(sqrt(2 / pi) (Z + 0.044715 Z^3))) / 2
+ * -infinity gives 0 in each, NaN stays NaN. */
+typedef enum NM_INT_ENUM {
+  NM_ACT_NONE = 0, NM_ACT_RELU = 1, NM_ACT_RELU2 = 2, NM_ACT_SILU = 3, NM_ACT_GELU = 4,
+  NM_ACT_GELU_TANH = 5
+} nm_act;
+
+/* Arguments as nm_spmm, every pattern, layout and T, and:
+ *   scale     R fp32 numbers, one a row, of NM_I8 and NM_FP8 alone (else NULL, or NM_ERR_DTYPE); NULL: 1
+ *   bias      R fp32 numbers, or NULL
+ *   residual  R x T in y_dt, or NULL; may be Y itself, which is then added to
+ *   Z         R x T in dt, the activation's argument as nm_spmm_act_grad takes it, or NULL (NM_I8 and
+ *             NM_FP8: NULL, or NM_ERR_DTYPE)
+ * y_dt is dt or NM_F32, and for NM_I8 and NM_FP8 one of NM_F32, NM_F16 and NM_BF16.  Sums as nm_spmm
+ * forms them (NM_I8: K < 2^17, exact, then one rounding to fp32).  K = 0 gives Z = b.
+ * workspace: nm_spmm_act_workspace_bytes(K, T, dt) bytes of device memory, whose contents do not
+ * matter: 0 where rows of X are whole 16-byte pieces, else room for X with longer rows. */
+size_t nm_spmm_act_workspace_bytes(int64_t K, int64_t T, nm_dtype dt);
+nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
+                      nm_layout layout, const void* X, int64_t T, nm_dtype dt, const float* scale,
+                      const float* bias, nm_act act, const void* residual, void* Z, void* Y,
+                      nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream);
+
+/* The gradient of nm_spmm_act for dt NM_F16 or NM_BF16, from dY (R x T) and, where there is an
+ * activation, Z:
+ *   dZ = act'(Z) dY (R x T),  dbias[r] = sum over t of dZ[r, t] (fp32, of the sums before rounding),
+ *   dW = dZ X^T (R x K: of the dense weight, as nm_srste_grad takes it),  dX = W_sparse^T dZ (K x T)
+ * all but dbias in dt; the residual's gradient is dY itself.  act' of RELU and RELU2 is 0 at 0.
+ * Each of dW, dX, dbias and dZ may be NULL and is then not computed; X is needed for dW, values and meta
+ * for dX alone, Z only with an activation (each else NULL if one likes).  dZ is rounded to dt before
+ * the products, whose sums are fp32 and rounded once.  R, K, T < 2^22, R*T and K*T < 2^36, else
+ * NM_ERR_SHAPE.  Fastest where R and T are multiples of 64.
+ * workspace: nm_spmm_act_grad_workspace_bytes of the sizes, of which results are wanted, and of
+ * whether there is an activation. */
+size_t nm_spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_act act, int want_dW,
+                                        int want_dX, int want_dZ);
+nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                           int m, nm_layout layout, const void* X, int64_t T, nm_dtype dt, nm_act act,
+                           const void* Z, const void* dY, void* dW, void* dX, float* dbias, void* dZ,
+                           void* workspace, size_t workspace_bytes, nm_stream_t stream);
+
+/* nm_matvec with the same epilogue, Y = act(Wq X + b) + residual, for one column or a few: bias R fp32
+ * numbers or NULL, residual R x T in y_dt or NULL (may be Y).  Everything else as nm_matvec, its
+ * workspace (nm_matvec_workspace_bytes) too. */
+nm_status nm_matvec_act(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
+                        int64_t K, int group, const void* X, int64_t T, nm_dtype dt, const float* bias,
+                        nm_act act, const void* residual, void* Y, nm_dtype y_dt, void* workspace,
+                        size_t workspace_bytes, nm_stream_t stream);
+
+/* ---- gradients' norm and clipping ---------------------------------------------------------
+ *
+ * norm = sqrt(sum of g^2 over every entry of `tensors` tensors), one fp32 number on the device.
+ * grads, outs, counts and dts are HOST arrays, read before the call returns: device pointers, numbers of
+ * entries and types (NM_F32, NM_F16 or NM_BF16, mixed as one likes).  A pointer needs its element's
+ * alignment only; a tensor without entries is left out.  Squares are summed in fp64 (eight at a time in
+ * fp32 where they fit), so no finite gradient overflows; a norm past fp32 is +infinity, and NaN and
+ * infinities show in it.  At most 2^20 tensors of less than 2^40 entries each, else NM_ERR_SHAPE. */
+size_t nm_grad_norm_workspace_bytes(const int64_t* counts, int64_t tensors);
+nm_status nm_grad_norm(const void* const* grads, const int64_t* counts, const nm_dtype* dts,
+                       int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
+                       nm_stream_t stream);
+
+/* out = g * (max_norm / norm), rounded once, where max_norm < norm < infinity, and g itself else.
+ * outs[i] may be grads[i] (and is then not written where nothing is clipped); any other overlap of what is
+ * written returns NM_ERR_ALIAS, the same tensor given twice among them.  given: NULL, or a norm to
+ * clip by, one fp32 number on the device (every rank's, joined); with NULL the tensors' own norm is
+ * taken and written to norm.  max_norm >= 0, else NM_ERR_SHAPE.  workspace as nm_grad_norm, none with a
+ * given norm. */
+nm_status nm_clip_grads(const void* const* grads, void* const* outs, const int64_t* counts,
+                        const nm_dtype* dts, int64_t tensors, float max_norm, const float* given,
+                        float* norm, void* workspace, size_t workspace_bytes, nm_stream_t stream);
+
+/* ---- penalties, biases and masks on logits ---------------------------------------------------
+ *
+ * Logits V x T (dt NM_F32, NM_F16 or NM_BF16), a column a sequence, as nm_matvec leaves them.  Column t's
+ * tokens are entries starts[t] .. starts[t + 1] - 1 of tokens (int64, `count` of them; starts has T + 1
+ * entries); the first prompts[t] of them are its prompt.  Of a word v that stands in them, a times
+ * after the prompt:
+ *   x = x > 0 ? x / repetition[t] : x * repetition[t]
+ *   x = x - presence[t] (if a > 0) - frequency[t] * a
+ * and then of every word
+ *   x = x + bias (V fp32 numbers, or V x T with bias_each != 0)
+ *   x = -infinity where bit v % 32 of allowed[t * ceil(V / 32) + v / 32] is 0
+ * in fp32, rounded once.  out may be logits.  Each of tokens (with starts), prompts, repetition,
+ * presence, frequency, bias and allowed may be NULL and is then left out.  Tokens outside 0 .. V - 1 and
+ * ranges outside the `count` tokens are passed over; a mask may leave a column nothing but -infinity.
+ * V < 2^31, T < 2^20, V*T < 2^36, count < 2^31, else NM_ERR_SHAPE.
+ * workspace: nm_adjust_logits_workspace_bytes(V, T, count) bytes (0 where the histories are short). */
+size_t nm_adjust_logits_workspace_bytes(int64_t V, int64_t T, int64_t count);
+nm_status nm_adjust_logits(const void* logits, nm_dtype dt, int64_t V, int64_t T,
+                           const int64_t* tokens, int64_t count, const int64_t* starts,
+                           const int64_t* prompts, const float* repetition, const float* presence,
+                           const float* frequency, const float* bias, int bias_each,
+                           const uint32_t* allowed, void* out, void* workspace,
+                           size_t workspace_bytes, nm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,12 @@ library functions raises.
     codes, scales = quantize(v, 64, layout="blocked", rows=R)
     y = matvec(codes, scales, x, 64, rows=R, meta=m)
 
+    y, z = spmm_act(values, meta, X, bias=b, act="silu", residual=x, keep=True)   # act(W X + b) + x
+    dW, dX, db = spmm_act_grad(values, meta, X, dY, z, act="silu")
+    y = matvec_act(codes, scales, x, 64, rows=R, act="gelu")    # the same for a few tokens, 4 bits
+    norm = clip_grads([dW, db], max_norm=1.0)                   # in place; grad_norm for the norm alone
+    logits = adjust_logits(logits, tokens, starts, repetition=r, bias=b, allowed=grammar)
+
 The compressed pair comes in two layouts (defined in include/nm.h): "rows"
 (values (R, K*n/m), meta (R, words)) and "blocked" (blocks of 16 rows x 64
 columns, the order the sparse product streams; values (G, S, 16, 64*n/m), meta
@@ -31,6 +37,8 @@ record R, so decompress and spmm take it as ``rows=``.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 
@@ -60,9 +68,15 @@ EXPORTS = ("nm_abi_version", "nm_status_str", "nm_values_bytes", "nm_meta_bytes"
            "nm_codes_bytes", "nm_scales_bytes", "nm_quantize", "nm_dequantize", "nm_matvec",
            "nm_matvec_workspace_bytes", "nm_xent", "nm_xent_workspace_bytes", "nm_xent_grad",
            "nm_xent_grad_workspace_bytes", "nm_orthogonalize",
-           "nm_orthogonalize_workspace_bytes")
+           "nm_orthogonalize_workspace_bytes",
+           "nm_spmm_act", "nm_spmm_act_workspace_bytes", "nm_spmm_act_grad",
+           "nm_spmm_act_grad_workspace_bytes", "nm_matvec_act", "nm_grad_norm",
+           "nm_grad_norm_workspace_bytes", "nm_clip_grads", "nm_adjust_logits",
+           "nm_adjust_logits_workspace_bytes")
 GROUPS = (32, 64, 128)   # stored columns that share a scale of the 4-bit codes
 STATIC_SCRATCH_BYTES = 64 << 20  # NM_STATIC_SCRATCH_BYTES
+# activations of a product's epilogue, by their nm_act codes
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
 SRSTE_DECAY = 0.0002  # the SR-STE page's default decay
 
 
@@ -124,12 +138,29 @@ def lib() -> ctypes.CDLL:
         L.nm_xent_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, size, vp]
         L.nm_orthogonalize_workspace_bytes.argtypes = [i64, i64, i32]
         L.nm_orthogonalize.argtypes = [vp, i32, i64, i64, i32, f32, vp, vp, size, vp]
+        L.nm_spmm_act_workspace_bytes.argtypes = [i64, i64, i32]
+        L.nm_spmm_act.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, vp, vp,
+                                  vp, i32, vp, size, vp]
+        L.nm_spmm_act_grad_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+        L.nm_spmm_act_grad.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, i32, vp, vp,
+                                       vp, vp, vp, vp, vp, size, vp]
+        L.nm_matvec_act.argtypes = [vp, vp, vp, i64, i64, i32, vp, i64, i32, vp, i32, vp, vp, i32,
+                                    vp, size, vp]
+        L.nm_grad_norm_workspace_bytes.argtypes = [vp, i64]
+        L.nm_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, size, vp]
+        L.nm_clip_grads.argtypes = [vp, vp, vp, vp, i64, f32, vp, vp, vp, size, vp]
+        L.nm_adjust_logits_workspace_bytes.argtypes = [i64, i64, i64]
+        L.nm_adjust_logits.argtypes = [vp, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, i32, vp,
+                                       vp, vp, size, vp]
         for f in ("nm_codes_bytes", "nm_scales_bytes", "nm_matvec_workspace_bytes",
                   "nm_xent_workspace_bytes", "nm_xent_grad_workspace_bytes",
-                  "nm_orthogonalize_workspace_bytes"):
+                  "nm_orthogonalize_workspace_bytes", "nm_spmm_act_workspace_bytes",
+                  "nm_spmm_act_grad_workspace_bytes", "nm_grad_norm_workspace_bytes",
+                  "nm_adjust_logits_workspace_bytes"):
             getattr(L, f).restype = size
         for f in ("nm_quantize", "nm_dequantize", "nm_matvec", "nm_xent", "nm_xent_grad",
-                  "nm_orthogonalize"):
+                  "nm_orthogonalize", "nm_spmm_act", "nm_spmm_act_grad", "nm_matvec_act",
+                  "nm_grad_norm", "nm_clip_grads", "nm_adjust_logits"):
             getattr(L, f).restype = i32
         for f in ("nm_mask", "nm_compress", "nm_decompress", "nm_spmm", "nm_prune",
                   "nm_srste_grad", "nm_tmask", "nm_tprune", "nm_compress_t", "nm_perm_gains",
@@ -688,4 +719,301 @@ def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7,
     _check("nm_orthogonalize", L.nm_orthogonalize(
         G.data_ptr(), dt, R, K, int(steps), float(eps), out.data_ptr(), ws_ptr,
         0 if ws is None else ws.numel(), _current_stream(G)))
+    return out
+
+
+# ---- a product with its epilogue, and the gradient --------------------------------------------
+
+
+def _device_of(t: torch.Tensor):
+    """t's device as the current one: the library launches on the current device."""
+    if torch._C._cuda_getDevice() == t.get_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _act(act: str) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    return code
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _expect(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, device) -> None:
+    """t, where it is given, is a contiguous tensor of that shape, type and device."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or
+                          t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}")
+
+
+def _row_numbers(t: torch.Tensor | None, name: str, rows: int, device):
+    """t, or its copy where it is a view that starts off 16 bytes."""
+    _expect(t, name, (rows,), torch.float32, device)
+    return None if t is None else _token_numbers(t)
+
+
+def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int = 2, m: int = 4,
+             bias: torch.Tensor | None = None, act: str = "none",
+             residual: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+             keep: bool = False, out_dtype: torch.dtype | None = None,
+             out: torch.Tensor | None = None, layout: str = "rows", rows: int | None = None):
+    """Y (R, T) = act(Z) + residual with Z = W_sparse @ X + bias: spmm with what a layer does to its
+    result in the product's epilogue, all in fp32 and rounded once.  act is one of ACTS; bias is
+    float32 (R,); residual (R, T) in Y's type may be out itself.  keep=True: (Y, Z), Z in X's type,
+    which spmm_act_grad takes.  int8 and float8 products take scale, float32 (R,): Z = scale *
+    (W_sparse @ X) + bias, and keep no Z.  out_dtype is X's type or float32, of int8 and float8
+    float32, float16 or bfloat16 (default bfloat16)."""
+    xdt = _dense_input(X, "X")
+    code = _act(act)
+    K, T = X.shape
+    dt, R = _check_compressed(values, meta, n, m, K, layout, rows)
+    if dt != xdt:
+        raise ValueError("values and X must have the same dtype")
+    if values.device != X.device:
+        raise ValueError("values and X must be on the same device")
+    eight = X.dtype in _BYTE
+    y_dtype = out_dtype or (torch.bfloat16 if eight else X.dtype)
+    if y_dtype not in _FLOAT or not (eight or y_dtype in (X.dtype, torch.float32)):
+        raise ValueError("out_dtype must be float32 or X's dtype (of int8 and float8: a float type)")
+    if scale is not None and not eight:
+        raise ValueError("scale goes with int8 and float8 products")
+    if keep and eight:
+        raise ValueError("int8 and float8 products keep no Z")
+    bias = _row_numbers(bias, "bias", R, X.device)
+    scale = _row_numbers(scale, "scale", R, X.device)
+    _expect(residual, "residual", (R, T), y_dtype, X.device)
+    _expect(out, "out", (R, T), y_dtype, X.device)
+    if out is None:
+        out = X.new_empty((R, T), dtype=y_dtype)
+    Z = X.new_empty((R, T)) if keep else None
+    L = lib()
+    with _device_of(X):
+        ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(K, T, dt))
+        _check("nm_spmm_act", L.nm_spmm_act(
+            values.data_ptr(), meta.data_ptr(), R, K, n, m, _layout(layout), X.data_ptr(), T, dt,
+            _addr(scale), _addr(bias), code, _addr(residual), _addr(Z), out.data_ptr(),
+            _DT[y_dtype], ws_ptr, 0 if ws is None else ws.numel(), _current_stream(X)))
+    return (out, Z) if keep else out
+
+
+GRADS = ("dW", "dX", "dbias", "dZ")
+
+
+def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: torch.Tensor | None,
+                  dY: torch.Tensor, Z: torch.Tensor | None = None, n: int = 2, m: int = 4,
+                  act: str = "none", layout: str = "rows", rows: int | None = None,
+                  want=("dW", "dX", "dbias")):
+    """The gradient of spmm_act for bfloat16 and float16, from dY (R, T) and the Z it kept (None
+    without an activation): those of "dW" (R, K, of the dense weight), "dX" (K, T), "dbias" (float32
+    (R,)) and "dZ" (R, T) that `want` names, in its order.  The residual's gradient is dY itself.
+    values and meta are needed for dX, X for dW (dX takes the width K from it, too); else None."""
+    code = _act(act)
+    want = tuple(want)
+    if not want or any(w not in GRADS for w in want):
+        raise ValueError(f"want must name some of {GRADS}")
+    _dense_input(dY, "dY", int8=False)
+    dt = _half(dY.dtype, "dY")
+    R, T = dY.shape
+    device = dY.device
+    if rows is not None and rows != R:
+        raise ValueError(f"rows={rows} does not match dY ({R} rows)")
+    if code:
+        if Z is None:
+            raise ValueError("an activation's gradient needs Z (spmm_act with keep=True)")
+        _expect(Z, "Z", (R, T), dY.dtype, device)
+    K = m  # of a call without products, where it does not count
+    lay = _layout("rows")
+    if "dW" in want or "dX" in want:
+        if X is None:
+            raise ValueError("dW and dX need X")
+        K = X.shape[0] if X.dim() == 2 else -1
+        _expect(X, "X", (K, T), dY.dtype, device)
+    if "dX" in want:
+        if values is None or meta is None:
+            raise ValueError("dX needs values and meta")
+        lay = _layout(layout)
+        vdt, vrows = _check_compressed(values, meta, n, m, K, layout, R)
+        if vdt != dt or vrows != R or values.device != device:
+            raise ValueError("values must have dY's rows, dtype and device")
+    shapes = dict(dW=((R, K), dY.dtype), dX=((K, T), dY.dtype), dbias=((R,), torch.float32),
+                  dZ=((R, T), dY.dtype))
+    res = {w: dY.new_empty(shapes[w][0], dtype=shapes[w][1]) for w in want}
+    L = lib()
+    dx = "dX" in want
+    with _device_of(dY):
+        ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_workspace_bytes(
+            R, K, T, code, "dW" in want, dx, "dZ" in want))
+        _check("nm_spmm_act_grad", L.nm_spmm_act_grad(
+            _addr(values) if dx else None, _addr(meta) if dx else None, R, K, n, m, lay,
+            _addr(X) if "dW" in want else None, T, dt, code, _addr(Z) if code else None,
+            dY.data_ptr(), _addr(res.get("dW")), _addr(res.get("dX")), _addr(res.get("dbias")),
+            _addr(res.get("dZ")), ws_ptr, 0 if ws is None else ws.numel(), _current_stream(dY)))
+    return tuple(res[w] for w in want)
+
+
+def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group: int = 64,
+               rows: int | None = None, meta: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, act: str = "none",
+               residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """matvec with spmm_act's epilogue: Y (rows, T) = act(Wq @ X + bias) + residual for one token or
+    a few; bias is float32 (rows,), residual (rows, T) in Y's type may be out itself."""
+    if rows is None:
+        raise ValueError("matvec_act needs rows= (the matrix's row count)")
+    _dense_input(X, "X", int8=False)
+    dt = _half(X.dtype, "X")
+    code = _act(act)
+    K, T = X.shape
+    device = X.device
+    if meta is not None and K % 64:
+        _check("nm_matvec_act", 8)
+    if _check_codes(codes, scales, rows, K // 2 if meta is not None else K, group) != dt:
+        raise ValueError("scales and X must have the same dtype")
+    if codes.device != device:
+        raise ValueError("codes and X must be on the same device")
+    if meta is not None:
+        _expect(meta, "meta", (-(-rows // 16), K // 64, 32), torch.int32, device)
+    y_dtype = out_dtype or X.dtype
+    if y_dtype != X.dtype and y_dtype != torch.float32:
+        raise ValueError("out_dtype must be X's dtype or float32")
+    bias = _row_numbers(bias, "bias", rows, device)
+    _expect(residual, "residual", (rows, T), y_dtype, device)
+    _expect(out, "out", (rows, T), y_dtype, device)
+    if out is None:
+        out = X.new_empty((rows, T), dtype=y_dtype)
+    L = lib()
+    with _device_of(X):
+        ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
+        _check("nm_matvec_act", L.nm_matvec_act(
+            codes.data_ptr(), scales.data_ptr(), _addr(meta), rows, K, group, X.data_ptr(), T, dt,
+            _addr(bias), code, _addr(residual), out.data_ptr(), _DT[y_dtype], ws_ptr,
+            0 if ws is None else ws.numel(), _current_stream(X)))
+    return out
+
+
+# ---- gradients' norm and clipping ------------------------------------------------------------
+
+
+_FLOAT_DT = {torch.float32: NM_F32, torch.float16: NM_F16, torch.bfloat16: NM_BF16}
+
+
+class _Tensors:
+    """The host arrays that nm_grad_norm and nm_clip_grads take, of dense float tensors on one GPU."""
+
+    def __init__(self, grads):
+        self.grads = grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
+        if not grads:
+            raise ValueError("no tensors")
+        device = grads[0].device
+        if device.type != "cuda":
+            raise ValueError("gradients must be on a GPU")
+        for g in grads:
+            if g.dtype not in _FLOAT_DT or g.device != device or not (
+                    g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous())):
+                raise ValueError("gradients must be float32, float16 or bfloat16 tensors without gaps "
+                                 "on one GPU")
+        self.pointers = array.array("q", [g.data_ptr() for g in grads])
+        self.counts = array.array("q", [g.numel() for g in grads])
+        self.dts = array.array("i", [_FLOAT_DT[g.dtype] for g in grads])
+
+    def addresses(self):
+        return (self.pointers.buffer_info()[0], self.counts.buffer_info()[0],
+                self.dts.buffer_info()[0], len(self.counts))
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm (float32, no dimensions) of all entries of a tensor or a list of them, of float32,
+    float16 and bfloat16 as they come; squares are summed in fp64."""
+    t = _Tensors(grads)
+    like = t.grads[0]
+    norm = like.new_empty((), dtype=torch.float32)
+    ptrs, counts, dts, n = t.addresses()
+    L = lib()
+    with _device_of(like):
+        ws, ws_ptr = _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
+        _check("nm_grad_norm", L.nm_grad_norm(ptrs, counts, dts, n, norm.data_ptr(), ws_ptr,
+                                              0 if ws is None else ws.numel(), _current_stream(like)))
+    return norm
+
+
+def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=None) -> torch.Tensor:
+    """Every gradient times max_norm / norm where the norm of all of them is finite and above
+    max_norm, in place or into `out` (tensors of the same shapes, strides and types); returns the norm
+    before clipping.  `norm` (float32, one number on the GPU) takes the place of the gradients' own, as
+    where each rank holds a part of them: join grad_norm's squares over the ranks first."""
+    t = _Tensors(grads)
+    o = t if out is None else _Tensors(out)
+    if o is not t and (len(o.grads) != len(t.grads) or any(
+            a.shape != b.shape or a.dtype != b.dtype or a.device != b.device or
+            (a.stride() != b.stride() and a.numel() > 0) for a, b in zip(t.grads, o.grads))):
+        raise ValueError("out must match the gradients' shapes, strides, dtypes and device")
+    like = t.grads[0]
+    given = norm
+    if norm is None:
+        norm = like.new_empty((), dtype=torch.float32)
+    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != like.device:
+        raise ValueError("norm must be one float32 number on the gradients' device")
+    ptrs, counts, dts, n = t.addresses()
+    L = lib()
+    with _device_of(like):
+        ws, ws_ptr = (None, None) if given is not None else \
+            _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
+        _check("nm_clip_grads", L.nm_clip_grads(
+            ptrs, o.pointers.buffer_info()[0], counts, dts, n, float(max_norm), _addr(given),
+            norm.data_ptr(), ws_ptr, 0 if ws is None else ws.numel(), _current_stream(like)))
+    return norm
+
+
+# ---- penalties, biases and masks on logits -----------------------------------------------------
+
+
+def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
+                  starts: torch.Tensor | None = None, prompts: torch.Tensor | None = None,
+                  repetition: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                  frequency: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                  allowed: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Logits (V, T), a column a sequence, after penalties for the sequences' own words, a bias and
+    a mask (out may be logits).  tokens: int64, column t's at starts[t] .. starts[t + 1] - 1 (starts:
+    int64 (T + 1,)), of which the first prompts[t] (int64 (T,)) are its prompt.  Of a word that
+    stands in them, a times after the prompt: x / repetition[t] where x > 0, else x * repetition[t];
+    then - presence[t] if a > 0 and - frequency[t] * a (each float32 (T,)).  Then + bias (float32
+    (V,) or (V, T)), and -infinity where bit v % 32 of allowed[t, v // 32] (int32 (T, ceil(V / 32)))
+    is 0.  What is None is left out; tokens outside the vocabulary are passed over."""
+    dt = _dense_input(logits, "logits", int8=False)
+    V, T = logits.shape
+    device = logits.device
+    count = 0
+    if tokens is not None:
+        if starts is None:
+            raise ValueError("tokens need starts")
+        count = tokens.numel()
+        _expect(tokens, "tokens", (count,), torch.int64, device)
+        _expect(starts, "starts", (T + 1,), torch.int64, device)
+        _expect(prompts, "prompts", (T,), torch.int64, device)
+        tokens, starts = _token_numbers(tokens), _token_numbers(starts)
+        prompts = None if prompts is None else _token_numbers(prompts)
+    elif starts is not None or prompts is not None:
+        raise ValueError("starts and prompts go with tokens")
+    penalties = [_row_numbers(t, name, T, device) for t, name in (
+        (repetition, "repetition"), (presence, "presence"), (frequency, "frequency"))]
+    each = bias is not None and bias.dim() == 2
+    _expect(bias, "bias", (V, T) if each else (V,), torch.float32, device)
+    _expect(allowed, "allowed", (T, -(-V // 32)), torch.int32, device)
+    _expect(out, "out", (V, T), logits.dtype, device)
+    bias = None if bias is None else _token_numbers(bias)
+    allowed = None if allowed is None else _token_numbers(allowed)
+    if out is None:
+        out = torch.empty_like(logits)
+    L = lib()
+    with _device_of(logits):
+        ws, ws_ptr = _workspace(logits, L.nm_adjust_logits_workspace_bytes(V, T, count))
+        _check("nm_adjust_logits", L.nm_adjust_logits(
+            logits.data_ptr(), dt, V, T, _addr(tokens), count, _addr(starts), _addr(prompts),
+            *map(_addr, penalties), _addr(bias), each, _addr(allowed), out.data_ptr(), ws_ptr,
+            0 if ws is None else ws.numel(), _current_stream(logits)))
     return out

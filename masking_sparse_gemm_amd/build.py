@@ -18,8 +18,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnm.so")
-SOURCES = ["nm_api.hip", "nm_compress.hip", "nm_spmm.hip", "nm_spmm_sk.hip", "nm_srste.hip",
-           "nm_tmask.hip", "nm_perm.hip", "nm_quant.hip", "nm_xent.hip", "nm_orth.hip"]
+SOURCES = ["nm_api.hip", "nm_compress.hip", "nm_spmm.hip", "nm_spmm_act.hip",
+           "nm_spmm_act_any.hip", "nm_spmm_sk.hip", "nm_srste.hip",
+           "nm_tmask.hip", "nm_perm.hip", "nm_quant.hip", "nm_xent.hip", "nm_orth.hip",
+           "nm_spmm_grad.hip", "nm_clip.hip", "nm_logits.hip"]
 # the measurement probes (include/nm_probe.h) link into a library of their own
 PROBE_SOURCES = ["nm_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libnm_probe.so")
@@ -47,10 +49,10 @@ def flags() -> list[str]:
 
 
 def _stale(src: str, obj: str) -> bool:
-    """The object is older than its source or any header of the package."""
+    """The object is older than its source, a source that it includes or any header of the package."""
     if not os.path.exists(obj):
         return True
-    deps = [os.path.join(CSRC, src)] + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
+    deps = [os.path.join(CSRC, s) for s in (src, "nm_spmm.hip") if s == src or "spmm_act" in src] + [os.path.join(CSRC, h) for h in os.listdir(CSRC)
                                         if h.endswith(".h")] + [os.path.join(ROOT, "include", "nm.h")]
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 

@@ -4,9 +4,11 @@
 // neither the device nor the outputs.  The global state is a per-device record of
 // whether the device is a gfx950, filled on first use, and the per-device address of
 // the static scratch buffer behind nm_perm_gains_static, looked up on first use.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "../../include/nm.h"
@@ -720,6 +722,318 @@ nm_status nm_orthogonalize(const void* G, nm_dtype dt, int64_t R, int64_t K, int
   if ((st = check_device()) != NM_OK) return st;
   return from_hip(nm::launch_orthogonalize(G, (int)dt, R, K, steps, eps, out, workspace,
                                            static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool act_ok(int act) { return act >= NM_ACT_NONE && act <= NM_ACT_GELU_TANH; }
+
+// What a result of a product with an epilogue may be rounded to.
+bool act_types_ok(int dt, int y_dt) {
+  if (!valid_dtype(dt) || !float_dtype(y_dt)) return false;
+  return elem_bytes((nm_dtype)dt) == 1 || y_dt == dt || y_dt == NM_F32;
+}
+
+bool below(int64_t a, int64_t b, int64_t most) { return a == 0 || b <= most / a; }
+
+}  // namespace
+
+extern "C" {
+
+size_t nm_spmm_act_workspace_bytes(int64_t K, int64_t T, nm_dtype dt) {
+  if (!valid_dtype(dt) || K < 0 || T < 0 || !below(K, T, (int64_t)1 << 40)) return 0;
+  return nm::spmm_act_workspace_bytes(K, T, (int)dt);
+}
+
+nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
+                      nm_layout layout, const void* X, int64_t T, nm_dtype dt, const float* scale,
+                      const float* bias, nm_act act, const void* residual, void* Z, void* Y,
+                      nm_dtype y_dt, void* workspace, size_t workspace_bytes, nm_stream_t stream) {
+  if (!act_types_ok(dt, y_dt)) return NM_ERR_DTYPE;
+  const bool eight = elem_bytes(dt) == 1;
+  if (eight ? Z != nullptr : scale != nullptr) return NM_ERR_DTYPE;
+  nm_status st = check_pattern(n, m);
+  if (st != NM_OK) return st;
+  if ((st = check_shape(R, K, m)) != NM_OK) return st;
+  if (dt == NM_I8 && K >= (int64_t)1 << 17) return NM_ERR_SHAPE;  // int32 sums stay exact
+  if ((st = check_layout(layout, K)) != NM_OK) return st;
+  if (layout == NM_LAYOUT_BLOCKED && !blocked_pattern_ok(dt, n, m)) return NM_ERR_UNSUPPORTED;
+  if (!act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (T < 0 || !below(K, T, (int64_t)1 << 40) || !below(R, T, (int64_t)1 << 40)) return NM_ERR_SHAPE;
+  if (missing(values, R * K) || missing(meta, R * K) || missing(X, K * T) || missing(Y, R * T))
+    return NM_ERR_NULL;
+  if (R * T == 0) return NM_OK;
+  if (!aligned16(values) || !aligned16(meta) || !aligned16(X) || !aligned16(Y) || !aligned16(scale) ||
+      !aligned16(bias) || !aligned16(residual) || !aligned16(Z))
+    return NM_ERR_ALIGN;
+  const size_t need = nm::spmm_act_workspace_bytes(K, T, (int)dt);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const int64_t y_bytes = R * T * elem_bytes(y_dt);
+  const Range r[] = {{Y, y_bytes},
+                     {Z, Z ? R * T * elem_bytes(dt) : 0},
+                     {workspace, (int64_t)need},
+                     {values, (int64_t)nm_values_bytes(R, K, n, m, dt, layout)},
+                     {meta, (int64_t)nm_meta_bytes(R, K, n, m, layout)},
+                     {X, K * T * elem_bytes(dt)},
+                     {scale, scale ? R * 4 : 0},
+                     {bias, bias ? R * 4 : 0},
+                     {residual, residual && residual != Y ? y_bytes : 0}};
+  if (any_alias(r, 3, 9)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  nm::Product p{};
+  p.scale = scale;
+  p.bias = bias;
+  p.residual = residual;
+  p.y = Y;
+  p.z = Z;
+  p.act = (int)act;
+  p.y_dt = (int)y_dt;
+  p.z_dt = (int)dt;
+  return from_hip(nm::run_spmm_act(values, meta, R, K, n, m, layout == NM_LAYOUT_BLOCKED, X, T, (int)dt,
+                                   p, workspace, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+nm_status check_spmm_grad(int64_t R, int64_t K, int64_t T) {
+  if (R < 0 || K < 0 || T < 0 || R >= kMaxSide || K >= kMaxSide || T >= kMaxSide) return NM_ERR_SHAPE;
+  nm_status st = check_shape(R, K, 1);
+  if (st == NM_OK) st = check_shape(R, T, 1);
+  return st == NM_OK ? check_shape(K, T, 1) : st;
+}
+}  // namespace
+
+size_t nm_spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_act act, int want_dW,
+                                        int want_dX, int want_dZ) {
+  if (check_spmm_grad(R, K, T) != NM_OK || !act_ok(act)) return 0;
+  return nm::spmm_act_grad_workspace_bytes(R, K, T, want_dW && R * K > 0, want_dX && K * T > 0,
+                                           want_dZ != 0, act != NM_ACT_NONE);
+}
+
+nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                           int m, nm_layout layout, const void* X, int64_t T, nm_dtype dt, nm_act act,
+                           const void* Z, const void* dY, void* dW, void* dX, float* dbias, void* dZ,
+                           void* workspace, size_t workspace_bytes, nm_stream_t stream) {
+  if (!half_dtype(dt)) return NM_ERR_DTYPE;
+  nm_status st = check_pattern(n, m);
+  if (st != NM_OK) return st;
+  if ((st = check_shape(R, K, m)) != NM_OK) return st;
+  if ((st = check_spmm_grad(R, K, T)) != NM_OK) return st;
+  if ((st = check_layout(layout, K)) != NM_OK) return st;
+  if (!act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (missing(dY, R * T) || (act != NM_ACT_NONE && missing(Z, R * T)) || (dW && missing(X, K * T)) ||
+      (dX && (missing(values, R * K) || missing(meta, R * K))))
+    return NM_ERR_NULL;
+  if (!aligned16(values) || !aligned16(meta) || !aligned16(X) || !aligned16(Z) || !aligned16(dY) ||
+      !aligned16(dW) || !aligned16(dX) || !aligned16(dbias) || !aligned16(dZ))
+    return NM_ERR_ALIGN;
+  const size_t need =
+      nm_spmm_act_grad_workspace_bytes(R, K, T, act, dW != nullptr, dX != nullptr, dZ != nullptr);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Range r[] = {{dW, dW ? R * K * 2 : 0},
+                     {dX, dX ? K * T * 2 : 0},
+                     {dbias, dbias ? R * 4 : 0},
+                     {dZ, dZ ? R * T * 2 : 0},
+                     {workspace, (int64_t)need},
+                     {values, dX ? (int64_t)nm_values_bytes(R, K, n, m, dt, layout) : 0},
+                     {meta, dX ? (int64_t)nm_meta_bytes(R, K, n, m, layout) : 0},
+                     {X, dW ? K * T * 2 : 0},
+                     {Z, act != NM_ACT_NONE ? R * T * 2 : 0},
+                     {dY, R * T * 2}};
+  if (any_alias(r, 5, 10)) return NM_ERR_ALIAS;
+  if (R * K + R * T + K * T == 0) return NM_OK;
+  if ((st = check_device()) != NM_OK) return st;
+  const nm::SpmmGradCall c{values, meta, R, K, n, m, layout == NM_LAYOUT_BLOCKED, X, T, dt == NM_BF16,
+                           (int)act, Z, dY, dW, dX, dbias, dZ};
+  return from_hip(nm::launch_spmm_act_grad(c, workspace, static_cast<hipStream_t>(stream)));
+}
+
+nm_status nm_matvec_act(const void* codes, const void* scales, const uint32_t* meta, int64_t R,
+                        int64_t K, int group, const void* X, int64_t T, nm_dtype dt, const float* bias,
+                        nm_act act, const void* residual, void* Y, nm_dtype y_dt, void* workspace,
+                        size_t workspace_bytes, nm_stream_t stream) {
+  if (!half_dtype(dt) || (y_dt != dt && y_dt != NM_F32)) return NM_ERR_DTYPE;
+  nm_status st = check_matvec(R, K, T, meta != nullptr);
+  if (st != NM_OK) return st;
+  if (!group_ok(group) || !act_ok(act)) return NM_ERR_UNSUPPORTED;
+  if (meta != nullptr && K % 64 != 0) return NM_ERR_LAYOUT;
+  if (missing(codes, R * K) || missing(scales, R * K) || missing(X, K * T) || missing(Y, R * T))
+    return NM_ERR_NULL;
+  if (R * T == 0) return NM_OK;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(meta) || !aligned16(X) || !aligned16(Y) ||
+      !aligned16(bias) || !aligned16(residual))
+    return NM_ERR_ALIGN;
+  const size_t need = nm::matvec_workspace_bytes(R, K, T, meta != nullptr);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const int64_t C = meta != nullptr ? K / 2 : K, y_bytes = R * T * elem_bytes(y_dt);
+  const Range r[] = {{Y, y_bytes},
+                     {workspace, (int64_t)need},
+                     {codes, codes_bytes(R, C)},
+                     {scales, scales_bytes(R, C, group)},
+                     {meta, meta != nullptr ? (R + 15) / 16 * 16 * (K / 8) : 0},
+                     {X, K * T * 2},
+                     {bias, bias ? R * 4 : 0},
+                     {residual, residual && residual != Y ? y_bytes : 0}};
+  if (any_alias(r, 2, 8)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  nm::Product p{};
+  p.bias = bias;
+  p.residual = residual;
+  p.y = Y;
+  p.act = (int)act;
+  p.y_dt = (int)y_dt;
+  return from_hip(nm::launch_matvec_act(codes, scales, meta, R, K, group, X, T, (int)dt, p, workspace,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+constexpr int64_t kMostTensors = (int64_t)1 << 20, kMostEntries = (int64_t)1 << 40;
+
+nm_status check_tensors(const void* const* grads, void* const* outs, const int64_t* counts,
+                        const nm_dtype* dts, int64_t tensors, bool write) {
+  if (tensors < 0 || tensors > kMostTensors) return NM_ERR_SHAPE;
+  if (tensors == 0) return NM_OK;
+  if (counts == nullptr || dts == nullptr || grads == nullptr || (write && outs == nullptr))
+    return NM_ERR_NULL;
+  for (int64_t i = 0; i < tensors; ++i) {
+    if (!float_dtype(dts[i])) return NM_ERR_DTYPE;
+    if (counts[i] < 0 || counts[i] >= kMostEntries) return NM_ERR_SHAPE;
+    if (missing(grads[i], counts[i]) || (write && missing(outs[i], counts[i]))) return NM_ERR_NULL;
+    const uintptr_t mask = (uintptr_t)elem_bytes(dts[i]) - 1;
+    if (counts[i] > 0 && ((reinterpret_cast<uintptr_t>(grads[i]) & mask) ||
+                          (write && (reinterpret_cast<uintptr_t>(outs[i]) & mask))))
+      return NM_ERR_ALIGN;
+  }
+  return NM_OK;
+}
+
+// Does what is written overlap anything else?  All ranges in the order of their starts: a written
+// one may not begin before the end of any earlier one, a read one not before that of a written one.
+bool tensors_alias(const void* const* grads, void* const* outs, const int64_t* counts,
+                   const nm_dtype* dts, int64_t tensors, const Range* more, int n_more, int written) {
+  struct Span {
+    uintptr_t begin, end;
+    bool write;
+  };
+  std::vector<Span> all;
+  all.reserve((size_t)(2 * tensors) + (size_t)n_more);
+  const auto add = [&](const void* p, int64_t bytes, bool write) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    if (p != nullptr && bytes > 0) all.push_back(Span{b, b + (uintptr_t)bytes, write});
+  };
+  for (int64_t i = 0; i < tensors; ++i) {
+    const int64_t bytes = counts[i] * elem_bytes(dts[i]);
+    if (outs) add(outs[i], bytes, true);
+    if (!outs || outs[i] != grads[i]) add(grads[i], bytes, false);
+  }
+  for (int i = 0; i < n_more; ++i) add(more[i].p, more[i].bytes, i < written);
+  std::sort(all.begin(), all.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any_end = 0, write_end = 0;
+  for (const Span& s : all) {
+    if (s.begin < (s.write ? any_end : write_end)) return true;
+    any_end = std::max(any_end, s.end);
+    if (s.write) write_end = std::max(write_end, s.end);
+  }
+  return false;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+size_t nm_grad_norm_workspace_bytes(const int64_t* counts, int64_t tensors) {
+  if (tensors <= 0 || tensors > kMostTensors || counts == nullptr) return 0;
+  return nm::norm_workspace_bytes(counts, tensors);
+}
+
+nm_status nm_grad_norm(const void* const* grads, const int64_t* counts, const nm_dtype* dts,
+                       int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
+                       nm_stream_t stream) try {
+  nm_status st = check_tensors(grads, nullptr, counts, dts, tensors, false);
+  if (st != NM_OK) return st;
+  if (norm == nullptr) return NM_ERR_NULL;
+  if (!aligned4(norm)) return NM_ERR_ALIGN;
+  const size_t need = nm_grad_norm_workspace_bytes(counts, tensors);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Range more[] = {{norm, 4}, {workspace, (int64_t)need}};
+  if (tensors_alias(grads, nullptr, counts, dts, tensors, more, 2, 2)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_clip(grads, nullptr, counts, reinterpret_cast<const int*>(dts), tensors, 0.f,
+                                  nullptr, norm, workspace, static_cast<hipStream_t>(stream)));
+} catch (const std::bad_alloc&) {
+  return NM_ERR_SHAPE;  // no host memory to check that many tensors
+}
+
+nm_status nm_clip_grads(const void* const* grads, void* const* outs, const int64_t* counts,
+                        const nm_dtype* dts, int64_t tensors, float max_norm, const float* given,
+                        float* norm, void* workspace, size_t workspace_bytes, nm_stream_t stream) try {
+  nm_status st = check_tensors(grads, outs, counts, dts, tensors, true);
+  if (st != NM_OK) return st;
+  if (!(max_norm >= 0.f)) return NM_ERR_SHAPE;
+  if (given == nullptr && norm == nullptr) return NM_ERR_NULL;
+  if (!aligned4(norm) || !aligned4(given)) return NM_ERR_ALIGN;
+  const size_t need = given ? 0 : nm_grad_norm_workspace_bytes(counts, tensors);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const Range more[] = {{given ? nullptr : norm, 4}, {workspace, (int64_t)need}, {given, 4}};
+  if (tensors_alias(grads, outs, counts, dts, tensors, more, 3, 2)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  return from_hip(nm::launch_clip(grads, outs, counts, reinterpret_cast<const int*>(dts), tensors,
+                                  max_norm, given, norm, workspace, static_cast<hipStream_t>(stream)));
+} catch (const std::bad_alloc&) {
+  return NM_ERR_SHAPE;
+}
+
+namespace {
+nm_status check_logits(int64_t V, int64_t T, int64_t count) {
+  const int64_t most = (int64_t)1 << 31;
+  if (V < 0 || T < 0 || V >= most || T >= (int64_t)1 << 20 || count < 0 || count >= most)
+    return NM_ERR_SHAPE;
+  return check_shape(V, T, 1);
+}
+}  // namespace
+
+size_t nm_adjust_logits_workspace_bytes(int64_t V, int64_t T, int64_t count) {
+  return check_logits(V, T, count) == NM_OK && V * T > 0 ? nm::logits_workspace_bytes(V, T, count) : 0;
+}
+
+nm_status nm_adjust_logits(const void* logits, nm_dtype dt, int64_t V, int64_t T,
+                           const int64_t* tokens, int64_t count, const int64_t* starts,
+                           const int64_t* prompts, const float* repetition, const float* presence,
+                           const float* frequency, const float* bias, int bias_each,
+                           const uint32_t* allowed, void* out, void* workspace,
+                           size_t workspace_bytes, nm_stream_t stream) {
+  if (!float_dtype(dt)) return NM_ERR_DTYPE;
+  nm_status st = check_logits(V, T, tokens ? count : 0);
+  if (st != NM_OK) return st;
+  if (missing(logits, V * T) || missing(out, V * T) || (tokens && missing(starts, T))) return NM_ERR_NULL;
+  if (V * T == 0) return NM_OK;
+  for (const void* p : {logits, (const void*)out, (const void*)tokens, (const void*)starts,
+                        (const void*)prompts, (const void*)repetition, (const void*)presence,
+                        (const void*)frequency, (const void*)bias, (const void*)allowed})
+    if (!aligned16(p)) return NM_ERR_ALIGN;
+  if (tokens == nullptr) count = 0;
+  const size_t need = nm_adjust_logits_workspace_bytes(V, T, count);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
+  const auto floats = [&](const float* p, int64_t n) { return Range{p, p ? n * 4 : 0}; };
+  const int64_t bytes = V * T * elem_bytes(dt);
+  const Range r[] = {{out, bytes},
+                     {workspace, (int64_t)need},
+                     {logits, logits != out ? bytes : 0},
+                     {tokens, tokens ? count * 8 : 0},
+                     {starts, tokens ? (T + 1) * 8 : 0},
+                     {prompts, prompts ? T * 8 : 0},
+                     floats(repetition, T),
+                     floats(presence, T),
+                     floats(frequency, T),
+                     floats(bias, bias_each ? V * T : V),
+                     {allowed, allowed ? T * ((V + 31) / 32) * 4 : 0}};
+  if (any_alias(r, 2, 11)) return NM_ERR_ALIAS;
+  if ((st = check_device()) != NM_OK) return st;
+  const nm::LogitsCall c{logits, (int)dt, V, T, tokens, count, starts, prompts, repetition, presence,
+                         frequency, bias, bias_each != 0, allowed, out};
+  return from_hip(nm::launch_adjust_logits(c, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -110,6 +110,7 @@ template <int WM, int WN, int FM, int FN, bool AS, bool BS, bool BF16, bool SWAP
           int PARTS = 1>
 struct Gemm {
   static constexpr int kFM = FM, kFN = FN, kWM = WM, kWN = WN;
+  static constexpr bool kAS = AS, kBS = BS;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kBM = 32 * FM * WM, kBN = 32 * FN * WN;
   static constexpr int kABytes = kBM * 2 * kGemmStep, kBBytes = kBN * 2 * kGemmStep;

@@ -44,6 +44,50 @@ hipError_t launch_spmm_sk(const void* values, const uint32_t* meta, int64_t R, i
                           const void* X, int64_t T, int dt, void* Y, int y_dt, void* workspace,
                           int groups, hipStream_t s);
 
+// What becomes of a product's sums: y = act(scale sum + bias) + residual, z the activation's argument
+// (types in nm_dtype codes, act in nm_act's; what is null is left out).  ldx: numbers in a row of X.
+struct Product {
+  const float *scale, *bias;
+  const void* residual;
+  void *y, *z;
+  int64_t ldx;
+  int act, y_dt, z_dt;
+};
+// Any pattern and type; rows of X are whole 16-byte pieces (nm_spmm.hip as nm_spmm_act.hip and
+// nm_spmm_act_any.hip).
+hipError_t launch_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                           int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
+                           hipStream_t s);
+hipError_t launch_expand_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                             int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
+                             hipStream_t s);
+
+// The same for any T (nm_spmm_grad.hip): rows of X that are not whole pieces are copied to the workspace.
+size_t spmm_act_workspace_bytes(int64_t K, int64_t T, int dt);
+hipError_t run_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
+                        bool blocked, const void* X, int64_t T, int dt, Product p, void* workspace,
+                        hipStream_t s);
+
+// The gradient of that (nm_spmm_grad.hip); what is null is not computed.
+struct SpmmGradCall {
+  const void* values;
+  const uint32_t* meta;
+  int64_t R, K;
+  int n, m;
+  bool blocked;
+  const void* X;
+  int64_t T;
+  bool bf16;
+  int act;
+  const void *Z, *dY;
+  void *dW, *dX;
+  float* dbias;
+  void* dZ;
+};
+size_t spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, bool want_w, bool want_x,
+                                     bool want_z, bool act);
+hipError_t launch_spmm_act_grad(const SpmmGradCall& c, void* workspace, hipStream_t s);
+
 // Compress of W's transpose (the K x R matrix, groups of m along R; R % m == 0, and
 // R % 64 == 0 for the blocked layout).
 hipError_t launch_select_t(const void* W, int elem_bytes, int64_t R, int64_t K, int n, int m,
@@ -82,6 +126,34 @@ size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse);
 hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
                          int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
                          void* workspace, hipStream_t s);
+
+hipError_t launch_matvec_act(const void* codes, const void* scales, const void* meta, int64_t R,
+                             int64_t K, int group, const void* X, int64_t T, int dt, const Product& p,
+                             void* workspace, hipStream_t s);
+
+// Norm of many tensors and clipping by it (nm_clip.hip): host arrays of `tensors` device pointers,
+// counts and nm_dtype codes.  outs null: the norm alone.  given null: the tensors' own norm.
+size_t norm_workspace_bytes(const int64_t* counts, int64_t tensors);
+hipError_t launch_clip(const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int* dts, int64_t tensors, float max_norm, const float* given,
+                       float* norm, void* workspace, hipStream_t s);
+
+// Penalties, biases and masks on logits (nm_logits.hip); null parts are left out.
+struct LogitsCall {
+  const void* logits;
+  int dt;
+  int64_t V, T;
+  const int64_t* tokens;
+  int64_t count;  // of tokens
+  const int64_t *starts, *prompts;
+  const float *repetition, *presence, *frequency;
+  const float* bias;
+  bool bias_each;
+  const uint32_t* allowed;
+  void* out;
+};
+size_t logits_workspace_bytes(int64_t V, int64_t T, int64_t count);
+hipError_t launch_adjust_logits(const LogitsCall& c, void* workspace, hipStream_t s);
 
 // Cross entropy of W X and its gradient (nm_xent.hip); the workspaces are 256-byte aligned parts.
 size_t xent_workspace_bytes(int64_t V, int64_t K, int64_t T);

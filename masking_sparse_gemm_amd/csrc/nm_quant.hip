@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "nm_act.h"
 #include "nm_grid.h"
 #include "nm_launch.h"
 #include "nm_mfma.h"
@@ -343,7 +344,16 @@ struct MatvecArgs {
   int slice;       // blocks of a slice of the stored columns
   int log_along;   // log2 of the waves that share 16 rows
   float4_t* part;  // slices x blocks of 16 rows x tiles of 16 columns x 64 lanes
+  Epilogue ep;     // of output type kAct
 };
+
+// One result of the product, of any output type.
+template <int YT>
+__device__ __forceinline__ void matvec_out(void* y, const Epilogue& ep, int64_t row, int64_t col,
+                                           int64_t T, float v) {
+  if constexpr (YT == kAct) finish_one(ep, row, col, T, v);
+  else store_from_f32<YT>(y, row * T + col, v);
+}
 
 // One block of 128 stored columns of 16 rows, as one lane holds it, and where the lane finds it:
 // with the wave's own scalar bases the loads need no vector address arithmetic.
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(64 * WAVES) matvec_kernel(MatvecArgs a) {
     float y = 0.f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) y += part[w * 64 + 16 * (row / 4) + t][row % 4];
-    if (16 * g + row < a.R) store_from_f32<YT>(a.y, (16 * g + row) * T + t, y);
+    if (16 * g + row < a.R) matvec_out<YT>(a.y, a.ep, 16 * g + row, t, T, y);
   }
 }
 
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(64 * kSliceWaves) matvec_slice_kernel(MatvecAr
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t row = 16 * mine + 4 * j + i;
-      if (row < a.R && col < a.T) store_from_f32<YT>(a.y, row * a.T + col, total[t][i]);
+      if (row < a.R && col < a.T) matvec_out<YT>(a.y, a.ep, row, col, a.T, total[t][i]);
     }
   }
 }
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(64 * kSliceWaves) matvec_slice_kernel(MatvecAr
 template <int YT>
 __global__ void __launch_bounds__(256)
     join_slices_kernel(const float4_t* __restrict__ part, int slices, int64_t pieces, int64_t tiles,
-                       int64_t R, int64_t T, void* __restrict__ y) {
+                       int64_t R, int64_t T, void* __restrict__ y, Epilogue ep) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= pieces) return;
   const int lane = e & 63;
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (row + i < R) store_from_f32<YT>(y, (row + i) * T + col, total[i]);
+    if (row + i < R) matvec_out<YT>(y, ep, row + i, col, T, total[i]);
 }
 
 // How several columns are cut.  Each workgroup reads X's rows of its slice, so rows are shared by
@@ -702,7 +712,7 @@ hipError_t launch_matvec_slices(const MatvecArgs& a, const MatvecPlan& p, hipStr
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.slices == 1) return e;
   join_slices_kernel<YT><<<(unsigned)((p.pieces + 255) / 256), 256, 0, s>>>(
-      a.part, p.slices, p.pieces, p.tiles * NT, a.R, a.T, a.y);
+      a.part, p.slices, p.pieces, p.tiles * NT, a.R, a.T, a.y, a.ep);
   return hipGetLastError();
 }
 
@@ -742,6 +752,7 @@ hipError_t launch_matvec_cols(const MatvecArgs& a, const MatvecPlan& p, hipStrea
 template <bool BF16, bool SPARSE, int LOG_GROUP>
 hipError_t launch_matvec_y(const MatvecArgs& a, const MatvecPlan& p, int y_dt, hipStream_t s) {
   constexpr int kSame = BF16 ? kBF16 : kF16;
+  if (y_dt == kAct) return launch_matvec_cols<BF16, SPARSE, LOG_GROUP, kAct>(a, p, s);
   return y_dt == kF32 ? launch_matvec_cols<BF16, SPARSE, LOG_GROUP, kF32>(a, p, s)
                       : launch_matvec_cols<BF16, SPARSE, LOG_GROUP, kSame>(a, p, s);
 }
@@ -822,9 +833,10 @@ size_t matvec_workspace_bytes(int64_t R, int64_t K, int64_t T, bool sparse) {
   return column_lds(R, K, T) ? 0 : (size_t)MatvecPlan(R, K, T, sparse).bytes;
 }
 
-hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
-                         int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
-                         void* workspace, hipStream_t s) {
+namespace {
+hipError_t launch_matvec_to(const void* codes, const void* scales, const void* meta, int64_t R,
+                            int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
+                            const Epilogue& ep, void* workspace, hipStream_t s) {
   const int64_t C = meta ? K / 2 : K;
   const MatvecPlan p(R, K, T, meta != nullptr);
   MatvecArgs a;
@@ -842,12 +854,27 @@ hipError_t launch_matvec(const void* codes, const void* scales, const void* meta
   a.slice = p.slice;
   a.log_along = p.log_along;
   a.part = static_cast<float4_t*>(workspace);
+  a.ep = ep;
   const int lg = log2_of(group);
   if (dt == kBF16)
     return meta ? launch_matvec_group<true, true>(a, p, lg, y_dt, s)
                 : launch_matvec_group<true, false>(a, p, lg, y_dt, s);
   return meta ? launch_matvec_group<false, true>(a, p, lg, y_dt, s)
               : launch_matvec_group<false, false>(a, p, lg, y_dt, s);
+}
+}  // namespace
+
+hipError_t launch_matvec(const void* codes, const void* scales, const void* meta, int64_t R,
+                         int64_t K, int group, const void* X, int64_t T, int dt, void* Y, int y_dt,
+                         void* workspace, hipStream_t s) {
+  return launch_matvec_to(codes, scales, meta, R, K, group, X, T, dt, Y, y_dt, Epilogue{}, workspace, s);
+}
+
+hipError_t launch_matvec_act(const void* codes, const void* scales, const void* meta, int64_t R,
+                             int64_t K, int group, const void* X, int64_t T, int dt, const Product& p,
+                             void* workspace, hipStream_t s) {
+  return launch_matvec_to(codes, scales, meta, R, K, group, X, T, dt, p.y, kAct, epilogue_of(p),
+                          workspace, s);
 }
 
 }  // namespace nm

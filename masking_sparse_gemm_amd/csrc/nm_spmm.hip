@@ -36,10 +36,15 @@
 // The blocked layout (include/nm.h) makes every direct load of compressed values or
 // metadata one contiguous run; the row layout is accepted by the same kernels at a lower
 // rate.  Accumulators are fp32 (int32 for int8) and rounded once to the output type.
+//
+// This file is compiled three times, in parallel: as it is for nm_spmm, and through nm_spmm_act.hip
+// and nm_spmm_act_any.hip (NM_SPMM_PART 1 and 2) for the same kernels with the output type kAct, whose
+// epilogue is nm_act.h's.
 #include <atomic>
 #include <cstdlib>
 #include <type_traits>
 
+#include "nm_act.h"
 #include "nm_launch.h"
 #include "nm_mfma.h"
 
@@ -251,7 +256,7 @@ struct TileMap {
 // walked in groups of gm row tiles x gn column tiles so that the 32 workgroups an XCD runs
 // at once share A stripes and X panels in its L2.  (8 x 4 and 4 x 8 groups time the same
 // within noise on the LLaMA, BERT and sweep shapes, for every element type.)
-TileMap make_tile_map(int tiles_m, int tiles_n, int xcds) {
+[[maybe_unused]] TileMap make_tile_map(int tiles_m, int tiles_n, int xcds) {
   TileMap map;
   map.tiles_m = tiles_m;
   map.tiles_n = tiles_n;
@@ -279,12 +284,13 @@ template <bool BF16, bool kPat12, bool kBlocked, int YT, int BM, int BN, int WAV
           int STAGES>
 __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
     smfmac_spmm_kernel(const uint16_t* __restrict__ values, const uint32_t* __restrict__ meta,
-                       const uint16_t* __restrict__ X, void* __restrict__ Y, int R, int K, int T,
+                       const uint16_t* __restrict__ X, typename OutOf<YT>::type Y, int R, int K, int T,
                        TileMap map) {
   using TL = SmfmacTile<BM, BN, WAVES_M, WAVES_N, STAGES>;
   constexpr int FM = TL::kFM, FN = TL::kFN, kStages = STAGES;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  const int ldx = x_stride(Y, T);  // row length of X
   int tile_m, tile_n;
   if (!map.tile_of(blockIdx.x, tile_m, tile_n)) return;  // whole workgroup, before any load
   const int tid = threadIdx.x;
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
     const int lc = pc ^ (r & 15);
     int col = t0 + 8 * lc;
     col = col < T ? col : 0;  // columns past T: any valid address (outputs past T only)
-    x_src[j] = ((int64_t)r * T + col) * 2;
+    x_src[j] = ((int64_t)r * ldx + col) * 2;
     x_dst[j] = (uint32_t)(w1k * 1024);
   }
   int64_t a_src[TL::kALoads];
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
   auto issue_step = [&](int step) {
     step = step < last_step ? step : last_step;
     uint8_t* st = smem + (step % kStages) * TL::kStageBytes;
-    const int64_t kx = (int64_t)step * kKStep * T * 2;                      // X rows
+    const int64_t kx = (int64_t)step * kKStep * ldx * 2;                      // X rows
     const int64_t ka = (int64_t)step * values_step_bytes<kBlocked>();       // values
     const int64_t km = (int64_t)step * meta_step_bytes<kBlocked, kPat12>();  // metadata
 #pragma unroll
@@ -407,6 +413,34 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
   wait_loads_and_barrier<0>();
 
   // ---- epilogue: lane holds rows 4q..4q+3, column l16 of each 16x16 fragment ----
+  if constexpr (YT == kAct) {
+    static_assert(FM % 2 == 0 && FN == 4, "slabs of 32 rows x 64 columns");
+    static_assert(TL::kWaves * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    float* slab = reinterpret_cast<float*>(smem + wave * kEpilogueBytes);
+    const int row0 = m0 + wm * TL::kWM, col0 = t0 + wn * TL::kWN;
+    SlabInputs in;
+    slab_load(in, Y, row0, col0, R, T, lane);
+#pragma unroll 1
+    for (int g = 0; g < FM / 2; ++g) {
+#pragma unroll
+      for (int fm = 0; fm < 2; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            slab[(16 * fm + 4 * q + i) * kSlabPitch + 16 * fn + l16] = acc[fm][fn][i];
+      const SlabInputs now = in;
+      if (g + 1 < FM / 2) slab_load(in, Y, row0 + 32 * (g + 1), col0, R, T, lane);
+      asm volatile("" ::: "memory");
+      slab_finish(now, slab, Y, row0 + 32 * g, col0, R, T, lane);
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int fm = 0; fm + 2 < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = acc[fm + 2][fn];
+    }
+    return;
+  }
 #pragma unroll
   for (int fm = 0; fm < FM; ++fm) {
 #pragma unroll
@@ -416,7 +450,8 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = m0 + wm * TL::kWM + fm * 16 + 4 * q + i;
-        if (row < R) store_from_f32<YT>(Y, (int64_t)row * T + col, acc[fm][fn][i]);
+        if constexpr (YT != kAct)
+          if (row < R) store_from_f32<YT>(Y, (int64_t)row * T + col, acc[fm][fn][i]);
       }
     }
   }
@@ -586,13 +621,14 @@ template <bool BF16, bool kPat12, bool kBlocked, int YT, int BM, int BN, int WAV
           int STAGES>
 __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
     smfmac32_spmm_kernel(const uint16_t* __restrict__ values, const uint32_t* __restrict__ meta,
-                         const uint16_t* __restrict__ X, void* __restrict__ Y, int R, int K,
+                         const uint16_t* __restrict__ X, typename OutOf<YT>::type Y, int R, int K,
                          int T, TileMap map) {
   using TL = Smfmac32Tile<BM, BN, WAVES_M, WAVES_N, STAGES>;
   constexpr int kStages = STAGES;
   constexpr int kRB = TL::kXRowBytes;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  const int ldx = x_stride(Y, T);  // row length of X
   int tile_m, tile_n;
   if (!map.tile_of(blockIdx.x, tile_m, tile_n)) return;  // whole workgroup, before any load
   const int tid = threadIdx.x;
@@ -620,7 +656,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
     const int lc = 2 * ((pc >> 1) ^ xpair_swizzle(r)) + (pc & 1);
     int col = t0 + 8 * lc;
     col = col < T ? col : 0;  // columns past T: any valid address (outputs past T only)
-    x_src[j] = ((int64_t)r * T + col) * 2;
+    x_src[j] = ((int64_t)r * ldx + col) * 2;
     x_dst[j] = (uint32_t)(w1k * 1024);
   }
   int64_t a_src[TL::kALoads];
@@ -649,7 +685,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
     constexpr int j0 = P * TL::kLoads / 4, j1 = (P + 1) * TL::kLoads / 4;
     step = step < last_step ? step : last_step;
     uint8_t* st = smem + (step % kStages) * TL::kStageBytes;
-    const int64_t kx = (int64_t)step * kKStep * T * 2;
+    const int64_t kx = (int64_t)step * kKStep * ldx * 2;
     const int64_t ka = (int64_t)step * values_step_bytes<kBlocked>();
     const int64_t km = (int64_t)step * meta_step_bytes<kBlocked, kPat12>();
 #pragma unroll
@@ -770,7 +806,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
   wait_loads_and_barrier<0>();
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   static_assert(TL::kWaves * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_block_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
                          t0 + wn * TL::kWN, R, T, lane);
 }
 
@@ -1132,13 +1168,14 @@ template <bool BF16, bool kPat12, bool kBlocked, int YT, int BM, int BN, int CWA
           int CWAVES_N, int PWAVES, int STAGES, int XB = 16>
 __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     smfmac_ws_spmm_kernel(const uint16_t* __restrict__ values, const uint32_t* __restrict__ meta,
-                          const uint16_t* __restrict__ X, void* __restrict__ Y, int R, int K,
+                          const uint16_t* __restrict__ X, typename OutOf<YT>::type Y, int R, int K,
                           int T, TileMap map) {
   using TL = WsTile<BM, BN, CWAVES_M, CWAVES_N, PWAVES, STAGES>;
   constexpr int kStages = STAGES;
   constexpr int kRB = TL::kXRowBytes;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  const int ldx = x_stride(Y, T);  // row length of X
   int tile_m, tile_n;
   if (!map.tile_of(blockIdx.x, tile_m, tile_n)) return;  // whole workgroup, before any load
   const int tid = threadIdx.x;
@@ -1174,11 +1211,11 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
       const int lc = 2 * ((pc >> 1) ^ xpair_swizzle(r)) + (pc & 1);
       int col = t0 + 8 * lc;
       col = col < T ? col : 0;  // columns past T: any valid address (outputs past T only)
-      x_off = (uint32_t)(((int64_t)r * T + col) * 2);
+      x_off = (uint32_t)(((int64_t)r * ldx + col) * 2);
 #pragma unroll
       for (int j = 0; j < kXLoads; ++j) {
         const int w1k = j * TL::kProducers + pw;
-        x_base[j] = xg + (int64_t)(4 * w1k) * T * 2;
+        x_base[j] = xg + (int64_t)(4 * w1k) * ldx * 2;
         x_dst[j] = (uint32_t)(w1k * 1024);
       }
     } else {
@@ -1192,7 +1229,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
 #pragma unroll
       for (int j = 0; j < kXLoads; ++j) {
         const int r = j * TL::kProducers + pw;
-        x_base[j] = xg + (int64_t)r * T * 2;
+        x_base[j] = xg + (int64_t)r * ldx * 2;
         x_dst[j] = (uint32_t)(r * BN * 2);
       }
     }
@@ -1262,7 +1299,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
       // it (a slot no wave reads any more), so every step issues the same loads
       const uint32_t sta = lds_addr(smem + (step % kStages) * TL::kStageBytes);
       step = step < last_step ? step : last_step;
-      const int64_t kx = (int64_t)step * kKStep * T * 2;
+      const int64_t kx = (int64_t)step * kKStep * ldx * 2;
       const int64_t ka = (int64_t)step * values_step_bytes<kBlocked>();
       const int64_t km = (int64_t)step * meta_step_bytes<kBlocked, kPat12>();
 #pragma unroll
@@ -1359,7 +1396,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
   // get time to land before plain instructions read the accumulators
   asm volatile("s_barrier\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_block_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
                          t0 + wn * TL::kWN, R, T, lane);
 }
 
@@ -1424,12 +1461,13 @@ template <bool kFp8, bool kBlocked, bool kPat12, int YT, int BM, int BN, int CWA
           int CWAVES_N, int PWAVES, int STAGES>
 __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     smfmac_i8_ws_spmm_kernel(const uint8_t* __restrict__ values, const uint32_t* __restrict__ meta,
-                             const uint8_t* __restrict__ X, void* __restrict__ Y, int R, int K,
+                             const uint8_t* __restrict__ X, typename OutOf<YT>::type Y, int R, int K,
                              int T, TileMap map) {
   using TL = WsI8Tile<BM, BN, CWAVES_M, CWAVES_N, PWAVES, STAGES>;
   constexpr int kStages = STAGES;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  const int ldx = x_stride(Y, T);  // row length of X
   int tile_m, tile_n;
   if (!map.tile_of(blockIdx.x, tile_m, tile_n)) return;  // whole workgroup, before any load
   const int tid = threadIdx.x;
@@ -1453,7 +1491,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
       const int r = slot >> 3, pc = slot & 7;
       int col = t0 + 16 * (pc ^ xsw_i8(r));
       col = col < T ? col : 0;  // columns past T: any valid address (outputs past T only)
-      x_src[j] = (int64_t)r * T + col;
+      x_src[j] = (int64_t)r * ldx + col;
       x_dst[j] = (uint32_t)(w1k * 1024);
     }
     // A stage holds, per 16-row group, the values as [64-wide half][row][32 bytes] (1 KB)
@@ -1502,7 +1540,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     auto issue_step = [&](int step) {
       step = step < last_step ? step : last_step;  // past the end: re-read the last step
       uint8_t* st = smem + (step % kStages) * TL::kStageBytes;
-      const int64_t kx = (int64_t)step * kI8KStep * T;
+      const int64_t kx = (int64_t)step * kI8KStep * ldx;
 #pragma unroll
       for (int j = 0; j < TL::kXLoads; ++j) global_to_lds<16>(X + x_src[j] + kx, st + x_dst[j]);
 #pragma unroll
@@ -1627,13 +1665,13 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
   }
   asm volatile("s_barrier\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
   static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_block_128x64<YT, AccV>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+  store_out_128x64<YT, AccV>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
                                    t0 + wn * TL::kWN, R, T, lane);
 }
 
 template <bool kFp8, bool kBlocked, bool kPat12, int YT>
 hipError_t run_smfmac_8bit(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                           const void* X, int64_t T, void* Y, hipStream_t s) {
+                           const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   constexpr int BM = 256, BN = 128, ST = 4;
   using TL = WsI8Tile<BM, BN, 2, 2, 4, ST>;
   auto kernel = smfmac_i8_ws_spmm_kernel<kFp8, kBlocked, kPat12, YT, BM, BN, 2, 2, 4, ST>;
@@ -1714,13 +1752,14 @@ template <bool BF16, bool kBlocked, int YT, int BM, int BN, int CWAVES_M, int CW
           int PWAVES, int STAGES, int XB = 16>
 __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     mfma48_ws_spmm_kernel(const uint16_t* __restrict__ values, const uint32_t* __restrict__ meta,
-                          const uint16_t* __restrict__ X, void* __restrict__ Y, int R, int K,
+                          const uint16_t* __restrict__ X, typename OutOf<YT>::type Y, int R, int K,
                           int T, TileMap map) {
   using TL = Ws48Tile<BM, BN, CWAVES_M, CWAVES_N, PWAVES, STAGES>;
   constexpr int kStages = STAGES;
   constexpr int kRB = TL::kXRowBytes;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  const int ldx = x_stride(Y, T);  // row length of X
   int tile_m, tile_n;
   if (!map.tile_of(blockIdx.x, tile_m, tile_n)) return;  // whole workgroup, before any load
   const int tid = threadIdx.x;
@@ -1754,14 +1793,14 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
         const int lc = 2 * ((pc >> 1) ^ xpair_swizzle(r)) + (pc & 1);
         int col = t0 + 8 * lc;
         col = col < T ? col : 0;
-        x_src[j] = ((int64_t)r * T + col) * 2;
+        x_src[j] = ((int64_t)r * ldx + col) * 2;
         x_dst[j] = (uint32_t)(w1k * 1024);
       } else {
         const int r = j * TL::kProducers + pw;  // one K row per load
         const int lp = (lane >> 3) ^ xpair_swizzle(r);
         int col = t0 + 16 * lp + 2 * (lane & 7);
         col = col < T ? col : 0;
-        x_src[j] = ((int64_t)r * T + col) * 2;
+        x_src[j] = ((int64_t)r * ldx + col) * 2;
         x_dst[j] = (uint32_t)(r * BN * 2);
       }
     }
@@ -1800,7 +1839,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     auto issue_step = [&](int step) {
       step = step < last_step ? step : last_step;
       uint8_t* st = smem + (step % kStages) * TL::kStageBytes;
-      const int64_t kx = (int64_t)step * kKStep * T * 2;
+      const int64_t kx = (int64_t)step * kKStep * ldx * 2;
       const int64_t ka = (int64_t)step * values_step_bytes<kBlocked>();
       const int64_t km = (int64_t)step * (kBlocked ? 192 : 12);
 #pragma unroll
@@ -1997,7 +2036,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
   }
   asm volatile("s_barrier" ::: "memory");  // the producers' last loads have landed
   static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_block_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
                          t0 + wn * TL::kWN, R, T, lane);
 }
 
@@ -2032,7 +2071,7 @@ __device__ __forceinline__ int ex_col(int c, int kk) {  // fp32: physical column
 template <int DT, int YT, int N, int M, bool kBlocked, bool kVecX>
 __global__ void __launch_bounds__(256)
     expand_mfma_spmm_kernel(const void* __restrict__ values, const uint32_t* __restrict__ meta,
-                            const void* __restrict__ X, void* __restrict__ Y, int64_t R,
+                            const void* __restrict__ X, typename OutOf<YT>::type Y, int64_t R,
                             int64_t K, int64_t T, int64_t tiles_n) {
   constexpr bool kF = DT == kF32;
   // fp8 and int8: widened to bf16 (exactly) when written to LDS.  int8 products are summed
@@ -2052,6 +2091,7 @@ __global__ void __launch_bounds__(256)
   static_assert(kItems * 256 == kEM * kGPS, "whole items per thread");
   static_assert(kXPieces * 256 * 16 == kEK * kEN * (int)sizeof(E), "whole X pieces");
   extern __shared__ __attribute__((aligned(16))) uint32_t ex_smem[];  // two stages
+  const int64_t ldx = x_stride(Y, T);  // row length of X
   const E* vals = static_cast<const E*>(values);
   const E* Xe = static_cast<const E*>(X);
   auto widen8 = [](uint32_t code) {  // an 8-bit element as fp32 (exact)
@@ -2076,12 +2116,12 @@ __global__ void __launch_bounds__(256)
       const int c = kPerChunk * (idx % kChunksPerRow);
       const int64_t k = k0 + kk, col = t0 + c;
       if constexpr (kVecX) {  // rows of X are whole 16-byte pieces
-        xr[j] = (k < K && col < T) ? *reinterpret_cast<const u32x4_t*>(Xe + k * T + col)
+        xr[j] = (k < K && col < T) ? *reinterpret_cast<const u32x4_t*>(Xe + k * ldx + col)
                                    : u32x4_t{0u, 0u, 0u, 0u};
       } else {  // any T: element loads, zeros past the last column
         uint32_t wv[4] = {0u, 0u, 0u, 0u};
         if (k < K) {
-          const E* src = Xe + k * T + col;
+          const E* src = Xe + k * ldx + col;
 #pragma unroll
           for (int e = 0; e < kPerChunk; ++e) {
             if (col + e < T) {
@@ -2283,6 +2323,21 @@ __global__ void __launch_bounds__(256)
   }
   // accumulator layout: lane (q, lr) of block (fm, fn) holds column lr and, in register e,
   // row 8 (e / 4) + 4 q + e % 4
+  if constexpr (YT == kAct) {  // every wave is past the loop's last barrier: LDS is free
+    static_assert(4 * kEpilogueBytes <= 2 * kEStageWords * 4, "epilogue LDS");
+    uint8_t* mine = reinterpret_cast<uint8_t*>(ex_smem) + wave * kEpilogueBytes;
+    if constexpr (kI) {
+      int16v_t sums[2][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sums[i >> 1][i & 1][e] = acc_i[i >> 1][i & 1][e];
+      finish_block<2>(sums, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
+    } else {
+      finish_block<2>(acc, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
+    }
+    return;
+  }
 #pragma unroll
   for (int fm = 0; fm < 2; ++fm)
 #pragma unroll
@@ -2291,11 +2346,13 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int64_t row = m0 + wm * 64 + fm * 32 + 8 * (e >> 2) + 4 * q + (e & 3);
-        if (row < R && col < T) {
-          if constexpr (kI)
-            static_cast<int32_t*>(Y)[row * T + col] = acc_i[fm][fn][e];
-          else
-            store_from_f32<YT>(Y, row * T + col, acc[fm][fn][e]);
+        if constexpr (YT != kAct) {
+          if (row < R && col < T) {
+            if constexpr (kI)
+              static_cast<int32_t*>(Y)[row * T + col] = acc_i[fm][fn][e];
+            else
+              store_from_f32<YT>(Y, row * T + col, acc[fm][fn][e]);
+          }
         }
       }
     }
@@ -2303,7 +2360,7 @@ __global__ void __launch_bounds__(256)
 
 template <int DT, int YT, bool kBlocked, bool kVecX>
 hipError_t run_expand(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
-                      int m, const void* X, int64_t T, void* Y, hipStream_t s) {
+                      int m, const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   const int64_t tiles_n = (T + kEN - 1) / kEN, tiles = (R + kEM - 1) / kEM * tiles_n;
   if (tiles > 0x7fffffff) return hipErrorInvalidValue;
   constexpr size_t lds = 2 * kEStageWords * sizeof(uint32_t);
@@ -2328,8 +2385,8 @@ hipError_t run_expand(const void* values, const uint32_t* meta, int64_t R, int64
 // X rows of whole 16-byte pieces take vector loads, any other T element loads.
 template <int DT, int YT>
 hipError_t run_expand_layout(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                             int n, int m, bool blocked, const void* X, int64_t T, void* Y,
-                             hipStream_t s) {
+                             int n, int m, bool blocked, const void* X, int64_t T,
+                             typename OutOf<YT>::type Y, hipStream_t s) {
   const bool vec = T % (DT == kF32 ? 4 : (DT == kFP8 || DT == kI8) ? 16 : 8) == 0;
   if (vec)
     return blocked ? run_expand<DT, YT, true, true>(values, meta, R, K, n, m, X, T, Y, s)
@@ -2338,7 +2395,7 @@ hipError_t run_expand_layout(const void* values, const uint32_t* meta, int64_t R
                  : run_expand<DT, YT, false, false>(values, meta, R, K, n, m, X, T, Y, s);
 }
 
-__global__ void zero_fill_kernel(uint32_t* __restrict__ p, int64_t words, int64_t tail_halves) {
+[[maybe_unused]] __global__ void zero_fill_kernel(uint32_t* __restrict__ p, int64_t words, int64_t tail_halves) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i < words) p[i] = 0u;
   if (i == words && tail_halves) reinterpret_cast<uint16_t*>(p + words)[0] = 0;
@@ -2358,10 +2415,11 @@ using TileOf = std::conditional_t<
 template <bool BF16, bool kPat12, bool kBlocked, int YT, int KIND, int BM, int BN, int WM_,
           int WN_, int PW, int ST_, int XB = 16>
 hipError_t launch_tile(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                       const void* X, int64_t T, void* Y, hipStream_t s) {
+                       const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   using TL = TileOf<KIND, BM, BN, WM_, WN_, PW, ST_>;
   const int tiles_m = (int)((R + BM - 1) / BM), tiles_n = (int)((T + BN - 1) / BN);
-  void (*kernel)(const uint16_t*, const uint32_t*, const uint16_t*, void*, int, int, int, TileMap);
+  void (*kernel)(const uint16_t*, const uint32_t*, const uint16_t*, typename OutOf<YT>::type, int,
+                 int, int, TileMap);
   if constexpr (KIND == 0)
     kernel = smfmac_spmm_kernel<BF16, kPat12, kBlocked, YT, BM, BN, WM_, WN_, ST_>;
   else if constexpr (KIND == 1)
@@ -2394,7 +2452,7 @@ constexpr TileChoice kTiles[kNumTiles] = {{256, 256, 1720.0}, {256, 128, 1900.0}
                                           {128, 128, 1150.0}};
 constexpr double kTileFixedUs = 5.0;
 
-int pick_tile(int64_t R, int64_t K, int64_t T) {
+[[maybe_unused]] int pick_tile(int64_t R, int64_t K, int64_t T) {
   // NM_SPMM_TILE=0/1/2 pins one shape (used by the tests to cover every shape)
   if (const char* e = getenv("NM_SPMM_TILE")) {
     if (e[0] >= '0' && e[0] < '0' + kNumTiles && e[1] == 0) return e[0] - '0';
@@ -2420,7 +2478,7 @@ int pick_tile(int64_t R, int64_t K, int64_t T) {
 
 template <bool BF16, bool kPat12, bool kBlocked, int YT>
 hipError_t run_smfmac(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                      const void* X, int64_t T, void* Y, hipStream_t s) {
+                      const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   if (T % 8 != 0)  // even T: the wave-specialised tile with 4-byte X pieces
     return launch_tile<BF16, kPat12, kBlocked, YT, 2, 256, 128, 2, 2, 4, 4, 4>(values, meta, R,
                                                                               K, X, T, Y, s);
@@ -2440,7 +2498,7 @@ hipError_t run_smfmac(const void* values, const uint32_t* meta, int64_t R, int64
 // 4:8, 16-bit, either layout: dense matrix cores on expanded groups, 256 x 128 tiles.
 template <bool BF16, bool kBlocked, int YT, int XB>
 hipError_t run_mfma48(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                      const void* X, int64_t T, void* Y, hipStream_t s) {
+                      const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   constexpr int BM = 256, BN = 128, ST = 4;
   using TL = Ws48Tile<BM, BN, 2, 2, 4, ST>;
   const int tiles_m = (int)((R + BM - 1) / BM), tiles_n = (int)((T + BN - 1) / BN);
@@ -2459,12 +2517,14 @@ hipError_t run_mfma48(const void* values, const uint32_t* meta, int64_t R, int64
 
 template <bool BF16, bool kPat12, int YT>
 hipError_t run_smfmac_layout(const void* values, const uint32_t* meta, int64_t R, int64_t K,
-                             bool blocked, const void* X, int64_t T, void* Y, hipStream_t s) {
+                             bool blocked, const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
   return blocked ? run_smfmac<BF16, kPat12, true, YT>(values, meta, R, K, X, T, Y, s)
                  : run_smfmac<BF16, kPat12, false, YT>(values, meta, R, K, X, T, Y, s);
 }
 
 }  // namespace
+
+#ifndef NM_SPMM_PART
 
 // XCDs of the current device: MI355X (gfx950) has 8, with 32 compute units each.
 // Looked up once per device.
@@ -2589,5 +2649,80 @@ hipError_t launch_spmm(const void* values, const uint32_t* meta, int64_t R, int6
              ? run_expand_layout<kF16, kF32>(values, meta, R, K, n, m, blocked, X, T, Y, s)
              : run_expand_layout<kF16, kF16>(values, meta, R, K, n, m, blocked, X, T, Y, s);
 }
+
+#elif NM_SPMM_PART == 1
+
+// The product with its epilogue on the matrix-core kernels above, X's rows of ep.ldx numbers in whole
+// 16-byte pieces; what they do not take goes to the expansion kernel (launch_expand_act).
+hipError_t launch_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                           int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
+                           hipStream_t s) {
+  const Epilogue Y = epilogue_of(p);
+  const bool pat24 = (n == 2 && m == 4), pat12 = (n == 1 && m == 2);
+  const bool half = dt == kBF16 || dt == kF16, b = dt == kBF16;
+  // sizes as launch_spmm
+  const bool sparse_shape =
+      K > 0 && K % kKStep == 0 && R < (1 << 30) && Y.ldx < (1 << 28) && K < (1 << 28);
+  if (half && sparse_shape && n == 4 && m == 8) {
+#define NM_48(BF, BL) return run_mfma48<BF, BL, kAct, 16>(values, meta, R, K, X, T, Y, s)
+    if (b) {
+      if (blocked) NM_48(true, true);
+      NM_48(true, false);
+    }
+    if (blocked) NM_48(false, true);
+    NM_48(false, false);
+#undef NM_48
+  }
+  if (half && sparse_shape && (pat24 || pat12)) {
+#define NM_S(BF, P12) return run_smfmac_layout<BF, P12, kAct>(values, meta, R, K, blocked, X, T, Y, s)
+    if (b) {
+      if (pat24) NM_S(true, false);
+      NM_S(true, true);
+    }
+    if (pat24) NM_S(false, false);
+    NM_S(false, true);
+#undef NM_S
+  }
+  const bool tiled_8bit = (dt == kI8 || dt == kFP8) && (pat24 || pat12) && K > 0 &&
+                          K % kI8KStep == 0 && R < (1 << 30) && Y.ldx < (1 << 30) && K < (1 << 30);
+  if (tiled_8bit) {
+#define NM_8(FP8, BL, P12) return run_smfmac_8bit<FP8, BL, P12, kAct>(values, meta, R, K, X, T, Y, s)
+    if (dt == kFP8) {
+      if (blocked) {
+        if (pat12) NM_8(true, true, true);
+        NM_8(true, true, false);
+      }
+      if (pat12) NM_8(true, false, true);
+      NM_8(true, false, false);
+    }
+    if (blocked) {
+      if (pat12) NM_8(false, true, true);
+      NM_8(false, true, false);
+    }
+    if (pat12) NM_8(false, false, true);
+    NM_8(false, false, false);
+#undef NM_8
+  }
+  return launch_expand_act(values, meta, R, K, n, m, blocked, X, T, dt, p, s);
+}
+
+#else
+
+hipError_t launch_expand_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
+                             int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
+                             hipStream_t s) {
+  const Epilogue Y = epilogue_of(p);
+#define NM_E(DT)                                                                            \
+  return blocked ? run_expand<DT, kAct, true, true>(values, meta, R, K, n, m, X, T, Y, s)   \
+                 : run_expand<DT, kAct, false, true>(values, meta, R, K, n, m, X, T, Y, s)
+  if (dt == kF32) NM_E(kF32);
+  if (dt == kBF16) NM_E(kBF16);
+  if (dt == kF16) NM_E(kF16);
+  if (dt == kI8) NM_E(kI8);
+  NM_E(kFP8);
+#undef NM_E
+}
+
+#endif
 
 }  // namespace nm

@@ -98,6 +98,50 @@ struct XentGradCut {
   }
 };
 
+// ---- gradient of the compressed product ---------------------------------------------------------
+
+// Both products of nm_spmm_act_grad in one launch: a tile size for both, and the splits of their sums
+// (dX's over R, dW's over T).  Estimated time: all tiles' work in a steady flow over the units, but no
+// less than the longest tile, plus the splits' sums written and read (5 GB a ms) and a launch to join
+// them.
+struct SpmmGradCut {
+  int tile = kTile256, splits_x = 1, splits_w = 1;
+  SpmmGradCut(int64_t R, int64_t K, int64_t T, bool want_w, bool want_x) {
+    const int64_t sx = pad64(R) / 64, sw = pad64(T) / 64;
+    const auto next = [](int z) { return z < 4 ? z + 1 : z + 2; };
+    const auto alone = [](int t, int64_t s) {
+      return t == kTile256 ? 2.0 * s + 8 : t == kTile128 ? 0.65 * s + 4 : 0.45 * s + 3;
+    };
+    const auto flow = [](int t, int64_t count, int64_t s) {
+      return t == kTile256 ? count * (2.0 * s + 8) / 256
+                           : count * (t == kTile128 ? 1.19 * s + 4.6 : 0.71 * s + 3.5) / 512;
+    };
+    const auto join = [](int z, int64_t numbers) { return z == 1 ? 0.0 : 3.0 + z * numbers * 8 / 5e6; };
+    double least = 1e30;
+    for (int t = 0; t < kXentTiles; ++t)
+      for (int zx = 1; zx <= kMaxSplit && (zx == 1 || (want_x && sx / zx >= 4)); zx = next(zx))
+        for (int zw = 1; zw <= kMaxSplit && (zw == 1 || (want_w && sw / zw >= 4)); zw = next(zw)) {
+          const int64_t lx = (sx + zx - 1) / zx, lw = (sw + zw - 1) / zw;
+          double us = 0, longest = 0;
+          if (want_x) {
+            us += flow(t, tiles_of(t, K, T) * zx, lx);
+            longest = alone(t, lx);
+          }
+          if (want_w) {
+            us += flow(t, tiles_of(t, R, K) * zw, lw);
+            longest = std::max(longest, alone(t, lw));
+          }
+          us = std::max(us, longest) + (want_x ? join(zx, K * T) : 0) + (want_w ? join(zw, R * K) : 0);
+          if (us < least) {
+            least = us;
+            tile = t;
+            splits_x = zx;
+            splits_w = zw;
+          }
+        }
+  }
+};
+
 // ---- orthogonalised update ---------------------------------------------------------------------
 
 // Square tiles of four sizes; a launch takes the one with the smallest estimated time: rounds of
