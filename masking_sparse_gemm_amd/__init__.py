@@ -38,8 +38,8 @@ record R, so decompress and spmm take it as ``rows=``.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
+import operator
 import os
 
 import torch
@@ -725,11 +725,15 @@ def orthogonalize(G: torch.Tensor, steps: int = 5, eps: float = 1e-7,
 # ---- a product with its epilogue, and the gradient --------------------------------------------
 
 
-def _device_of(t: torch.Tensor):
-    """t's device as the current one: the library launches on the current device."""
+def _launch(name: str, t: torch.Tensor, *args) -> None:
+    """The library's call `name`, with t's device as the current one, on which it launches."""
+    f = getattr(lib(), name)
     if torch._C._cuda_getDevice() == t.get_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+        rc = f(*args, _current_stream(t))
+    else:
+        with torch.cuda.device(t.device):
+            rc = f(*args, _current_stream(t))
+    _check(name, rc)
 
 
 def _act(act: str) -> int:
@@ -791,12 +795,11 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
         out = X.new_empty((R, T), dtype=y_dtype)
     Z = X.new_empty((R, T)) if keep else None
     L = lib()
-    with _device_of(X):
-        ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(K, T, dt))
-        _check("nm_spmm_act", L.nm_spmm_act(
-            values.data_ptr(), meta.data_ptr(), R, K, n, m, _layout(layout), X.data_ptr(), T, dt,
-            _addr(scale), _addr(bias), code, _addr(residual), _addr(Z), out.data_ptr(),
-            _DT[y_dtype], ws_ptr, 0 if ws is None else ws.numel(), _current_stream(X)))
+    ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(K, T, dt))
+    _launch("nm_spmm_act", X,
+        values.data_ptr(), meta.data_ptr(), R, K, n, m, _layout(layout), X.data_ptr(), T, dt,
+        _addr(scale), _addr(bias), code, _addr(residual), _addr(Z), out.data_ptr(),
+        _DT[y_dtype], ws_ptr, 0 if ws is None else ws.numel())
     return (out, Z) if keep else out
 
 
@@ -844,14 +847,13 @@ def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: tor
     res = {w: dY.new_empty(shapes[w][0], dtype=shapes[w][1]) for w in want}
     L = lib()
     dx = "dX" in want
-    with _device_of(dY):
-        ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_workspace_bytes(
-            R, K, T, code, "dW" in want, dx, "dZ" in want))
-        _check("nm_spmm_act_grad", L.nm_spmm_act_grad(
-            _addr(values) if dx else None, _addr(meta) if dx else None, R, K, n, m, lay,
-            _addr(X) if "dW" in want else None, T, dt, code, _addr(Z) if code else None,
-            dY.data_ptr(), _addr(res.get("dW")), _addr(res.get("dX")), _addr(res.get("dbias")),
-            _addr(res.get("dZ")), ws_ptr, 0 if ws is None else ws.numel(), _current_stream(dY)))
+    ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_workspace_bytes(
+        R, K, T, code, "dW" in want, dx, "dZ" in want))
+    _launch("nm_spmm_act_grad", dY,
+        _addr(values) if dx else None, _addr(meta) if dx else None, R, K, n, m, lay,
+        _addr(X) if "dW" in want else None, T, dt, code, _addr(Z) if code else None,
+        dY.data_ptr(), _addr(res.get("dW")), _addr(res.get("dX")), _addr(res.get("dbias")),
+        _addr(res.get("dZ")), ws_ptr, 0 if ws is None else ws.numel())
     return tuple(res[w] for w in want)
 
 
@@ -886,12 +888,11 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
     if out is None:
         out = X.new_empty((rows, T), dtype=y_dtype)
     L = lib()
-    with _device_of(X):
-        ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
-        _check("nm_matvec_act", L.nm_matvec_act(
-            codes.data_ptr(), scales.data_ptr(), _addr(meta), rows, K, group, X.data_ptr(), T, dt,
-            _addr(bias), code, _addr(residual), out.data_ptr(), _DT[y_dtype], ws_ptr,
-            0 if ws is None else ws.numel(), _current_stream(X)))
+    ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
+    _launch("nm_matvec_act", X,
+        codes.data_ptr(), scales.data_ptr(), _addr(meta), rows, K, group, X.data_ptr(), T, dt,
+        _addr(bias), code, _addr(residual), out.data_ptr(), _DT[y_dtype], ws_ptr,
+        0 if ws is None else ws.numel())
     return out
 
 
@@ -901,6 +902,9 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
 _FLOAT_DT = {torch.float32: NM_F32, torch.float16: NM_F16, torch.bfloat16: NM_BF16}
 
 
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 class _Tensors:
     """The host arrays that nm_grad_norm and nm_clip_grads take, of dense float tensors on one GPU."""
 
@@ -908,21 +912,29 @@ class _Tensors:
         self.grads = grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
         if not grads:
             raise ValueError("no tensors")
-        device = grads[0].device
-        if device.type != "cuda":
-            raise ValueError("gradients must be on a GPU")
-        for g in grads:
-            if g.dtype not in _FLOAT_DT or g.device != device or not (
-                    g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous())):
-                raise ValueError("gradients must be float32, float16 or bfloat16 tensors without gaps "
-                                 "on one GPU")
-        self.pointers = array.array("q", [g.data_ptr() for g in grads])
-        self.counts = array.array("q", [g.numel() for g in grads])
-        self.dts = array.array("i", [_FLOAT_DT[g.dtype] for g in grads])
+        self.device = grads[0].device
+        dts = list(map(_FLOAT_DT.get, map(_dtype_of, grads)))
+        # (a step of a model has hundreds of tensors: one look at all of them for each property)
+        self.contiguous = all(map(torch.Tensor.is_contiguous, grads))
+        if self.device.type != "cuda" or None in dts or \
+                len(set(map(torch.Tensor.get_device, grads))) != 1 or not (self.contiguous or all(
+                    g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous()) for g in grads)):
+            raise ValueError("gradients must be float32, float16 or bfloat16 tensors without gaps on "
+                             "one GPU")
+        self.pointers = array.array("q", map(torch.Tensor.data_ptr, grads))
+        self.counts = array.array("q", map(torch.Tensor.numel, grads))
+        self.dts = array.array("i", dts)
 
     def addresses(self):
         return (self.pointers.buffer_info()[0], self.counts.buffer_info()[0],
                 self.dts.buffer_info()[0], len(self.counts))
+
+    def same_places(self, other) -> bool:
+        """Whether entry i of a tensor here stands for entry i of the other's."""
+        return (self.dts == other.dts and self.device == other.device and
+                list(map(_shape_of, self.grads)) == list(map(_shape_of, other.grads)) and
+                ((self.contiguous and other.contiguous) or all(
+                    a.stride() == b.stride() for a, b in zip(self.grads, other.grads))))
 
 
 def grad_norm(grads) -> torch.Tensor:
@@ -933,10 +945,9 @@ def grad_norm(grads) -> torch.Tensor:
     norm = like.new_empty((), dtype=torch.float32)
     ptrs, counts, dts, n = t.addresses()
     L = lib()
-    with _device_of(like):
-        ws, ws_ptr = _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
-        _check("nm_grad_norm", L.nm_grad_norm(ptrs, counts, dts, n, norm.data_ptr(), ws_ptr,
-                                              0 if ws is None else ws.numel(), _current_stream(like)))
+    ws, ws_ptr = _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
+    _launch("nm_grad_norm", like, ptrs, counts, dts, n, norm.data_ptr(), ws_ptr,
+                                          0 if ws is None else ws.numel())
     return norm
 
 
@@ -947,9 +958,7 @@ def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=Non
     where each rank holds a part of them: join grad_norm's squares over the ranks first."""
     t = _Tensors(grads)
     o = t if out is None else _Tensors(out)
-    if o is not t and (len(o.grads) != len(t.grads) or any(
-            a.shape != b.shape or a.dtype != b.dtype or a.device != b.device or
-            (a.stride() != b.stride() and a.numel() > 0) for a, b in zip(t.grads, o.grads))):
+    if o is not t and not o.same_places(t):
         raise ValueError("out must match the gradients' shapes, strides, dtypes and device")
     like = t.grads[0]
     given = norm
@@ -959,12 +968,11 @@ def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=Non
         raise ValueError("norm must be one float32 number on the gradients' device")
     ptrs, counts, dts, n = t.addresses()
     L = lib()
-    with _device_of(like):
-        ws, ws_ptr = (None, None) if given is not None else \
-            _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
-        _check("nm_clip_grads", L.nm_clip_grads(
-            ptrs, o.pointers.buffer_info()[0], counts, dts, n, float(max_norm), _addr(given),
-            norm.data_ptr(), ws_ptr, 0 if ws is None else ws.numel(), _current_stream(like)))
+    ws, ws_ptr = (None, None) if given is not None else \
+        _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
+    _launch("nm_clip_grads", like,
+        ptrs, o.pointers.buffer_info()[0], counts, dts, n, float(max_norm), _addr(given),
+        norm.data_ptr(), ws_ptr, 0 if ws is None else ws.numel())
     return norm
 
 
@@ -1010,10 +1018,9 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     if out is None:
         out = torch.empty_like(logits)
     L = lib()
-    with _device_of(logits):
-        ws, ws_ptr = _workspace(logits, L.nm_adjust_logits_workspace_bytes(V, T, count))
-        _check("nm_adjust_logits", L.nm_adjust_logits(
-            logits.data_ptr(), dt, V, T, _addr(tokens), count, _addr(starts), _addr(prompts),
-            *map(_addr, penalties), _addr(bias), each, _addr(allowed), out.data_ptr(), ws_ptr,
-            0 if ws is None else ws.numel(), _current_stream(logits)))
+    ws, ws_ptr = _workspace(logits, L.nm_adjust_logits_workspace_bytes(V, T, count))
+    _launch("nm_adjust_logits", logits,
+        logits.data_ptr(), dt, V, T, _addr(tokens), count, _addr(starts), _addr(prompts),
+        *map(_addr, penalties), _addr(bias), each, _addr(allowed), out.data_ptr(), ws_ptr,
+        0 if ws is None else ws.numel())
     return out

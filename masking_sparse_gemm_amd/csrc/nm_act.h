@@ -44,8 +44,8 @@ __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
   return z < 0.f ? tail : 1.f - tail;
 }
 
-// z times a share of it; a share of 0 gives 0 (-0) for z = -infinity too.
-__device__ __forceinline__ float share_of(float z, float s) { return s == 0.f ? 0.f * s : z * s; }
+// z times a share of it; a share of 0 gives -0 for z = -infinity too (a NaN is in the share as well).
+__device__ __forceinline__ float share_of(float z, float s) { return fmaxf(z, -3.402823466e38f) * s; }
 
 // act(v) of N numbers; the choice is the same for the whole launch, so it is made once for all of them.
 template <int N>
@@ -273,54 +273,66 @@ __device__ __forceinline__ void finish_one(const Epilogue& ep, int64_t row, int6
   put(ep.y, ep.y_dt, v[0]);
 }
 
-// A wave's 32 rows x 64 columns of sums, as fp32 in its own part of LDS (row-major, kSlabPitch
-// floats a row).  A lane takes pieces k = 0 .. 3: row 8 k + lane / 8, eight columns from
-// 8 (lane % 8).  The residual and the row's scale and bias are loaded ahead (SlabInputs), so that
-// they are under way while the slab before is worked on.
-constexpr int kSlabPitch = 68;  // floats: a padded row, as kEpilogueBytes has it
-static_assert(32 * kSlabPitch * 4 <= kEpilogueBytes, "a slab fits a wave's part");
+// 64 rows x 64 columns of sums in LDS, fp32, row-major, kSlabPitch floats a row (padded against bank
+// conflicts), finished by one wave.  A lane takes eight columns from 8 (lane % 8) of rows
+// 8 k + lane / 8, k = 0 .. 7, in two groups of four; a group's residual, scales and biases are loaded
+// (GroupInputs) before the group ahead of it is worked on, the first ones before the slab is written.
+// DT: the product's type, which Z has, and Y if it is not fp32 (8-bit products: any Y).
+constexpr int kSlabPitch = 68;
+constexpr int kSlabBytes = 64 * kSlabPitch * 4;
 
-struct SlabInputs {
+struct GroupInputs {
   RawEight residual[4];
   float scale[4], bias[4];
 };
 
-__device__ __forceinline__ void slab_load(SlabInputs& in, const Epilogue& ep, int64_t row0,
-                                          int64_t col0, int64_t R, int64_t T, int lane) {
+template <int DT>
+__device__ __forceinline__ int y_type(const Epilogue& ep) {
+  if constexpr (DT == kF32) return kF32;
+  else if constexpr (DT == kBF16 || DT == kF16) return ep.y_dt == kF32 ? kF32 : DT;
+  else return ep.y_dt;
+}
+
+template <int DT>
+__device__ __forceinline__ void group_load(GroupInputs& in, const Epilogue& ep, int64_t row0,
+                                           int64_t col0, int64_t R, int64_t T, int lane) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t row = row0 + 8 * k + (lane >> 3), col = col0 + 8 * (lane & 7);
     const bool live = row < R && col < T;
     in.scale[k] = ep.scale && live ? ep.scale[row] : 1.f;
     in.bias[k] = ep.bias && live ? ep.bias[row] : 0.f;
-    if (ep.residual && live) in.residual[k] = load_eight(ep.residual, ep.y_dt, row * T + col, T - col);
+    if (ep.residual && live)
+      in.residual[k] = load_eight(ep.residual, y_type<DT>(ep), row * T + col, T - col);
   }
 }
 
-__device__ __forceinline__ void slab_finish(const SlabInputs& in, const float* slab,
-                                            const Epilogue& ep, int64_t row0, int64_t col0, int64_t R,
-                                            int64_t T, int lane) {
-  SlabInputs cur = in;
+template <int DT>
+__device__ __forceinline__ void group_finish(const GroupInputs& in, const float* slab,
+                                             const Epilogue& ep, int64_t row0, int64_t col0, int64_t R,
+                                             int64_t T, int lane) {
+  GroupInputs cur = in;
+  const int64_t col = col0 + 8 * (lane & 7), left = T - col;
+  int64_t row = row0 + (lane >> 3), i = row * T + col;
+  const float* sums = slab + (lane >> 3) * kSlabPitch + 8 * (lane & 7);
 #pragma unroll 1  // the activations' code once: cur's pieces move down instead
-  for (int k = 0; k < 4; ++k) {
-    const int r = 8 * k + (lane >> 3), c = 8 * (lane & 7);
-    const int64_t row = row0 + r, col = col0 + c;
-    if (row < R && col < T) {
-      const float4_t a = *reinterpret_cast<const float4_t*>(slab + r * kSlabPitch + c);
-      const float4_t b = *reinterpret_cast<const float4_t*>(slab + r * kSlabPitch + c + 4);
+  for (int k = 0; k < 4; ++k, row += 8, i += 8 * T, sums += 8 * kSlabPitch) {
+    if (row < R && left > 0) {
+      const float4_t a = *reinterpret_cast<const float4_t*>(sums);
+      const float4_t b = *reinterpret_cast<const float4_t*>(sums + 4);
       float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], cur.scale[0], cur.bias[0]);
-      const int64_t i = row * T + col;
-      if (ep.z) store_eight(ep.z, ep.z_dt, i, T - col, v);
+      if constexpr (DT == kF32 || DT == kBF16 || DT == kF16)
+        if (ep.z) store_eight(ep.z, DT, i, left, v);
       act_values(ep.act, v);
       if (ep.residual) {
         float x[8];
-        to_floats(cur.residual[0], ep.y_dt, x);
+        to_floats(cur.residual[0], y_type<DT>(ep), x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += x[e];
       }
-      store_eight(ep.y, ep.y_dt, i, T - col, v);
+      store_eight(ep.y, y_type<DT>(ep), i, left, v);
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -331,45 +343,90 @@ __device__ __forceinline__ void slab_finish(const SlabInputs& in, const float* s
   }
 }
 
-// Stores a wave's FM blocks of 32 rows x 64 columns, accumulators as of store_block_128x64.
-template <int FM, typename AccV>
+// The slab's two groups; `first` are the first one's inputs.
+template <int DT>
+__device__ __forceinline__ void slab_finish(const GroupInputs& first, const float* slab,
+                                            const Epilogue& ep, int64_t row0, int64_t col0, int64_t R,
+                                            int64_t T, int lane) {
+  GroupInputs in = first;
+#pragma unroll 1
+  for (int g = 0; g < 2; ++g) {
+    const GroupInputs now = in;
+    if (g == 0) group_load<DT>(in, ep, row0 + 32, col0, R, T, lane);
+    group_finish<DT>(now, slab + g * 32 * kSlabPitch, ep, row0 + 32 * g, col0, R, T, lane);
+  }
+}
+
+// Two fragments down of 32 rows x 64 columns (layout as of store_block_128x64) to LDS.
+template <typename AccV>
+__device__ __forceinline__ void slab_write(const AccV (&a)[2], const AccV (&b)[2], float* slab,
+                                           int lane) {
+  const int l32 = lane & 31, q = lane >> 5;
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float* d = slab + (8 * (i / 4) + 4 * q + (i % 4)) * kSlabPitch + 32 * f + l32;
+      d[0] = (float)a[f][i];
+      d[32 * kSlabPitch] = (float)b[f][i];
+    }
+}
+
+// LDS serves a wave in order: between its writes and its other lanes' reads only the compiler has to
+// keep it.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
+// Stores a wave's FM (2 or 4) blocks of 32 rows x 64 columns through its own kSlabBytes of LDS.
+template <int DT, int FM, typename AccV>
 __device__ __forceinline__ void finish_block(const AccV (&acc)[FM][2], uint8_t* lds,
                                              const Epilogue& ep, int64_t row0, int64_t col0,
                                              int64_t R, int64_t T, int lane) {
-  const int l32 = lane & 31, q = lane >> 5;
   float* slab = reinterpret_cast<float*>(lds);
   AccV cur[FM][2];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int f = 0; f < 2; ++f) cur[i][f] = acc[i][f];
-  SlabInputs in;
-  slab_load(in, ep, row0, col0, R, T, lane);
-#pragma unroll 1
-  for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll 1  // (as in group_finish)
+  for (int h = 0; h < FM / 2; ++h) {
+    GroupInputs in;
+    group_load<DT>(in, ep, row0 + 64 * h, col0, R, T, lane);
+    slab_write(cur[0], cur[1], slab, lane);
+    keep_order();
+    slab_finish<DT>(in, slab, ep, row0 + 64 * h, col0, R, T, lane);
+    keep_order();
+    if constexpr (FM == 4) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        slab[(8 * (i / 4) + 4 * q + (i % 4)) * kSlabPitch + 32 * f + l32] = (float)cur[0][f][i];
-    const SlabInputs now = in;
-    if (fm + 1 < FM) slab_load(in, ep, row0 + 32 * (fm + 1), col0, R, T, lane);
-    asm volatile("" ::: "memory");  // LDS serves a wave in order: only the compiler has to keep it
-    slab_finish(now, slab, ep, row0 + 32 * fm, col0, R, T, lane);
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int i = 0; i + 1 < FM; ++i)
-#pragma unroll
-      for (int f = 0; f < 2; ++f) cur[i][f] = cur[i + 1][f];
+        for (int f = 0; f < 2; ++f) cur[i][f] = cur[i + 2][f];
+    }
   }
 }
 
-// A wave's block of a product to its output, of either kind.
-template <int YT, typename AccV = float16v_t>
+// The same for a workgroup of four waves that hold 128 x 64 blocks each and four that do not: the
+// blocks go to LDS whole, and all eight waves finish half of one each, since the activation's
+// arithmetic would keep four waves longer than their stores.  Wave w has block w % 4 and half w / 4.
+constexpr int kBlockBytes = 2 * kSlabBytes;
+__device__ __forceinline__ float* slab_of(uint8_t* smem, int wave) {
+  return reinterpret_cast<float*>(smem + (wave & 3) * kBlockBytes + (wave >> 2) * kSlabBytes);
+}
+template <int DT>
+__device__ __forceinline__ void finish_half(uint8_t* smem, const Epilogue& ep, int m0, int t0, int R,
+                                            int T, int wave, int lane) {
+  const int row0 = m0 + ((wave & 3) >> 1) * 128 + (wave >> 2) * 64, col0 = t0 + (wave & 1) * 64;
+  GroupInputs in;
+  group_load<DT>(in, ep, row0, col0, R, T, lane);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every block is in LDS
+  slab_finish<DT>(in, slab_of(smem, wave), ep, row0, col0, R, T, lane);
+}
+
+// A wave's block of a product to its output, of either kind (DT: as above).
+template <int DT, int YT, typename AccV = float16v_t>
 __device__ __forceinline__ void store_out_128x64(const AccV (&acc)[4][2], uint8_t* lds,
                                                  const typename OutOf<YT>::type& Y, int row0,
                                                  int col0, int R, int T, int lane) {
-  if constexpr (YT == kAct) finish_block<4>(acc, lds, Y, row0, col0, R, T, lane);
+  if constexpr (YT == kAct) finish_block<DT, 4>(acc, lds, Y, row0, col0, R, T, lane);
   else store_block_128x64<YT, AccV>(acc, lds, Y, row0, col0, R, T, lane);
 }
 

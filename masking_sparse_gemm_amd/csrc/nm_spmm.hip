@@ -414,31 +414,22 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
 
   // ---- epilogue: lane holds rows 4q..4q+3, column l16 of each 16x16 fragment ----
   if constexpr (YT == kAct) {
-    static_assert(FM % 2 == 0 && FN == 4, "slabs of 32 rows x 64 columns");
-    static_assert(TL::kWaves * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-    float* slab = reinterpret_cast<float*>(smem + wave * kEpilogueBytes);
+    static_assert(FM == 4 && FN == 4, "a slab of 64 rows x 64 columns");
+    static_assert(TL::kWaves * kSlabBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    constexpr int kDT = BF16 ? kBF16 : kF16;
+    float* slab = reinterpret_cast<float*>(smem + wave * kSlabBytes);
     const int row0 = m0 + wm * TL::kWM, col0 = t0 + wn * TL::kWN;
-    SlabInputs in;
-    slab_load(in, Y, row0, col0, R, T, lane);
-#pragma unroll 1
-    for (int g = 0; g < FM / 2; ++g) {
+    GroupInputs in;
+    group_load<kDT>(in, Y, row0, col0, R, T, lane);
 #pragma unroll
-      for (int fm = 0; fm < 2; ++fm)
+    for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
+      for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            slab[(16 * fm + 4 * q + i) * kSlabPitch + 16 * fn + l16] = acc[fm][fn][i];
-      const SlabInputs now = in;
-      if (g + 1 < FM / 2) slab_load(in, Y, row0 + 32 * (g + 1), col0, R, T, lane);
-      asm volatile("" ::: "memory");
-      slab_finish(now, slab, Y, row0 + 32 * g, col0, R, T, lane);
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int fm = 0; fm + 2 < FM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn) acc[fm][fn] = acc[fm + 2][fn];
-    }
+        for (int i = 0; i < 4; ++i)
+          slab[(16 * fm + 4 * q + i) * kSlabPitch + 16 * fn + l16] = acc[fm][fn][i];
+    keep_order();
+    slab_finish<kDT>(in, slab, Y, row0, col0, R, T, lane);
     return;
   }
 #pragma unroll
@@ -805,9 +796,10 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N)
   // to land before plain instructions read the accumulators
   wait_loads_and_barrier<0>();
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-  static_assert(TL::kWaves * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
-                         t0 + wn * TL::kWN, R, T, lane);
+  constexpr int kPart = YT == kAct ? kSlabBytes : kEpilogueBytes;  // of a wave
+  static_assert(TL::kWaves * kPart <= kStages * TL::kStageBytes, "epilogue LDS");
+  store_out_128x64<BF16 ? kBF16 : kF16, YT>(acc, smem + wave * kPart, Y, m0 + wm * TL::kWM,
+                                            t0 + wn * TL::kWN, R, T, lane);
 }
 
 // The 2:4 consumer's whole K loop as one asm statement, so that LDS reads can stay in
@@ -1354,6 +1346,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     }
     // loads past the end have landed before the consumers reuse LDS for the epilogue
     wait_loads_and_barrier<0>();
+    if constexpr (YT == kAct) finish_half<BF16 ? kBF16 : kF16>(smem, Y, m0, t0, R, T, wave, lane);
     return;
   }
 
@@ -1395,9 +1388,17 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
   // the producers' last loads have landed (final barrier), and the last smfmac results
   // get time to land before plain instructions read the accumulators
   asm volatile("s_barrier\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-  static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
-                         t0 + wn * TL::kWN, R, T, lane);
+  if constexpr (YT == kAct) {
+    static_assert(CWAVES_M == 2 && CWAVES_N == 2 && PWAVES == 4, "blocks as finish_half has them");
+    static_assert(4 * kBlockBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    slab_write(acc[0], acc[1], slab_of(smem, wave), lane);
+    slab_write(acc[2], acc[3], slab_of(smem, wave + 4), lane);
+    finish_half<BF16 ? kBF16 : kF16>(smem, Y, m0, t0, R, T, wave, lane);
+  } else {
+    static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    store_block_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+                             t0 + wn * TL::kWN, R, T, lane);
+  }
 }
 
 // ===========================================================================
@@ -1563,6 +1564,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
       wait_loads_and_barrier<(kStages - 3) * TL::kLoads>();  // step s+2 landed
     }
     wait_loads_and_barrier<0>();  // no load in flight when the consumers reuse LDS
+    if constexpr (YT == kAct) finish_half<kFp8 ? kFP8 : kI8>(smem, Y, m0, t0, R, T, wave, lane);
     return;
   }
 
@@ -1664,9 +1666,17 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     asm volatile("s_barrier" ::: "memory");  // step s+2 landed; stage of step s released
   }
   asm volatile("s_barrier\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
-  static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_out_128x64<YT, AccV>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
-                                   t0 + wn * TL::kWN, R, T, lane);
+  if constexpr (YT == kAct) {
+    static_assert(CWAVES_M == 2 && CWAVES_N == 2 && PWAVES == 4, "blocks as finish_half has them");
+    static_assert(4 * kBlockBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    slab_write(acc[0], acc[1], slab_of(smem, wave), lane);
+    slab_write(acc[2], acc[3], slab_of(smem, wave + 4), lane);
+    finish_half<kFp8 ? kFP8 : kI8>(smem, Y, m0, t0, R, T, wave, lane);
+  } else {
+    static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    store_block_128x64<YT, AccV>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+                             t0 + wn * TL::kWN, R, T, lane);
+  }
 }
 
 template <bool kFp8, bool kBlocked, bool kPat12, int YT>
@@ -1894,6 +1904,7 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
       asm volatile("s_barrier" ::: "memory");  // step s+2 landed and its masks built
     }
     wait_loads_and_barrier<0>();  // loads past the end landed before the epilogue
+    if constexpr (YT == kAct) finish_half<BF16 ? kBF16 : kF16>(smem, Y, m0, t0, R, T, wave, lane);
     return;
   }
 
@@ -2035,9 +2046,17 @@ __global__ void __launch_bounds__(64 * (CWAVES_M * CWAVES_N + PWAVES))
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // stage of step s released
   }
   asm volatile("s_barrier" ::: "memory");  // the producers' last loads have landed
-  static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
-  store_out_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
-                         t0 + wn * TL::kWN, R, T, lane);
+  if constexpr (YT == kAct) {
+    static_assert(CWAVES_M == 2 && CWAVES_N == 2 && PWAVES == 4, "blocks as finish_half has them");
+    static_assert(4 * kBlockBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    slab_write(acc[0], acc[1], slab_of(smem, wave), lane);
+    slab_write(acc[2], acc[3], slab_of(smem, wave + 4), lane);
+    finish_half<BF16 ? kBF16 : kF16>(smem, Y, m0, t0, R, T, wave, lane);
+  } else {
+    static_assert(TL::kConsumers * kEpilogueBytes <= kStages * TL::kStageBytes, "epilogue LDS");
+    store_block_128x64<YT>(acc, smem + wave * kEpilogueBytes, Y, m0 + wm * TL::kWM,
+                             t0 + wn * TL::kWN, R, T, lane);
+  }
 }
 
 // ===========================================================================
@@ -2324,17 +2343,17 @@ __global__ void __launch_bounds__(256)
   // accumulator layout: lane (q, lr) of block (fm, fn) holds column lr and, in register e,
   // row 8 (e / 4) + 4 q + e % 4
   if constexpr (YT == kAct) {  // every wave is past the loop's last barrier: LDS is free
-    static_assert(4 * kEpilogueBytes <= 2 * kEStageWords * 4, "epilogue LDS");
-    uint8_t* mine = reinterpret_cast<uint8_t*>(ex_smem) + wave * kEpilogueBytes;
+    static_assert(4 * kSlabBytes <= 2 * kEStageWords * 4, "epilogue LDS");
+    uint8_t* mine = reinterpret_cast<uint8_t*>(ex_smem) + wave * kSlabBytes;
     if constexpr (kI) {
       int16v_t sums[2][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) sums[i >> 1][i & 1][e] = acc_i[i >> 1][i & 1][e];
-      finish_block<2>(sums, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
+      finish_block<DT, 2>(sums, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
     } else {
-      finish_block<2>(acc, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
+      finish_block<DT, 2>(acc, mine, Y, m0 + wm * 64, t0 + wn * 64, R, T, lane);
     }
     return;
   }
@@ -2479,9 +2498,11 @@ constexpr double kTileFixedUs = 5.0;
 template <bool BF16, bool kPat12, bool kBlocked, int YT>
 hipError_t run_smfmac(const void* values, const uint32_t* meta, int64_t R, int64_t K,
                       const void* X, int64_t T, typename OutOf<YT>::type Y, hipStream_t s) {
-  if (T % 8 != 0)  // even T: the wave-specialised tile with 4-byte X pieces
-    return launch_tile<BF16, kPat12, kBlocked, YT, 2, 256, 128, 2, 2, 4, 4, 4>(values, meta, R,
-                                                                              K, X, T, Y, s);
+  if constexpr (YT != kAct) {  // (its X has whole pieces)
+    if (T % 8 != 0)  // even T: the wave-specialised tile with 4-byte X pieces
+      return launch_tile<BF16, kPat12, kBlocked, YT, 2, 256, 128, 2, 2, 4, 4, 4>(values, meta, R,
+                                                                                K, X, T, Y, s);
+  }
   switch (pick_tile(R, K, T)) {
     case 0:
       return launch_tile<BF16, kPat12, kBlocked, YT, 1, 256, 256, 2, 4, 0, 3>(values, meta, R, K,
