@@ -138,7 +138,7 @@ def lib() -> ctypes.CDLL:
         L.nm_xent_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, size, vp]
         L.nm_orthogonalize_workspace_bytes.argtypes = [i64, i64, i32]
         L.nm_orthogonalize.argtypes = [vp, i32, i64, i64, i32, f32, vp, vp, size, vp]
-        L.nm_spmm_act_workspace_bytes.argtypes = [i64, i64, i32]
+        L.nm_spmm_act_workspace_bytes.argtypes = [i64, i64, i32, i32, i64, i32]
         L.nm_spmm_act.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, vp, vp,
                                   vp, i32, vp, size, vp]
         L.nm_spmm_act_grad_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32]
@@ -795,7 +795,7 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
         out = X.new_empty((R, T), dtype=y_dtype)
     Z = X.new_empty((R, T)) if keep else None
     L = lib()
-    ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(K, T, dt))
+    ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(R, K, n, m, T, dt))
     _launch("nm_spmm_act", X,
         values.data_ptr(), meta.data_ptr(), R, K, n, m, _layout(layout), X.data_ptr(), T, dt,
         _addr(scale), _addr(bias), code, _addr(residual), _addr(Z), out.data_ptr(),

@@ -742,9 +742,11 @@ bool below(int64_t a, int64_t b, int64_t most) { return a == 0 || b <= most / a;
 
 extern "C" {
 
-size_t nm_spmm_act_workspace_bytes(int64_t K, int64_t T, nm_dtype dt) {
-  if (!valid_dtype(dt) || K < 0 || T < 0 || !below(K, T, (int64_t)1 << 40)) return 0;
-  return nm::spmm_act_workspace_bytes(K, T, (int)dt);
+size_t nm_spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, nm_dtype dt) {
+  if (!valid_dtype(dt) || check_pattern(n, m) != NM_OK || check_shape(R, K, m) != NM_OK || T < 0 ||
+      !below(K, T, (int64_t)1 << 40) || !below(R, T, (int64_t)1 << 40) || R * T == 0)
+    return 0;
+  return nm::spmm_act_workspace_bytes(R, K, n, m, T, (int)dt);
 }
 
 nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
@@ -768,7 +770,7 @@ nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64
   if (!aligned16(values) || !aligned16(meta) || !aligned16(X) || !aligned16(Y) || !aligned16(scale) ||
       !aligned16(bias) || !aligned16(residual) || !aligned16(Z))
     return NM_ERR_ALIGN;
-  const size_t need = nm::spmm_act_workspace_bytes(K, T, (int)dt);
+  const size_t need = nm::spmm_act_workspace_bytes(R, K, n, m, T, (int)dt);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const int64_t y_bytes = R * T * elem_bytes(y_dt);
   const Range r[] = {{Y, y_bytes},

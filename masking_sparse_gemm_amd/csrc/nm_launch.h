@@ -62,8 +62,14 @@ hipError_t launch_expand_act(const void* values, const uint32_t* meta, int64_t R
                              int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
                              hipStream_t s);
 
-// The same for any T (nm_spmm_grad.hip): rows of X that are not whole pieces are copied to the workspace.
-size_t spmm_act_workspace_bytes(int64_t K, int64_t T, int dt);
+// 2:4, 1:2 and 1:4 of any type for few tokens (nm_thin.hip; K % 64 == 0); the workspace takes X turned.
+hipError_t launch_thin(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
+                       bool blocked, const void* X, int64_t T, int dt, const Product& product,
+                       void* workspace, hipStream_t s);
+
+// The same for any T (nm_spmm_grad.hip): X is copied to the workspace for the thin product and where
+// its rows are not whole pieces.
+size_t spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, int dt);
 hipError_t run_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                         bool blocked, const void* X, int64_t T, int dt, Product p, void* workspace,
                         hipStream_t s);

@@ -21,12 +21,15 @@ namespace nm {
 namespace {
 
 constexpr int kMostCells = 8192;           // words x columns of a workgroup
+constexpr int kEach = 8;                   // of them to a work-item, at most
 constexpr int kMostThreads = 1024;
+constexpr int kCounts = 8448;              // in LDS: columns of one more than the tile's words, and copies
 constexpr uint32_t kSeen = 0x80000000u;    // of a count: the word is in the prompt
 
 // A workgroup's tile: 2^log_cols columns, 2^log_cells entries, `threads` work-items.
 struct LogitsPlan {
   int log_cols, log_cells, threads;
+  int copies;        // of a workgroup's counts
   int64_t blocks_v, blocks_t;
   bool table;        // the counts go through the workspace
   LogitsPlan(int64_t V, int64_t T, int64_t count);
@@ -34,7 +37,7 @@ struct LogitsPlan {
 
 struct LogitsArgs {
   LogitsCall c;
-  int log_cols, log_cells;
+  int log_cols, log_cells, copies;
   uint32_t* counts;  // V x T, or null
 };
 
@@ -54,18 +57,52 @@ __global__ void __launch_bounds__(256) clear_counts_kernel(uint32_t* __restrict_
     counts[i] = 0u;
 }
 
-// Workgroups (x) share a column's (y, and on) tokens.
-__global__ void __launch_bounds__(256) count_kernel(LogitsCall c, uint32_t* __restrict__ counts) {
+// Workgroups (x) share a column's (y, and on) tokens, kRun at a time.  A text's frequent words would
+// queue at one address of the table, so a workgroup first counts in LDS, at a place given by the word's
+// low bits, which the first word to come holds; only words that find theirs held go to the table at
+// once.
+constexpr int kRun = 8192, kPlaces = 4096;
+
+__global__ void __launch_bounds__(1024) count_kernel(LogitsCall c, uint32_t* __restrict__ counts) {
+  __shared__ int held[kPlaces];
+  __shared__ uint32_t sums[kPlaces];
+  const auto put = [&](int64_t v, int64_t t, uint32_t sum) {
+    uint32_t* cell = counts + v * c.T + t;
+    if (sum & kSeen) atomicOr(cell, kSeen);
+    if (sum & ~kSeen) atomicAdd(cell, sum & ~kSeen);
+  };
   for (int64_t t = blockIdx.y; t < c.T; t += gridDim.y) {
     int64_t begin, own, end;
     tokens_of(c, t, begin, own, end);
-    for (int64_t i = begin + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end;
-         i += (int64_t)gridDim.x * 256) {
-      const int64_t v = c.tokens[i];
-      if (v < 0 || v >= c.V) continue;
-      if (i < own) atomicOr(counts + v * c.T + t, kSeen);
-      else atomicAdd(counts + v * c.T + t, 1u);
+    for (int i = threadIdx.x; i < kPlaces; i += 1024) {
+      held[i] = -1;
+      sums[i] = 0u;
     }
+    __syncthreads();
+    for (int64_t i0 = begin + (int64_t)blockIdx.x * kRun; i0 < end; i0 += (int64_t)gridDim.x * kRun) {
+      int64_t v[kRun / 1024];
+#pragma unroll
+      for (int j = 0; j < kRun / 1024; ++j)
+        v[j] = c.tokens[min(i0 + j * 1024 + (int)threadIdx.x, end - 1)];
+#pragma unroll
+      for (int j = 0; j < kRun / 1024; ++j) {
+        const int64_t i = i0 + j * 1024 + threadIdx.x;
+        if (i >= end || v[j] < 0 || v[j] >= c.V) continue;
+        const int place = (int)v[j] & (kPlaces - 1), word = (int)v[j];
+        int who = held[place];
+        if (who == -1) {
+          who = atomicCAS(held + place, -1, word);
+          if (who == -1) who = word;
+        }
+        if (who != word) put(word, t, i < own ? kSeen : 1u);
+        else if (i < own) atomicOr(sums + place, kSeen);
+        else atomicAdd(sums + place, 1u);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kPlaces; i += 1024)
+      if (held[i] >= 0) put(held[i], t, sums[i]);
+    __syncthreads();
   }
 }
 
@@ -78,17 +115,28 @@ __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
 
 // HISTORY: 0 none, 1 counted here in LDS, 2 from the table.
 template <int DT, int HISTORY>
-__global__ void __launch_bounds__(kMostThreads) adjust_kernel(LogitsArgs a) {
-  __shared__ uint32_t cells[HISTORY == 1 ? kMostCells : 1];
+__global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
+  __shared__ uint32_t cells[HISTORY == 1 ? kCounts : 1];
   __shared__ uint32_t bits[kMostCells / 32];
+  __shared__ int64_t ranges[HISTORY == 1 ? 32 : 1][3];
   const LogitsCall& c = a.c;
   const int tid = threadIdx.x, threads = blockDim.x;
   const int cols = 1 << a.log_cols, all = 1 << a.log_cells, words = all >> a.log_cols;
   const int64_t t0 = (int64_t)blockIdx.y * cols, v0 = (int64_t)blockIdx.x * words;
   const int64_t t = t0 + (tid & (cols - 1));  // this work-item's column
   const bool live = t < c.T;
+  // the logits are under way while the tokens are counted
+  float x[kEach];
+  const auto place = [&](int k) {  // of entry k of this work-item, held within the matrix
+    const int64_t v = v0 + ((tid + k * threads) >> a.log_cols);
+    return min(v, c.V - 1) * c.T + min(t, c.T - 1);
+  };
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (tid + k * threads < all) x[k] = logit_at<DT>(c.logits, place(k));
   if constexpr (HISTORY == 1) {
-    for (int i = tid; i < all; i += threads) cells[i] = 0u;
+    for (int i = tid; i < a.copies * cols * (words + 1); i += threads) cells[i] = 0u;
+    if (tid < cols && live) tokens_of(c, t, ranges[tid][0], ranges[tid][1], ranges[tid][2]);
   }
   if (c.allowed) {  // words is a multiple of 32: whole words of the mask
     const int64_t row = (c.V + 31) / 32;
@@ -99,22 +147,24 @@ __global__ void __launch_bounds__(kMostThreads) adjust_kernel(LogitsArgs a) {
   }
   __syncthreads();
   if constexpr (HISTORY == 1) {
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 4;
     const int lane = tid & 63, wave = tid >> 6, waves = threads >> 6;
+    // a text's frequent words would have a wave's lanes wait for one another: several copies of the
+    // counts, and a column's words on banks of their own
+    uint32_t* copy = cells + (lane & (a.copies - 1)) * cols * (words + 1);
     // a wave a column, or several where columns are few
     const int shares = waves > cols ? waves >> a.log_cols : 1, share = waves > cols ? wave >> a.log_cols : 0;
     for (int k = waves > cols ? wave & (cols - 1) : wave; k < cols && t0 + k < c.T; k += waves) {
-      int64_t begin, own, end;
-      tokens_of(c, t0 + k, begin, own, end);
+      const int64_t begin = ranges[k][0], own = ranges[k][1], end = ranges[k][2];
       for (int64_t i = begin + share * 64 + lane; i < end; i += kBatch * 64 * shares) {
-        int64_t v[kBatch];
+        int64_t v[kBatch];  // (loads without conditions, or each would be waited for)
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          v[j] = i + 64 * shares * j < end ? c.tokens[i + 64 * shares * j] - v0 : -1;
+        for (int j = 0; j < kBatch; ++j) v[j] = c.tokens[min(i + 64 * shares * j, end - 1)];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          if (v[j] < 0 || v[j] >= words || v[j] >= c.V - v0) continue;
-          uint32_t* cell = cells + ((int)v[j] << a.log_cols) + k;
+          v[j] -= v0;
+          if (i + 64 * shares * j >= end || v[j] < 0 || v[j] >= words || v[j] >= c.V - v0) continue;
+          uint32_t* cell = copy + k * (words + 1) + (int)v[j];
           if (i + 64 * shares * j < own) atomicOr(cell, kSeen);
           else atomicAdd(cell, 1u);
         }
@@ -126,50 +176,52 @@ __global__ void __launch_bounds__(kMostThreads) adjust_kernel(LogitsArgs a) {
   const float repetition = HISTORY && c.repetition ? c.repetition[t] : 1.f;
   const float presence = HISTORY && c.presence ? c.presence[t] : 0.f;
   const float frequency = HISTORY && c.frequency ? c.frequency[t] : 0.f;
-  const bool penalised = c.repetition != nullptr;
-  constexpr int kBatch = 8;  // loads in flight
-#pragma unroll 1
-  for (int i0 = tid; i0 < all; i0 += kBatch * threads) {
-    float x[kBatch], b[kBatch];
-    uint32_t n[kBatch];
+  float b[kEach];
+  uint32_t n[kEach];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * threads;
-      const int64_t v = v0 + (i >> a.log_cols);
-      const bool in = i < all && v < c.V;
-      x[k] = in ? logit_at<DT>(c.logits, v * c.T + t) : 0.f;
-      b[k] = in && c.bias ? c.bias[c.bias_each ? v * c.T + t : v] : 0.f;
-      n[k] = 0;
-      if constexpr (HISTORY == 1) n[k] = in ? cells[i] : 0u;
-      if constexpr (HISTORY == 2) n[k] = in ? a.counts[v * c.T + t] : 0u;
-    }
+  for (int k = 0; k < kEach; ++k) {
+    if (tid + k * threads >= all) continue;
+    const int64_t v = v0 + ((tid + k * threads) >> a.log_cols);
+    if (c.bias) b[k] = c.bias[c.bias_each ? place(k) : min(v, c.V - 1)];
+    if constexpr (HISTORY == 2) n[k] = a.counts[place(k)];
+  }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * threads, w = i >> a.log_cols;
-      const int64_t v = v0 + w;
-      if (i >= all || v >= c.V) continue;
-      float y = x[k];
-      if (HISTORY && n[k] != 0) {
-        if (penalised) y = y > 0.f ? y / repetition : y * repetition;
-        const uint32_t own = n[k] & ~kSeen;
-        if (own != 0) y = (y - presence) - frequency * (float)own;
+  for (int k = 0; k < kEach; ++k) {
+    const int i = tid + k * threads, w = i >> a.log_cols;
+    const int64_t v = v0 + w;
+    if (i >= all || v >= c.V) continue;
+    float y = x[k];
+    uint32_t count = 0;
+    if constexpr (HISTORY == 2) count = n[k];
+    if constexpr (HISTORY == 1) {
+      uint32_t seen = 0;
+      for (int q = 0; q < a.copies; ++q) {
+        const uint32_t one = cells[(q * cols + (tid & (cols - 1))) * (words + 1) + w];
+        seen |= one & kSeen;
+        count += one & ~kSeen;
       }
-      if (c.bias) y += b[k];
-      if (c.allowed && !((bits[((w >> 5) << a.log_cols) + (tid & (cols - 1))] >> (w & 31)) & 1u))
-        y = -INFINITY;
-      store_from_f32<DT>(c.out, v * c.T + t, y);
+      count |= seen;
     }
+    if (HISTORY && count != 0) {
+      if (c.repetition) y = y > 0.f ? y / repetition : y * repetition;
+      const uint32_t own = count & ~kSeen;
+      if (own != 0) y = (y - presence) - frequency * (float)own;
+    }
+    if (c.bias) y += b[k];
+    if (c.allowed && !((bits[((w >> 5) << a.log_cols) + (tid & (cols - 1))] >> (w & 31)) & 1u))
+      y = -INFINITY;
+    store_from_f32<DT>(c.out, v * c.T + t, y);
   }
 }
 
 int64_t table_bytes(int64_t V, int64_t T) { return V * T * 4; }
 
-// Columns: 16, whose 64 bytes (fp32) of a row are one request, or what there are, to a power of two.
-// Entries: as many as fit, since every workgroup reads its columns' tokens, but few enough that all
-// 256 units have a workgroup.
+// Columns: 32, whose 128 bytes (fp32) of a row are a whole line, or what there are, to a power of two.
+// Entries: as many as fit, since every workgroup reads its columns' tokens (50257 x 64: 8192 a
+// workgroup 18 us, 4096 25, 1024 80), but few enough that all 256 units have a workgroup.
 LogitsPlan::LogitsPlan(int64_t V, int64_t T, int64_t count) {
   log_cols = 0;
-  while (log_cols < 4 && ((int64_t)1 << log_cols) < T) ++log_cols;
+  while (log_cols < 5 && ((int64_t)1 << log_cols) < T) ++log_cols;
   const int64_t cols = (int64_t)1 << log_cols;
   blocks_t = (T + cols - 1) / cols;
   const int least = std::max(8, 5 + log_cols);  // whole words of the mask
@@ -179,11 +231,18 @@ LogitsPlan::LogitsPlan(int64_t V, int64_t T, int64_t count) {
   }
   const int64_t words = ((int64_t)1 << log_cells) / cols;
   blocks_v = (V + words - 1) / words;
+  copies = std::min(16, kMostCells >> log_cells);
   const int64_t each = count / std::max<int64_t>(1, T);  // tokens of a column
-  threads = log_cells >= 13 || each > 2048 ? kMostThreads : 256;
-  // in LDS each of blocks_v workgroups reads a column's tokens; through the table they are read once,
-  // and the table is written and read, with two more launches
-  table = (double)blocks_v * (double)count * 8 > 3.0 * (double)table_bytes(V, T) + 64e6;
+  if (each <= 512) copies = 1;
+  threads = each > 4096 ? kMostThreads : std::max(256, (1 << log_cells) / kEach);
+  // In LDS each of blocks_v workgroups reads a column's tokens, as fast as the caches give them to the
+  // units that work; through the table they are read once, and the table is written and read, with two
+  // more launches.  `count` is the room for tokens, of which a part is in use.  Measured, us in LDS /
+  // through the table: 32000 words, one column of 2000 tokens 5.2 / 9.9, of 100,000 19.7 / 12.5; 50257 x
+  // 64, 48,000 tokens 18 / 22, 256,000 62 / 28, 1,000,000 205 / 40; 128000 x 256 with few 63 / 91.
+  const double share = std::min(1.0, (double)(blocks_v * blocks_t) / 256), cells = (double)V * (double)T;
+  const double in_lds = 3 + 0.45e-6 * cells + (double)blocks_v * (double)count * 8 / (24e6 * share);
+  table = in_lds > 8 + 1.1e-6 * cells;
 }
 
 template <int DT>
@@ -204,7 +263,7 @@ size_t logits_workspace_bytes(int64_t V, int64_t T, int64_t count) {
 hipError_t launch_adjust_logits(const LogitsCall& c, void* workspace, hipStream_t s) {
   const bool any = c.count > 0 && (c.repetition || c.presence || c.frequency);
   const LogitsPlan p(c.V, c.T, c.count);
-  LogitsArgs a{c, p.log_cols, p.log_cells, nullptr};
+  LogitsArgs a{c, p.log_cols, p.log_cells, p.copies, nullptr};
   int history = any ? 1 : 0;
   if (any && p.table) {
     history = 2;
@@ -213,8 +272,8 @@ hipError_t launch_adjust_logits(const LogitsCall& c, void* workspace, hipStream_
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t cols = std::min<int64_t>(c.T, 4096);
-    const int64_t each = std::min((c.count / c.T + 1023) / 1024, 4096 / cols);
-    count_kernel<<<dim3((unsigned)std::max<int64_t>(1, each), (unsigned)cols), 256, 0, s>>>(c, a.counts);
+    const int64_t each = std::min((c.count / c.T + kRun - 1) / kRun, 2048 / cols);
+    count_kernel<<<dim3((unsigned)std::max<int64_t>(1, each), (unsigned)cols), 1024, 0, s>>>(c, a.counts);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (c.dt == kF32) return launch_adjust<kF32>(a, p, history, s);

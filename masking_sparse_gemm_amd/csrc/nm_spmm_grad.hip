@@ -325,7 +325,9 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
 
 }  // namespace
 
-size_t spmm_act_workspace_bytes(int64_t K, int64_t T, int dt) {
+size_t spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, int dt) {
+  if (thin_preferred(R, K, n, m, T, elem_of(dt)))
+    return (size_t)(ThinPlan(R, K, T, dt == kF32).Tp * K * (dt == kF32 ? 4 : 2));
   const int64_t ldx = whole_row(T, dt);
   return ldx == T ? 0 : (size_t)whole256(K * ldx * elem_of(dt));
 }
@@ -333,6 +335,8 @@ size_t spmm_act_workspace_bytes(int64_t K, int64_t T, int dt) {
 hipError_t run_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                         bool blocked, const void* X, int64_t T, int dt, Product p, void* workspace,
                         hipStream_t s) {
+  if (thin_preferred(R, K, n, m, T, elem_of(dt)))
+    return launch_thin(values, meta, R, K, n, m, blocked, X, T, dt, p, workspace, s);
   p.ldx = whole_row(T, dt);
   if (p.ldx != T && K > 0) {
     const hipError_t e = widen(X, K, T, workspace, K, p.ldx, elem_of(dt), s);

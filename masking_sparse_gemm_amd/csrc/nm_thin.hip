@@ -1,0 +1,404 @@
+// nm_thin.hip -- nm_spmm_act for few tokens and small matrices (gfx950), 2:4, 1:2 and 1:4, every type.
+//
+// The tiled kernels of nm_spmm.hip give a workgroup 128 rows or more and walk K in one barrier a
+// step, so with few rows and columns most units have nothing to do and the rest wait.  Here a
+// workgroup has 16 RG rows and 16 NT columns, and its eight waves take the steps of 64 K in turn, each
+// with the next step's loads in flight, no barrier and no LDS until their sums are joined there in wave
+// order.  Both operands come from memory as the structured-sparse instruction (v_smfmac_f32_16x16x64)
+// wants them: the compressed rows as they lie, and X from a transposed copy in which a lane's K are
+// contiguous, made by a first small launch.  fp8 and int8 become bf16 exactly on the way (int8 sums are
+// exact: fp32 holds 1024 K of products of up to 2^14, then they move to int32).  1:2 places become
+// 2:4's by their bits, a 1:4 group a pair with a zero.  fp32, which has no sparse instruction, is
+// expanded in registers for v_mfma_f32_16x16x4_f32.
+//
+// Bound by the first loads' latency on small matrices and by the reads of W on large ones.
+#include <algorithm>
+#include <type_traits>
+
+#include "nm_act.h"
+#include "nm_launch.h"
+#include "nm_tiles.h"
+
+namespace nm {
+namespace {
+
+constexpr int kThinWaves = 8;
+enum { kP24, kP12, kP14 };  // patterns
+
+// ---- X, transposed -------------------------------------------------------------------
+
+// v in 16 bits: as it is (16-bit types), exactly as bf16 (8-bit types).
+template <int DT>
+__device__ __forceinline__ uint32_t to_half(uint32_t raw) {
+  if constexpr (DT == kI8) return f32_to_bf16((float)(int8_t)raw);
+  else if constexpr (DT == kFP8) return f32_to_bf16(e4m3_to_f32(raw));
+  else return raw;
+}
+
+template <int DT>
+struct ThinElem {
+  typedef std::conditional_t<DT == kF32, float, std::conditional_t<DT == kI8 || DT == kFP8, uint8_t,
+                                                                   uint16_t>> type;
+  typedef std::conditional_t<DT == kF32, uint32_t, uint16_t> turned;  // of X's copy
+};
+
+struct TurnArgs {
+  const void* x;      // K x T
+  int64_t K, T, Tp;   // Tp: columns with the zeros after them
+  void* xt;           // Tp / 16 x K / 64 blocks of 16 columns x 64 K
+};
+
+// 64 x 64 of X a workgroup, through LDS.  A block of X's copy holds 16 columns and 64 K as the product's
+// lanes read it, each load of a wave 1 KB in one run: piece i of lane 16 q + l, 16 bytes at
+// 64 i + 16 q + l, has of column l the K 32 i + 8 q .. + 7, in fp32 16 q + 4 i .. + 3.
+template <int DT>
+__global__ void __launch_bounds__(256) turn_kernel(TurnArgs p) {
+  typedef typename ThinElem<DT>::type E;
+  typedef typename ThinElem<DT>::turned O;
+  constexpr int kPer = 16 / sizeof(O), kPieces = 64 / kPer;  // of 16 bytes, a column
+  __shared__ O tile[64][DT == kF32 ? 65 : 66];  // [column][k]
+  const E* x = static_cast<const E*>(p.x);
+  const int64_t k0 = (int64_t)blockIdx.x * 64, t0 = (int64_t)blockIdx.y * 64;
+  const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+  E in[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    in[i] = t0 + c < p.T ? x[(k0 + r + 4 * i) * p.T + t0 + c] : E(0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (DT == kF32) tile[c][r + 4 * i] = __float_as_uint(in[i]);
+    else tile[c][r + 4 * i] = (uint16_t)to_half<DT>(in[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 64 * kPieces / 256; ++i) {
+    const int at = i * 256 + threadIdx.x, b = at / (16 * kPieces), in_b = at % (16 * kPieces);
+    const int piece = in_b >> 6, q = (in_b >> 4) & 3, col = 16 * b + (in_b & 15);
+    const int k = DT == kF32 ? 16 * q + 4 * piece : 32 * piece + 8 * q;
+    if (t0 + col >= p.Tp) continue;
+    u32x4_t w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (DT == kF32) w[e] = tile[col][k + e];
+      else w[e] = tile[col][k + 2 * e] | (uint32_t)tile[col][k + 2 * e + 1] << 16;
+    }
+    const int64_t block = (t0 / 16 + b) * (p.K / 64) + blockIdx.x;
+    static_cast<u32x4_t*>(p.xt)[block * (16 * kPieces) + in_b] = w;
+  }
+}
+
+// ---- the product ---------------------------------------------------------------------------------
+
+struct ThinArgs {
+  const uint8_t* values;
+  const uint8_t* meta;
+  const void* xt;
+  int64_t R, K, T, Tp;
+  Epilogue ep;
+};
+
+// Sixteen K of a row as they lie: 8 values (1:4: 4) and their places.
+template <int DT, int PAT>
+struct ThinRaw {
+  typedef typename ThinElem<DT>::type E;
+  static constexpr int kValues = PAT == kP14 ? 4 : 8;
+  static constexpr int kBytes = kValues * (int)sizeof(E);
+  uint32_t w[kBytes / 4];
+  uint32_t places;
+
+  // values: the row's first of the sixteen K; places: their first byte
+  __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const u32x4_t x = reinterpret_cast<const u32x4_t*>(v)[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[4 * i + e] = x[e];
+      }
+    } else if constexpr (kBytes == 8) {
+      const u32x2_t x = *reinterpret_cast<const u32x2_t*>(v);
+      w[0] = x[0];
+      w[1] = x[1];
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(v);
+    }
+    places = PAT == kP24 ? *reinterpret_cast<const uint16_t*>(m) : *m;
+  }
+
+  __device__ __forceinline__ uint32_t raw(int i) const {
+    if constexpr (sizeof(E) == 4) return w[i];
+    else if constexpr (sizeof(E) == 2) return (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    else return (w[i / 4] >> (8 * (i & 3))) & 0xFFu;
+  }
+
+  // The A operand of the sparse instruction and its index word.
+  __device__ __forceinline__ u32x4_t operand(uint32_t& ix) const {
+    if constexpr (PAT == kP24) {
+      ix = places;
+    } else if constexpr (PAT == kP12) {  // bit i -> bit 2 i; the second of a pair is in the upper half
+      uint32_t x = places;
+      x = (x | (x << 4)) & 0x0F0Fu;
+      x = (x | (x << 2)) & 0x3333u;
+      ix = ((x | (x << 1)) & 0x5555u) | 0x8888u;
+    } else {  // (value, 0) at places 0 and 1, or (0, value) at 0 and the value's
+      ix = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t p = (places >> (2 * g)) & 3u;
+        ix |= (p == 0 ? 4u : p << 2) << (4 * g);
+      }
+    }
+    if constexpr (sizeof(E) == 2 && PAT != kP14) return u32x4_t{w[0], w[1], w[2], w[3]};
+    u32x4_t a;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if constexpr (PAT == kP14)
+        a[g] = to_half<DT>(raw(g)) << (((places >> (2 * g)) & 3u) == 0 ? 0 : 16);
+      else
+        a[g] = to_half<DT>(raw(2 * g)) | to_half<DT>(raw(2 * g + 1)) << 16;
+    }
+    return a;
+  }
+
+  // fp32: the sixteen numbers of the dense row.
+  __device__ __forceinline__ void expand(float (&d)[16]) const {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (PAT == kP24) {
+          const uint32_t p = places >> (4 * g);
+          const float lo = (p & 3u) == (uint32_t)k ? __uint_as_float(w[2 * g]) : 0.f;
+          d[4 * g + k] = ((p >> 2) & 3u) == (uint32_t)k ? __uint_as_float(w[2 * g + 1]) : lo;
+        } else if constexpr (PAT == kP12) {
+          const int i = 2 * g + k / 2;
+          d[4 * g + k] = ((places >> i) & 1u) == (uint32_t)(k & 1) ? __uint_as_float(w[i]) : 0.f;
+        } else {
+          d[4 * g + k] = ((places >> (2 * g)) & 3u) == (uint32_t)k ? __uint_as_float(w[g]) : 0.f;
+        }
+      }
+  }
+};
+
+template <bool F16>
+__device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t& b0, const u32x4_t& b1,
+                                                const float4_t& c, uint32_t ix) {
+  typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
+  const u32x8_t b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+  if constexpr (F16)
+    return __builtin_amdgcn_smfmac_f32_16x16x64_f16(__builtin_bit_cast(f16x8_t, a),
+                                                    __builtin_bit_cast(f16x16_t, b), c, (int)ix, 0, 0);
+  else
+    return __builtin_amdgcn_smfmac_f32_16x16x64_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                     __builtin_bit_cast(bf16x16_t, b), c, (int)ix, 0,
+                                                     0);
+}
+
+template <int DT, int PAT, bool BLOCKED, int RG, int NT>
+__global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
+  typedef typename ThinElem<DT>::type E;
+  typedef ThinRaw<DT, PAT> Raw;
+  constexpr bool kF = DT == kF32;
+  constexpr int kRows = 16 * RG, kCols = 16 * NT;
+  constexpr int kRowValues = PAT == kP14 ? 16 : 32, kRowMeta = PAT == kP24 ? 8 : 4;  // a row and step
+  constexpr int kPitch = kCols + 4;  // of the sums in LDS
+  __shared__ __attribute__((aligned(16))) float sums[kThinWaves][kRows * kPitch];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int steps = (int)(p.K / 64);
+  const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kCols;
+  const int64_t groups = (p.R + 15) / 16;
+
+  // this lane's rows (past the matrix: its last group or row again) and columns of X
+  const uint8_t *v[RG], *m[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    if constexpr (BLOCKED) {
+      const int64_t b = min(r0 / 16 + g, groups - 1);
+      v[g] = p.values + (b * steps * 16 + l16) * kRowValues * (int64_t)sizeof(E) + q * Raw::kBytes;
+      m[g] = p.meta + (b * steps * 16 + l16) * kRowMeta + q * (kRowMeta / 4);
+    } else {
+      const int64_t row = min(r0 + 16 * g + l16, p.R - 1);
+      v[g] = p.values + row * steps * kRowValues * (int64_t)sizeof(E) + q * Raw::kBytes;
+      m[g] = p.meta + row * steps * kRowMeta + q * (kRowMeta / 4);
+    }
+  }
+  constexpr int kVStep = (BLOCKED ? 16 : 1) * kRowValues * (int)sizeof(E);
+  constexpr int kMStep = (BLOCKED ? 16 : 1) * kRowMeta;
+  constexpr int kPieces = kF ? 4 : 2;  // of X's copy to a lane, step and fragment
+  const u32x4_t* x = static_cast<const u32x4_t*>(p.xt) + (t0 / 16 * steps) * (64 * kPieces) + lane;
+
+  struct Step {
+    Raw a[RG];
+    u32x4_t b[NT][kPieces];
+  };
+  const auto load = [&](Step& f, int s) {
+#pragma unroll
+    for (int g = 0; g < RG; ++g) f.a[g].load(v[g] + (int64_t)s * kVStep, m[g] + (int64_t)s * kMStep);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const u32x4_t* at = x + ((int64_t)t * steps + s) * (64 * kPieces);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) f.b[t][i] = at[64 * i];
+    }
+  };
+  float4_t acc[RG][NT];
+  int4 whole[DT == kI8 ? RG : 1][DT == kI8 ? NT : 1];  // int8: exact totals
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      acc[g][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+      if constexpr (DT == kI8) whole[g][t] = int4{0, 0, 0, 0};
+    }
+  Step next;
+  if (wave < steps) load(next, wave);
+  int count = 0;
+  for (int s = wave; s < steps; s += kThinWaves) {
+    const Step cur = next;
+    if (s + kThinWaves < steps) load(next, s + kThinWaves);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      if constexpr (kF) {
+        float d[16];
+        cur.a[g].expand(d);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)  // K 16 q + k in lane quarter q
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k], __uint_as_float(cur.b[t][k / 4][k % 4]),
+                                                             acc[g][t], 0, 0, 0);
+      } else {
+        uint32_t ix;
+        const u32x4_t a = cur.a[g].operand(ix);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[g][t] = thin_smfmac<DT == kF16>(a, cur.b[t][0], cur.b[t][1], acc[g][t], ix);
+      }
+    }
+    if constexpr (DT == kI8) {
+      if ((++count & 15) == 0 || s + kThinWaves >= steps) {
+#pragma unroll
+        for (int g = 0; g < RG; ++g)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            whole[g][t].x += (int)acc[g][t][0];
+            whole[g][t].y += (int)acc[g][t][1];
+            whole[g][t].z += (int)acc[g][t][2];
+            whole[g][t].w += (int)acc[g][t][3];
+            acc[g][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+          }
+      }
+    }
+  }
+
+  // lane (l16, q) holds rows 4 q .. + 3 of column l16 of each fragment
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* d = sums[wave] + (16 * g + 4 * q) * kPitch + 16 * t + l16;
+      if constexpr (DT == kI8) {
+        d[0] = __int_as_float(whole[g][t].x);
+        d[kPitch] = __int_as_float(whole[g][t].y);
+        d[2 * kPitch] = __int_as_float(whole[g][t].z);
+        d[3 * kPitch] = __int_as_float(whole[g][t].w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i * kPitch] = acc[g][t][i];
+      }
+    }
+  const int row = threadIdx.x / (2 * NT), col = threadIdx.x % (2 * NT) * 8;
+  const int64_t r = r0 + row, t = t0 + col;
+  const bool mine = row < kRows && r < p.R && t < p.T;
+  const int64_t i = r * p.T + t, left = p.T - t;
+  RawEight residual{};
+  float scale = 1.f, bias = 0.f;
+  if (mine) {
+    if (p.ep.residual) residual = load_eight(p.ep.residual, y_type<DT>(p.ep), i, left);
+    if (p.ep.scale) scale = p.ep.scale[r];
+    if (p.ep.bias) bias = p.ep.bias[r];
+  }
+  __syncthreads();
+  if (!mine) return;
+  float y[8];
+  if constexpr (DT == kI8) {
+    int n[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kThinWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] += __float_as_int(sums[w][row * kPitch + col + e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (float)n[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThinWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += sums[w][row * kPitch + col + e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(y[e], scale, bias);
+  if constexpr (DT == kF32 || DT == kBF16 || DT == kF16)
+    if (p.ep.z) store_eight(p.ep.z, DT, i, left, y);
+  act_values(p.ep.act, y);
+  if (p.ep.residual) {
+    float add[8];
+    to_floats(residual, y_type<DT>(p.ep), add);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] += add[e];
+  }
+  store_eight(p.ep.y, y_type<DT>(p.ep), i, left, y);
+}
+
+template <int DT, int PAT, bool BLOCKED>
+hipError_t launch_cols(const ThinArgs& p, const ThinPlan& plan, hipStream_t s) {
+  const auto go = [&](auto rg, auto nt) {
+    constexpr int RG = decltype(rg)::value, NT = decltype(nt)::value;
+    const dim3 grid((unsigned)((p.R + 16 * RG - 1) / (16 * RG)), (unsigned)(plan.Tp / (16 * NT)));
+    thin_kernel<DT, PAT, BLOCKED, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
+    return hipGetLastError();
+  };
+  typedef std::integral_constant<int, 1> One;
+  typedef std::integral_constant<int, 2> Two;
+  if (plan.nt == 1) return go(One{}, One{});
+  if (plan.nt == 2 || DT == kF32) return go(Two{}, Two{});
+  return go(Two{}, std::integral_constant<int, 4>{});
+}
+
+template <int DT>
+hipError_t launch_thin_as(const ThinArgs& p, const ThinPlan& plan, int pat, bool blocked, const void* X,
+                          void* xt, hipStream_t s) {
+  const TurnArgs turn{X, p.K, p.T, p.Tp, xt};
+  turn_kernel<DT><<<dim3((unsigned)(p.K / 64), (unsigned)((p.Tp + 63) / 64)), 256, 0, s>>>(turn);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (blocked) {
+    if (pat == kP24) return launch_cols<DT, kP24, true>(p, plan, s);
+    if (pat == kP12) return launch_cols<DT, kP12, true>(p, plan, s);
+    return launch_cols<DT, kP14, true>(p, plan, s);
+  }
+  if (pat == kP24) return launch_cols<DT, kP24, false>(p, plan, s);
+  if (pat == kP12) return launch_cols<DT, kP12, false>(p, plan, s);
+  return launch_cols<DT, kP14, false>(p, plan, s);
+}
+
+}  // namespace
+
+hipError_t launch_thin(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
+                       bool blocked, const void* X, int64_t T, int dt, const Product& product,
+                       void* workspace, hipStream_t s) {
+  const ThinPlan plan(R, K, T, dt == kF32);
+  void* xt = workspace;
+  const ThinArgs p{static_cast<const uint8_t*>(values), reinterpret_cast<const uint8_t*>(meta), xt, R,
+                   K, T, plan.Tp, epilogue_of(product)};
+  const int pat = m == 2 ? kP12 : n == 2 ? kP24 : kP14;
+  if (dt == kBF16) return launch_thin_as<kBF16>(p, plan, pat, blocked, X, xt, s);
+  if (dt == kF16) return launch_thin_as<kF16>(p, plan, pat, blocked, X, xt, s);
+  if (dt == kF32) return launch_thin_as<kF32>(p, plan, pat, blocked, X, xt, s);
+  if (dt == kI8) return launch_thin_as<kI8>(p, plan, pat, blocked, X, xt, s);
+  return launch_thin_as<kFP8>(p, plan, pat, blocked, X, xt, s);
+}
+
+}  // namespace nm

@@ -98,6 +98,53 @@ struct XentGradCut {
   }
 };
 
+// ---- compressed products of few tokens ------------------------------------------------------------
+
+// The thin product's workgroup: 16 rg rows, 16 nt columns, a step of 64 K to each of eight waves at a
+// time; Tp: padded columns.  Estimated time (us): two launches and the first loads, then rounds of
+// workgroups over 256 units times eight steps at `step`, which a unit's loads set.  Measured for 64
+// steps: one round of 16 x 16 8.3, 32 x 32 10.3, 32 x 64 13.0; 16 rounds of 32 x 64 145; in fp32, whose
+// expanded products set it, 13.2 and 29.
+struct ThinPlan {
+  int rg = 1, nt = 1;
+  int64_t Tp = 0;
+  double us = 1e30;
+  ThinPlan(int64_t R, int64_t K, int64_t T, bool f32) {
+    constexpr int kShapes[3][2] = {{1, 1}, {2, 2}, {2, 4}};
+    constexpr double kStep[3] = {0.41, 0.65, 1.0}, kStep32[2] = {1.0, 3.0};
+    for (int i = 0; i < (f32 ? 2 : 3); ++i) {
+      const int64_t rows = 16 * kShapes[i][0], cols = 16 * kShapes[i][1], tp = (T + cols - 1) / cols;
+      const int64_t groups = (R + rows - 1) / rows * tp, eights = (K / 64 + 7) / 8;
+      const double t = 5 + (double)((groups + 255) / 256) * (double)eights * (f32 ? kStep32[i] : kStep[i]);
+      if (t < us) {
+        us = t;
+        rg = kShapes[i][0];
+        nt = kShapes[i][1];
+        Tp = tp * cols;
+      }
+    }
+  }
+};
+
+// Estimated time of the tiled kernels on the same product: a tile's steps alone where there are few
+// tiles, the rate where there are many.  Measured alone, us a step of 64 K: 2:4 and 1:2 in 16 bits
+// 0.49, in 8 bits 0.22, expanded 16 and 8 bits 1.45, fp32 5.25.
+inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
+  const double S = (double)K / 64, work = 2.0 * (double)R * (double)K * (double)T;
+  const bool sparse = (n == 2 && m == 4) || (n == 1 && m == 2);
+  if (elem == 4) return std::max(5.3 + 5.25 * S, 5 + work / 0.115e9);
+  if (!sparse || (elem == 1 && K % 128 != 0)) return std::max(7 + 1.45 * S, 5 + work / 0.54e9);
+  if (elem == 1) return std::max(9.7 + 0.22 * S, 6 + work / 3.0e9);
+  return std::max(7.2 + 0.49 * S, 5 + work / 1.6e9);
+}
+
+// Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).
+inline bool thin_preferred(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
+  const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4));
+  if (!pattern || K == 0 || K % 64 != 0 || T > 4096) return false;
+  return ThinPlan(R, K, T, elem == 4).us < tiled_us(R, K, n, m, T, elem);
+}
+
 // ---- gradient of the compressed product ---------------------------------------------------------
 
 // Both products of nm_spmm_act_grad in one launch: a tile size for both, and the splits of their sums

@@ -89,12 +89,30 @@ def test_row_layout_of_any_width(K, T):
     run(50, K, T, 2, 4, "fp16", "rows", "gelu_tanh", True, False, True, "fp32")
 
 
+# sizes that the tiled kernels take (test_more_tiles.py holds the rule to it)
+MANY = [(2000, 128, 2056), (2000, 128, 2061)]
+
+
 @pytest.mark.parametrize("tile", ["0", "1", "2"])
-@pytest.mark.parametrize("T", [256, 261])
-def test_every_tile(tile, T, monkeypatch):
+@pytest.mark.parametrize("R,K,T", MANY)
+def test_every_tile(tile, R, K, T, monkeypatch):
     monkeypatch.setenv("NM_SPMM_TILE", tile)
-    run(500, 512, T, 2, 4, "bf16", "blocked", "silu", True, True, True, "bf16")
-    run(500, 512, T, 1, 2, "fp16", "blocked", "none", False, True, False, "fp32")
+    run(R, K, T, 2, 4, "bf16", "blocked", "silu", True, True, True, "bf16")
+    run(R, K, T, 1, 2, "fp16", "rows", "none", False, True, False, "fp32")
+
+
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (4, 8), (1, 4)])
+@pytest.mark.parametrize("layout", ["rows", "blocked"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32", "int8", "fp8"])
+@pytest.mark.parametrize("R,K,T", MANY)
+def test_many_tokens(n, m, layout, dtype, R, K, T):
+    run(R, K, T, n, m, dtype, layout, "gelu", True, True, dtype not in EIGHT,
+        "bf16" if dtype in EIGHT else dtype)
+
+
+@pytest.mark.parametrize("dtype", ["int8", "fp8"])
+def test_many_tokens_of_bytes_in_half_steps(dtype):
+    run(2000, 192, 2061, 2, 4, dtype, "blocked", "relu2", True, False, False, "fp32")
 
 
 @pytest.mark.parametrize("bias,residual,keep", [(b, r, k) for b in (0, 1) for r in (0, 1) for k in (0, 1)])
@@ -103,9 +121,18 @@ def test_parts(bias, residual, keep):
 
 
 def test_plain_call_is_spmm():
-    values, meta, X, _, _ = inputs(300, 512, 136, 2, 4, "bf16", "blocked")
-    want = nm.spmm(values, meta, X, 2, 4, layout="blocked", rows=300)
-    assert torch.equal(nm.spmm_act(values, meta, X, layout="blocked", rows=300), want)
+    """Both form the same sums in orders of their own, each within sum_bound, and round once."""
+    values, meta, X, W, Xd = inputs(300, 512, 136, 2, 4, "bf16", "blocked")
+    want = nm.spmm(values, meta, X, 2, 4, layout="blocked", rows=300).double().cpu()
+    got = nm.spmm_act(values, meta, X, layout="blocked", rows=300)
+    off = 2 * (ref.sum_bound(256, W.abs() @ Xd.abs()) + ref.rounding(want, torch.bfloat16))
+    ref.check(got, want, off * (1 + 2 * ref.HALF[torch.bfloat16]), "Y")
+
+
+def test_plain_call_is_spmm_bit_for_bit_in_the_same_kernel():
+    values, meta, X, _, _ = inputs(2000, 128, 2056, 2, 4, "bf16", "blocked")
+    want = nm.spmm(values, meta, X, 2, 4, layout="blocked", rows=2000)
+    assert torch.equal(nm.spmm_act(values, meta, X, layout="blocked", rows=2000), want)
 
 
 @pytest.mark.parametrize("T", [40, 41])

@@ -16,11 +16,14 @@ BF, F16, F32, I8, FP8 = nm.NM_BF16, nm.NM_F16, nm.NM_F32, nm.NM_I8, nm.NM_FP8
 
 def test_sizes():
     L = nm.lib()
-    assert L.nm_spmm_act_workspace_bytes(64, 8, BF) == 0
-    assert L.nm_spmm_act_workspace_bytes(64, 7, BF) == 64 * 8 * 2
-    assert L.nm_spmm_act_workspace_bytes(64, 7, F32) == 64 * 8 * 4
-    assert L.nm_spmm_act_workspace_bytes(64, 17, I8) == 64 * 32
-    assert L.nm_spmm_act_workspace_bytes(-1, 7, BF) == L.nm_spmm_act_workspace_bytes(64, 7, 9) == 0
+    act = L.nm_spmm_act_workspace_bytes
+    assert act(32, 60, 2, 4, 8, BF) == 0                 # rows of X are whole pieces
+    assert act(32, 60, 2, 4, 7, BF) == 60 * 8 * 2 // 256 * 256 + 256
+    assert act(32, 60, 2, 4, 7, F32) == 60 * 8 * 4 // 256 * 256 + 256
+    assert act(32, 64, 2, 4, 7, BF) == 64 * 16 * 2       # few tokens: X turned, 16 columns
+    assert act(32, 64, 2, 4, 7, F32) == 64 * 16 * 4 and act(32, 64, 1, 2, 7, I8) == 64 * 16 * 2
+    assert act(8192, 4096, 2, 4, 2048, BF) == 0          # many: as it lies
+    assert act(32, -4, 2, 4, 7, BF) == act(32, 64, 2, 4, 7, 9) == act(32, 64, 5, 4, 7, BF) == 0
     need = L.nm_spmm_act_grad_workspace_bytes
     assert need(64, 64, 64, 0, 1, 0, 0) == 0                       # dW = dY X^T as they lie
     assert need(64, 64, 64, 0, 1, 1, 0) == 64 * 64 * 2             # the dense W
@@ -56,14 +59,14 @@ def test_spmm_act_refusals():
     assert spmm_act(act=6) == spmm_act(act=-1) == "unsupported"
     assert spmm_act(dt=I8, Z=None, n=1, m=8, ydt=F32) == "unsupported"
     assert spmm_act(values=None) == spmm_act(meta=None) == spmm_act(X=None) == spmm_act(Y=None) == "null"
-    assert spmm_act(T=15, ws=None) == "null" and spmm_act(T=15, size=100) == "scratch"
+    assert spmm_act(ws=None) == "null" and spmm_act(size=100) == "scratch"
     for name in ("values", "meta", "X", "bias", "residual", "Z", "Y"):
         assert spmm_act(**{name: ODD}) == "align", name
-    assert spmm_act(T=15, ws=ODD) == "align"
+    assert spmm_act(ws=ODD) == "align"
     assert spmm_act(dt=I8, Z=None, scale=ODD, ydt=F32) == "align"
     for name in ("values", "meta", "X", "bias", "Z"):
         assert spmm_act(**{name: far(7)}) == "alias", name
-    assert spmm_act(Z=far(5)) == spmm_act(T=15, ws=far(3)) == spmm_act(T=15, ws=far(6)) == "alias"
+    assert spmm_act(Z=far(5)) == spmm_act(ws=far(3)) == spmm_act(ws=far(6)) == "alias"
     assert spmm_act(residual=ctypes.c_void_p(far(7).value + 64)) == "alias"
     assert spmm_act(residual=far(7)) == "device"                   # in place: as far as a GPU
     assert spmm_act(bias=None, residual=None, Z=None) == "device"
