@@ -39,7 +39,6 @@ from __future__ import annotations
 
 import array
 import ctypes
-import operator
 import os
 
 import torch
@@ -902,9 +901,6 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
 _FLOAT_DT = {torch.float32: NM_F32, torch.float16: NM_F16, torch.bfloat16: NM_BF16}
 
 
-_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
-
-
 class _Tensors:
     """The host arrays that nm_grad_norm and nm_clip_grads take, of dense float tensors on one GPU."""
 
@@ -912,17 +908,17 @@ class _Tensors:
         self.grads = grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
         if not grads:
             raise ValueError("no tensors")
-        self.device = grads[0].device
-        dts = list(map(_FLOAT_DT.get, map(_dtype_of, grads)))
-        # (a step of a model has hundreds of tensors: one look at all of them for each property)
-        self.contiguous = all(map(torch.Tensor.is_contiguous, grads))
-        if self.device.type != "cuda" or None in dts or \
-                len(set(map(torch.Tensor.get_device, grads))) != 1 or not (self.contiguous or all(
-                    g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous()) for g in grads)):
+        # (a step of a model has hundreds of tensors, and a look at one costs more than its clipping)
+        dts = [_FLOAT_DT.get(g.dtype) for g in grads]
+        self.contiguous = all([g.is_contiguous() for g in grads])
+        devices = set([g.get_device() for g in grads])
+        if None in dts or len(devices) != 1 or min(devices) < 0 or not (self.contiguous or all(
+                g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous()) for g in grads)):
             raise ValueError("gradients must be float32, float16 or bfloat16 tensors without gaps on "
                              "one GPU")
-        self.pointers = array.array("q", map(torch.Tensor.data_ptr, grads))
-        self.counts = array.array("q", map(torch.Tensor.numel, grads))
+        self.device = devices.pop()
+        self.pointers = array.array("q", [g.data_ptr() for g in grads])
+        self.counts = array.array("q", [g.numel() for g in grads])
         self.dts = array.array("i", dts)
 
     def addresses(self):
@@ -931,10 +927,10 @@ class _Tensors:
 
     def same_places(self, other) -> bool:
         """Whether entry i of a tensor here stands for entry i of the other's."""
-        return (self.dts == other.dts and self.device == other.device and
-                list(map(_shape_of, self.grads)) == list(map(_shape_of, other.grads)) and
-                ((self.contiguous and other.contiguous) or all(
-                    a.stride() == b.stride() for a, b in zip(self.grads, other.grads))))
+        return (self.dts == other.dts and self.counts == other.counts and
+                self.device == other.device and ((self.contiguous and other.contiguous) or all(
+                    a.shape == b.shape and a.stride() == b.stride()
+                    for a, b in zip(self.grads, other.grads))))
 
 
 def grad_norm(grads) -> torch.Tensor:
@@ -953,13 +949,13 @@ def grad_norm(grads) -> torch.Tensor:
 
 def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=None) -> torch.Tensor:
     """Every gradient times max_norm / norm where the norm of all of them is finite and above
-    max_norm, in place or into `out` (tensors of the same shapes, strides and types); returns the norm
-    before clipping.  `norm` (float32, one number on the GPU) takes the place of the gradients' own, as
+    max_norm, in place or into `out` (tensors of the same sizes, types and order of entries); returns the
+    norm before clipping.  `norm` (float32, one number on the GPU) takes the place of the gradients' own, as
     where each rank holds a part of them: join grad_norm's squares over the ranks first."""
     t = _Tensors(grads)
     o = t if out is None else _Tensors(out)
     if o is not t and not o.same_places(t):
-        raise ValueError("out must match the gradients' shapes, strides, dtypes and device")
+        raise ValueError("out must match the gradients' sizes, order of entries, dtypes and device")
     like = t.grads[0]
     given = norm
     if norm is None:

@@ -9,7 +9,8 @@
 // dense weight, as SR-STE takes it.  W^T has no structure that the sparse instruction could use (W's
 // groups run along its rows), so W is decompressed and both products are dense (nm_gemm.h).
 //
-// Both products go out in one launch, dX's long sums first: alone, each leaves units idle at its end.
+// What the products need (dZ, X and W in whole steps) goes out in one launch where W is small, and both
+// products in one, dX's long sums first: alone, each leaves units idle at its end.
 #include <algorithm>
 
 #include "nm_act.h"
@@ -34,11 +35,10 @@ typedef uint32_t u32x4_byte_t __attribute__((ext_vector_type(4), aligned(1)));
 
 // E: an element's storage.  A thread a 16-byte piece of the output.
 template <typename E>
-__global__ void __launch_bounds__(256) widen_kernel(WidenArgs p) {
+__device__ __forceinline__ void widen_pieces(const WidenArgs& p, int64_t first, int64_t stride) {
   constexpr int kPer = 16 / sizeof(E);
   const int64_t pieces = p.out_width / kPer, total = p.out_rows * pieces;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = first; i < total; i += stride) {
     const int64_t r = i / pieces, c = i % pieces * kPer;
     u32x4_t v{0, 0, 0, 0};
     if (r < p.rows && c < p.width) {
@@ -55,6 +55,10 @@ __global__ void __launch_bounds__(256) widen_kernel(WidenArgs p) {
     }
     reinterpret_cast<u32x4_t*>(p.out)[i] = v;
   }
+}
+template <typename E>
+__global__ void __launch_bounds__(256) widen_kernel(WidenArgs p) {
+  widen_pieces<E>(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 hipError_t widen(const void* in, int64_t rows, int64_t width, void* out, int64_t out_rows,
@@ -90,11 +94,10 @@ struct SlopeArgs {
 
 // WPR waves of a workgroup's four to a row; its sums are joined in wave order.
 template <bool BF16, int WPR>
-__global__ void __launch_bounds__(256) slope_kernel(SlopeArgs p) {
+__device__ __forceinline__ void slope_rows(const SlopeArgs& p, int64_t group, float* part) {
   constexpr int DT = BF16 ? kBF16 : kF16, kRows = 4 / WPR;
-  __shared__ float part[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = (int64_t)blockIdx.x * kRows + wave / WPR;
+  const int64_t row = group * kRows + wave / WPR;
   const int64_t width = p.padded ? p.Tp : p.T, rows = p.padded ? p.Rp : p.R;
   float sum = 0.f;
   if (row < rows) {
@@ -139,6 +142,87 @@ __global__ void __launch_bounds__(256) slope_kernel(SlopeArgs p) {
     }
   } else if (lane == 0 && row < p.R) {
     p.dbias[row] = sum;
+  }
+}
+
+template <bool BF16, int WPR>
+__global__ void __launch_bounds__(256) slope_kernel(SlopeArgs p) {
+  __shared__ float part[4];
+  slope_rows<BF16, WPR>(p, blockIdx.x, part);
+}
+
+// ---- W ---------------------------------------------------------------------------------------------
+
+// The dense W of a pair of any pattern and layout, 16 bits, rows of Kp numbers with zeros after the K-th:
+// a thread eight of them.  For small matrices and widths that are not multiples of 8; the others are
+// decompressed by nm_compress.hip's kernels, which are specialised for each pattern.
+struct ExpandArgs {
+  const uint16_t* values;
+  const uint8_t* meta;
+  int64_t R, K, Kp;
+  int n, m, bits;
+  bool blocked;
+  uint16_t* out;
+};
+__device__ __forceinline__ void expand_pieces(const ExpandArgs& p, int64_t first, int64_t stride) {
+  const int64_t pieces = p.Kp / 8, total = p.R * pieces, row_values = p.K / p.m * p.n;
+  const int per = 64 / p.m * p.n;  // values of a row and step of the blocked layout
+  const int64_t meta_row = (row_values * p.bits + 31) / 32 * 4;
+  for (int64_t i = first; i < total; i += stride) {
+    const int64_t r = i / pieces;
+    const int k0 = (int)(i % pieces * 8);
+    uint64_t half[2] = {0, 0};  // numbers 0 .. 3 and 4 .. 7
+    const int groups = 8 / p.m;
+    for (int g = 0; g < groups && k0 + g * p.m < p.K; ++g) {
+      const int64_t f0 = (int64_t)(k0 / p.m + g) * p.n;  // the group's first value in its row
+      int64_t vi, bit;
+      const uint8_t* places;
+      if (p.blocked) {
+        const int64_t block = ((r >> 4) * (p.K / 64) + f0 / per) * 16 + (r & 15);
+        vi = block * per + f0 % per;
+        places = p.meta + block * (per * p.bits / 8);
+        bit = f0 % per * p.bits;
+      } else {
+        vi = r * row_values + f0;
+        places = p.meta + r * meta_row;
+        bit = f0 * p.bits;
+      }
+      for (int j = 0; j < p.n; ++j, bit += p.bits) {
+        const int shift = (int)(bit & 7);
+        uint32_t field = places[bit >> 3] >> shift;
+        if (shift + p.bits > 8) field |= (uint32_t)places[(bit >> 3) + 1] << (8 - shift);
+        const int at = g * p.m + (int)(field & (uint32_t)(p.m - 1));
+        // (as the decompression has it: the later value of a place that is given twice)
+        const uint64_t v = p.values[vi + j], mask = (uint64_t)0xFFFF << (16 * (at & 3));
+        const uint64_t put = v << (16 * (at & 3));
+        if (at < 4) half[0] = (half[0] & ~mask) | put;
+        else half[1] = (half[1] & ~mask) | put;
+      }
+    }
+    reinterpret_cast<u32x4_t*>(p.out)[i] =
+        u32x4_t{(uint32_t)half[0], (uint32_t)(half[0] >> 32), (uint32_t)half[1], (uint32_t)(half[1] >> 32)};
+  }
+}
+
+// All that the products need in one launch: workgroups for dZ's rows, then for X, then for W.
+struct PrepareArgs {
+  SlopeArgs slope;
+  WidenArgs x;
+  ExpandArgs w;
+  unsigned slope_groups, x_groups, w_groups;
+};
+template <bool BF16>
+__global__ void __launch_bounds__(256) prepare_kernel(PrepareArgs p) {
+  __shared__ float part[4];
+  const unsigned b = blockIdx.x;
+  if (b < p.slope_groups) {
+    slope_rows<BF16, 1>(p.slope, b, part);
+  } else if (b < p.slope_groups + p.x_groups) {
+    widen_pieces<uint16_t>(p.x, (int64_t)(b - p.slope_groups) * 256 + threadIdx.x,
+                           (int64_t)p.x_groups * 256);
+  } else {
+    expand_pieces(p.w, (int64_t)(b - p.slope_groups - p.x_groups) * 256 + threadIdx.x,
+                  (int64_t)p.w_groups * 256);
   }
 }
 
@@ -216,23 +300,25 @@ __global__ void __launch_bounds__(256) join_splits_kernel(GradProduct p) {
   }
 }
 
+// Entries of W up to which it is expanded in the launch that prepares the rest: 1000 x 768 in 3.5 us of
+// its own, and a launch less; past it the specialised kernels' rate counts.
+constexpr int64_t kSmallW = 4 << 20;
+
 // Where everything lies in the workspace.
 struct SpmmGradLayout {
   int64_t Rp, Tp, Kp;           // Kp: row length of the dense W
-  bool pad_z, pad_x, pad_w;     // dZ goes to a padded copy; X is copied; W is decompressed, then copied
+  bool pad_z, pad_x;            // dZ goes to a padded copy; X is copied
   SpmmGradCut cut;
-  int64_t z, x, w, w_tight, sums_x, sums_w, total;
+  int64_t z, x, w, sums_x, sums_w, total;
   SpmmGradLayout(int64_t R, int64_t K, int64_t T, bool want_w, bool want_x, bool want_z, bool act)
       : Rp(pad64(R)), Tp(pad64(T)), Kp(K % 8 == 0 ? K : pad64(K)), cut(R, K, T, want_w, want_x) {
     const bool whole = Rp == R && Tp == T, product = want_w || want_x;
     pad_z = product && (!whole || (act && !want_z));
     pad_x = want_w && Tp != T;
-    pad_w = want_x && Kp != K;
     z = 0;
     x = z + (pad_z ? whole256(Rp * Tp * 2) : 0);
     w = x + (pad_x ? whole256(K * Tp * 2) : 0);
-    w_tight = w + (want_x ? whole256(R * Kp * 2) : 0);
-    sums_x = w_tight + (pad_w ? whole256(R * K * 2) : 0);
+    sums_x = w + (want_x ? whole256(R * Kp * 2) : 0);
     sums_w = sums_x + (cut.splits_x > 1 ? whole256(cut.splits_x * K * ((T + 3) / 4 * 4) * 4) : 0);
     total = sums_w + (cut.splits_w > 1 ? whole256(cut.splits_w * R * ((K + 3) / 4 * 4) * 4) : 0);
   }
@@ -265,33 +351,46 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
   const bool want_w = c.dW && R * K > 0, want_x = c.dX && K * T > 0, act = c.act != kActNone;
   const SpmmGradLayout L(R, K, T, want_w, want_x, c.dZ != nullptr, act);
   const uint16_t* dz = static_cast<const uint16_t*>(act ? c.dZ : c.dY);
-  hipError_t e;
-  if (R > 0 && (L.pad_z || c.dZ || c.dbias)) {
-    SlopeArgs a{c.Z, c.dY, R, T, c.act, nullptr, L.Rp, L.Tp, static_cast<uint16_t*>(c.dZ), c.dbias};
-    if (L.pad_z) {
-      a.padded = reinterpret_cast<uint16_t*>(ws + L.z);
-      dz = a.padded;
-    }
-    const int64_t rows = a.padded ? L.Rp : R;
-    // a wave a row fills the device where rows are many or short
-    if (rows >= 2048 || T <= 512)
-      slope_kernel<BF16, 1><<<(unsigned)((rows + 3) / 4), 256, 0, s>>>(a);
-    else
-      slope_kernel<BF16, 4><<<(unsigned)rows, 256, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  if (!want_w && !want_x) return hipSuccess;
   const uint16_t* x = static_cast<const uint16_t*>(c.X);
+  hipError_t e;
+  PrepareArgs a{};
+  if (R > 0 && (L.pad_z || c.dZ || c.dbias)) {
+    a.slope = SlopeArgs{c.Z, c.dY, R, T, c.act, nullptr, L.Rp, L.Tp, static_cast<uint16_t*>(c.dZ), c.dbias};
+    if (L.pad_z) {
+      a.slope.padded = reinterpret_cast<uint16_t*>(ws + L.z);
+      dz = a.slope.padded;
+    }
+    const int64_t rows = a.slope.padded ? L.Rp : R;
+    if (rows >= 2048 || T <= 512) {  // a wave a row fills the device where rows are many or short
+      a.slope_groups = (unsigned)((rows + 3) / 4);
+    } else {
+      slope_kernel<BF16, 4><<<(unsigned)rows, 256, 0, s>>>(a.slope);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
   if (L.pad_x) {
-    if ((e = widen(c.X, K, T, ws + L.x, K, L.Tp, 2, s)) != hipSuccess) return e;
+    a.x = WidenArgs{static_cast<const uint8_t*>(c.X), ws + L.x, K, T, K, L.Tp};
+    a.x_groups = stride_grid(K * L.Tp / 8, 256);
     x = reinterpret_cast<const uint16_t*>(ws + L.x);
   }
   if (want_x && R > 0) {
-    uint8_t* to = ws + (L.pad_w ? L.w_tight : L.w);
-    e = launch_decompress(c.values, c.meta, 2, R, K, c.n, c.m, c.blocked, to, s);
-    if (e == hipSuccess && L.pad_w) e = widen(to, R, K, ws + L.w, R, L.Kp, 2, s);
-    if (e != hipSuccess) return e;
+    uint16_t* to = reinterpret_cast<uint16_t*>(ws + L.w);
+    if (R * K > kSmallW && L.Kp == K) {
+      e = launch_decompress(c.values, c.meta, 2, R, K, c.n, c.m, c.blocked, to, s);
+      if (e != hipSuccess) return e;
+    } else {
+      a.w = ExpandArgs{static_cast<const uint16_t*>(c.values), reinterpret_cast<const uint8_t*>(c.meta), R,
+                       K, L.Kp, c.n, c.m, c.m == 2 ? 1 : c.m == 4 ? 2 : 3, c.blocked, to};
+      a.w_groups = stride_grid(R * L.Kp / 8, 256);
+    }
   }
+  const unsigned groups = a.slope_groups + a.x_groups + a.w_groups;
+  if (groups > 0) {
+    if (groups == a.slope_groups) slope_kernel<BF16, 1><<<groups, 256, 0, s>>>(a.slope);
+    else prepare_kernel<BF16><<<groups, 256, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (!want_w && !want_x) return hipSuccess;
   GradProducts p{};
   p.x.a = GemmOperand{reinterpret_cast<const uint16_t*>(ws + L.w), L.Kp, L.Kp, 0};
   p.x.b = GemmOperand{dz, L.Tp, L.Tp, 0};
@@ -327,7 +426,7 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
 
 size_t spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, int dt) {
   if (thin_preferred(R, K, n, m, T, elem_of(dt)))
-    return (size_t)(ThinPlan(R, K, T, dt == kF32).Tp * K * (dt == kF32 ? 4 : 2));
+    return (size_t)(ThinPlan(R, K, T, dt == kF32).Tp * pad64(K) * (dt == kF32 ? 4 : 2));
   const int64_t ldx = whole_row(T, dt);
   return ldx == T ? 0 : (size_t)whole256(K * ldx * elem_of(dt));
 }

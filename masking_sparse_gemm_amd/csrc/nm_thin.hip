@@ -62,8 +62,13 @@ __global__ void __launch_bounds__(256) turn_kernel(TurnArgs p) {
   const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
   E in[16];
 #pragma unroll
+  for (int i = 0; i < 16; ++i) {  // (loads without conditions, or each would be waited for)
+    const int64_t k = k0 + r + 4 * i;
+    in[i] = x[min(k, p.K - 1) * p.T + min(t0 + c, p.T - 1)];
+  }
+#pragma unroll
   for (int i = 0; i < 16; ++i)
-    in[i] = t0 + c < p.T ? x[(k0 + r + 4 * i) * p.T + t0 + c] : E(0);
+    if (t0 + c >= p.T || k0 + r + 4 * i >= p.K) in[i] = E(0);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if constexpr (DT == kF32) tile[c][r + 4 * i] = __float_as_uint(in[i]);
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(256) turn_kernel(TurnArgs p) {
       if constexpr (DT == kF32) w[e] = tile[col][k + e];
       else w[e] = tile[col][k + 2 * e] | (uint32_t)tile[col][k + 2 * e + 1] << 16;
     }
-    const int64_t block = (t0 / 16 + b) * (p.K / 64) + blockIdx.x;
+    const int64_t block = (t0 / 16 + b) * ((p.K + 63) / 64) + blockIdx.x;
     static_cast<u32x4_t*>(p.xt)[block * (16 * kPieces) + in_b] = w;
   }
 }
@@ -94,6 +99,7 @@ struct ThinArgs {
   const uint8_t* meta;
   const void* xt;
   int64_t R, K, T, Tp;
+  int64_t row_values, row_meta;  // of the row layout: values, bytes of metadata
   Epilogue ep;
 };
 
@@ -105,6 +111,31 @@ struct ThinRaw {
   static constexpr int kBytes = kValues * (int)sizeof(E);
   uint32_t w[kBytes / 4];
   uint32_t places;
+
+  // The row's values and places at any address, its sixteen K ending after `left` values (none or fewer
+  // than kValues, whole groups; zeros at place 0 after them): the row layout where K is not whole steps.
+  __device__ __forceinline__ void load_ragged(const uint8_t* v, const uint8_t* m, int64_t left) {
+    typedef uint32_t one_t __attribute__((aligned(1)));
+    typedef uint16_t half_t __attribute__((aligned(1)));
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) w[i] = 0u;
+    places = 0u;
+    if (left >= kValues) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 4; ++i) w[i] = reinterpret_cast<const one_t*>(v)[i];
+      places = PAT == kP24 ? *reinterpret_cast<const half_t*>(m) : *m;
+    } else if (left > 0) {
+#pragma unroll
+      for (int i = 0; i < kValues; ++i) {
+        if (i >= left) continue;
+        if constexpr (sizeof(E) == 4) w[i] = reinterpret_cast<const one_t*>(v)[i];
+        else if constexpr (sizeof(E) == 2) w[i / 2] |= (uint32_t)reinterpret_cast<const half_t*>(v)[i] << (16 * (i & 1));
+        else w[i / 4] |= (uint32_t)v[i] << (8 * (i & 3));
+      }
+      places = *m;  // rows of metadata are whole words: a second byte only where values need it
+      if (PAT == kP24 && left > 4) places |= (uint32_t)m[1] << 8;
+    }
+  }
 
   // values: the row's first of the sixteen K; places: their first byte
   __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m) {
@@ -194,7 +225,8 @@ __device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t&
                                                      0);
 }
 
-template <int DT, int PAT, bool BLOCKED, int RG, int NT>
+// RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).
+template <int DT, int PAT, bool BLOCKED, bool RAGGED, int RG, int NT>
 __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   typedef typename ThinElem<DT>::type E;
   typedef ThinRaw<DT, PAT> Raw;
@@ -205,7 +237,8 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   __shared__ __attribute__((aligned(16))) float sums[kThinWaves][kRows * kPitch];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int steps = (int)(p.K / 64);
+  const int steps = (int)((p.K + 63) / 64);
+  static_assert(!(BLOCKED && RAGGED), "blocks are whole steps");
   const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kCols;
   const int64_t groups = (p.R + 15) / 16;
 
@@ -219,8 +252,8 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
       m[g] = p.meta + (b * steps * 16 + l16) * kRowMeta + q * (kRowMeta / 4);
     } else {
       const int64_t row = min(r0 + 16 * g + l16, p.R - 1);
-      v[g] = p.values + row * steps * kRowValues * (int64_t)sizeof(E) + q * Raw::kBytes;
-      m[g] = p.meta + row * steps * kRowMeta + q * (kRowMeta / 4);
+      v[g] = p.values + row * p.row_values * (int64_t)sizeof(E) + q * Raw::kBytes;
+      m[g] = p.meta + row * p.row_meta + q * (kRowMeta / 4);
     }
   }
   constexpr int kVStep = (BLOCKED ? 16 : 1) * kRowValues * (int)sizeof(E);
@@ -234,7 +267,11 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   };
   const auto load = [&](Step& f, int s) {
 #pragma unroll
-    for (int g = 0; g < RG; ++g) f.a[g].load(v[g] + (int64_t)s * kVStep, m[g] + (int64_t)s * kMStep);
+    for (int g = 0; g < RG; ++g) {
+      const uint8_t *va = v[g] + (int64_t)s * kVStep, *ma = m[g] + (int64_t)s * kMStep;
+      if constexpr (RAGGED) f.a[g].load_ragged(va, ma, p.row_values - (4 * (int64_t)s + q) * Raw::kValues);
+      else f.a[g].load(va, ma);
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const u32x4_t* at = x + ((int64_t)t * steps + s) * (64 * kPieces);
@@ -352,12 +389,12 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   store_eight(p.ep.y, y_type<DT>(p.ep), i, left, y);
 }
 
-template <int DT, int PAT, bool BLOCKED>
+template <int DT, int PAT, bool BLOCKED, bool RAGGED>
 hipError_t launch_cols(const ThinArgs& p, const ThinPlan& plan, hipStream_t s) {
   const auto go = [&](auto rg, auto nt) {
     constexpr int RG = decltype(rg)::value, NT = decltype(nt)::value;
     const dim3 grid((unsigned)((p.R + 16 * RG - 1) / (16 * RG)), (unsigned)(plan.Tp / (16 * NT)));
-    thin_kernel<DT, PAT, BLOCKED, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
+    thin_kernel<DT, PAT, BLOCKED, RAGGED, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, 1> One;
@@ -371,17 +408,18 @@ template <int DT>
 hipError_t launch_thin_as(const ThinArgs& p, const ThinPlan& plan, int pat, bool blocked, const void* X,
                           void* xt, hipStream_t s) {
   const TurnArgs turn{X, p.K, p.T, p.Tp, xt};
-  turn_kernel<DT><<<dim3((unsigned)(p.K / 64), (unsigned)((p.Tp + 63) / 64)), 256, 0, s>>>(turn);
+  turn_kernel<DT><<<dim3((unsigned)((p.K + 63) / 64), (unsigned)((p.Tp + 63) / 64)), 256, 0, s>>>(turn);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (blocked) {
-    if (pat == kP24) return launch_cols<DT, kP24, true>(p, plan, s);
-    if (pat == kP12) return launch_cols<DT, kP12, true>(p, plan, s);
-    return launch_cols<DT, kP14, true>(p, plan, s);
-  }
-  if (pat == kP24) return launch_cols<DT, kP24, false>(p, plan, s);
-  if (pat == kP12) return launch_cols<DT, kP12, false>(p, plan, s);
-  return launch_cols<DT, kP14, false>(p, plan, s);
+  const auto go = [&](auto pattern) {
+    constexpr int PAT = decltype(pattern)::value;
+    if (blocked) return launch_cols<DT, PAT, true, false>(p, plan, s);
+    if (p.K % 64 == 0) return launch_cols<DT, PAT, false, false>(p, plan, s);
+    return launch_cols<DT, PAT, false, true>(p, plan, s);
+  };
+  if (pat == kP24) return go(std::integral_constant<int, kP24>{});
+  if (pat == kP12) return go(std::integral_constant<int, kP12>{});
+  return go(std::integral_constant<int, kP14>{});
 }
 
 }  // namespace
@@ -392,7 +430,8 @@ hipError_t launch_thin(const void* values, const uint32_t* meta, int64_t R, int6
   const ThinPlan plan(R, K, T, dt == kF32);
   void* xt = workspace;
   const ThinArgs p{static_cast<const uint8_t*>(values), reinterpret_cast<const uint8_t*>(meta), xt, R,
-                   K, T, plan.Tp, epilogue_of(product)};
+                   K, T, plan.Tp, K / m * n, ((K / m * n) * (m == 2 ? 1 : 2) + 31) / 32 * 4,
+                   epilogue_of(product)};
   const int pat = m == 2 ? kP12 : n == 2 ? kP24 : kP14;
   if (dt == kBF16) return launch_thin_as<kBF16>(p, plan, pat, blocked, X, xt, s);
   if (dt == kF16) return launch_thin_as<kF16>(p, plan, pat, blocked, X, xt, s);

@@ -114,7 +114,7 @@ struct ThinPlan {
     constexpr double kStep[3] = {0.41, 0.65, 1.0}, kStep32[2] = {1.0, 3.0};
     for (int i = 0; i < (f32 ? 2 : 3); ++i) {
       const int64_t rows = 16 * kShapes[i][0], cols = 16 * kShapes[i][1], tp = (T + cols - 1) / cols;
-      const int64_t groups = (R + rows - 1) / rows * tp, eights = (K / 64 + 7) / 8;
+      const int64_t groups = (R + rows - 1) / rows * tp, eights = ((K + 63) / 64 + 7) / 8;
       const double t = 5 + (double)((groups + 255) / 256) * (double)eights * (f32 ? kStep32[i] : kStep[i]);
       if (t < us) {
         us = t;
@@ -130,8 +130,8 @@ struct ThinPlan {
 // tiles, the rate where there are many.  Measured alone, us a step of 64 K: 2:4 and 1:2 in 16 bits
 // 0.49, in 8 bits 0.22, expanded 16 and 8 bits 1.45, fp32 5.25.
 inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
-  const double S = (double)K / 64, work = 2.0 * (double)R * (double)K * (double)T;
-  const bool sparse = (n == 2 && m == 4) || (n == 1 && m == 2);
+  const double S = (double)((K + 63) / 64), work = 2.0 * (double)R * (double)K * (double)T;
+  const bool sparse = ((n == 2 && m == 4) || (n == 1 && m == 2)) && K % 64 == 0;
   if (elem == 4) return std::max(5.3 + 5.25 * S, 5 + work / 0.115e9);
   if (!sparse || (elem == 1 && K % 128 != 0)) return std::max(7 + 1.45 * S, 5 + work / 0.54e9);
   if (elem == 1) return std::max(9.7 + 0.22 * S, 6 + work / 3.0e9);
@@ -141,7 +141,7 @@ inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) 
 // Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).
 inline bool thin_preferred(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
   const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4));
-  if (!pattern || K == 0 || K % 64 != 0 || T > 4096) return false;
+  if (!pattern || K == 0 || T > 4096) return false;
   return ThinPlan(R, K, T, elem == 4).us < tiled_us(R, K, n, m, T, elem);
 }
 
@@ -163,7 +163,7 @@ struct SpmmGradCut {
       return t == kTile256 ? count * (2.0 * s + 8) / 256
                            : count * (t == kTile128 ? 1.19 * s + 4.6 : 0.71 * s + 3.5) / 512;
     };
-    const auto join = [](int z, int64_t numbers) { return z == 1 ? 0.0 : 3.0 + z * numbers * 8 / 5e6; };
+    const auto join = [](int z, int64_t numbers) { return z == 1 ? 0.0 : 4.5 + z * numbers * 8 / 5e6; };
     double least = 1e30;
     for (int t = 0; t < kXentTiles; ++t)
       for (int zx = 1; zx <= kMaxSplit && (zx == 1 || (want_x && sx / zx >= 4)); zx = next(zx))

@@ -17,9 +17,10 @@ BF, F16, F32, I8, FP8 = nm.NM_BF16, nm.NM_F16, nm.NM_F32, nm.NM_I8, nm.NM_FP8
 def test_sizes():
     L = nm.lib()
     act = L.nm_spmm_act_workspace_bytes
-    assert act(32, 60, 2, 4, 8, BF) == 0                 # rows of X are whole pieces
-    assert act(32, 60, 2, 4, 7, BF) == 60 * 8 * 2 // 256 * 256 + 256
-    assert act(32, 60, 2, 4, 7, F32) == 60 * 8 * 4 // 256 * 256 + 256
+    assert act(32, 72, 3, 8, 8, BF) == 0                 # rows of X are whole pieces
+    assert act(32, 72, 3, 8, 7, BF) == 72 * 8 * 2 // 256 * 256 + 256
+    assert act(32, 72, 3, 8, 7, F32) == 72 * 8 * 4 and act(32, 72, 3, 8, 17, I8) == 72 * 32
+    assert act(32, 60, 2, 4, 7, BF) == 64 * 16 * 2       # few tokens: X turned, in whole steps
     assert act(32, 64, 2, 4, 7, BF) == 64 * 16 * 2       # few tokens: X turned, 16 columns
     assert act(32, 64, 2, 4, 7, F32) == 64 * 16 * 4 and act(32, 64, 1, 2, 7, I8) == 64 * 16 * 2
     assert act(8192, 4096, 2, 4, 2048, BF) == 0          # many: as it lies

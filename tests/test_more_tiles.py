@@ -40,7 +40,7 @@ def rule(tmp_path_factory):
 def test_thin_or_tiled(rule):
     assert rule(4096, 4096, 2, 4, 1, 2)["thin"] and rule(1000, 1024, 2, 4, 517, 2)["thin"]
     assert not rule(11008, 4096, 2, 4, 2048, 2)["thin"] and not rule(4096, 11008, 2, 4, 2048, 2)["thin"]
-    assert not rule(64, 100, 2, 4, 1, 2)["thin"]       # K is not whole steps
+    assert rule(64, 100, 2, 4, 1, 2)["thin"]           # K need not be whole steps
     assert not rule(64, 64, 4, 8, 1, 2)["thin"] and not rule(64, 64, 2, 2, 1, 2)["thin"]
     assert rule(4096, 4096, 1, 4, 256, 2)["thin"] and rule(4096, 4096, 2, 4, 512, 4)["thin"]
     assert not rule(16, 64, 2, 4, 1 << 20, 2)["thin"]
