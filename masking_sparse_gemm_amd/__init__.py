@@ -746,17 +746,19 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _expect(t: torch.Tensor | None, name: str, shape, dtype: torch.dtype, device) -> None:
-    """t, where it is given, is a contiguous tensor of that shape, type and device."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or
-                          t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}")
+def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, device: int) -> None:
+    """t, where it is given, is a contiguous tensor of that shape and type on GPU number `device`."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != device or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on GPU {device}")
 
 
-def _row_numbers(t: torch.Tensor | None, name: str, rows: int, device):
+def _row_numbers(t: torch.Tensor | None, name: str, rows: int, device: int):
     """t, or its copy where it is a view that starts off 16 bytes."""
+    if t is None:
+        return None
     _expect(t, name, (rows,), torch.float32, device)
-    return None if t is None else _token_numbers(t)
+    return _token_numbers(t)
 
 
 def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int = 2, m: int = 4,
@@ -776,7 +778,8 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
     dt, R = _check_compressed(values, meta, n, m, K, layout, rows)
     if dt != xdt:
         raise ValueError("values and X must have the same dtype")
-    if values.device != X.device:
+    device = X.get_device()
+    if values.get_device() != device:
         raise ValueError("values and X must be on the same device")
     eight = X.dtype in _BYTE
     y_dtype = out_dtype or (torch.bfloat16 if eight else X.dtype)
@@ -786,10 +789,10 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
         raise ValueError("scale goes with int8 and float8 products")
     if keep and eight:
         raise ValueError("int8 and float8 products keep no Z")
-    bias = _row_numbers(bias, "bias", R, X.device)
-    scale = _row_numbers(scale, "scale", R, X.device)
-    _expect(residual, "residual", (R, T), y_dtype, X.device)
-    _expect(out, "out", (R, T), y_dtype, X.device)
+    bias = _row_numbers(bias, "bias", R, device)
+    scale = _row_numbers(scale, "scale", R, device)
+    _expect(residual, "residual", (R, T), y_dtype, device)
+    _expect(out, "out", (R, T), y_dtype, device)
     if out is None:
         out = X.new_empty((R, T), dtype=y_dtype)
     Z = X.new_empty((R, T)) if keep else None
@@ -820,7 +823,7 @@ def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: tor
     _dense_input(dY, "dY", int8=False)
     dt = _half(dY.dtype, "dY")
     R, T = dY.shape
-    device = dY.device
+    device = dY.get_device()
     if rows is not None and rows != R:
         raise ValueError(f"rows={rows} does not match dY ({R} rows)")
     if code:
@@ -839,7 +842,7 @@ def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: tor
             raise ValueError("dX needs values and meta")
         lay = _layout(layout)
         vdt, vrows = _check_compressed(values, meta, n, m, K, layout, R)
-        if vdt != dt or vrows != R or values.device != device:
+        if vdt != dt or vrows != R or values.get_device() != device:
             raise ValueError("values must have dY's rows, dtype and device")
     shapes = dict(dW=((R, K), dY.dtype), dX=((K, T), dY.dtype), dbias=((R,), torch.float32),
                   dZ=((R, T), dY.dtype))
@@ -869,12 +872,12 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
     dt = _half(X.dtype, "X")
     code = _act(act)
     K, T = X.shape
-    device = X.device
+    device = X.get_device()
     if meta is not None and K % 64:
         _check("nm_matvec_act", 8)
     if _check_codes(codes, scales, rows, K // 2 if meta is not None else K, group) != dt:
         raise ValueError("scales and X must have the same dtype")
-    if codes.device != device:
+    if codes.get_device() != device:
         raise ValueError("codes and X must be on the same device")
     if meta is not None:
         _expect(meta, "meta", (-(-rows // 16), K // 64, 32), torch.int32, device)
@@ -990,7 +993,7 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     is 0.  What is None is left out; tokens outside the vocabulary are passed over."""
     dt = _dense_input(logits, "logits", int8=False)
     V, T = logits.shape
-    device = logits.device
+    device = logits.get_device()
     count = 0
     if tokens is not None:
         if starts is None:

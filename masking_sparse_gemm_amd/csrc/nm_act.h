@@ -311,39 +311,36 @@ template <int DT>
 __device__ __forceinline__ void group_finish(const GroupInputs& in, const float* slab,
                                              const Epilogue& ep, int64_t row0, int64_t col0, int64_t R,
                                              int64_t T, int lane) {
-  GroupInputs cur = in;
-  const int64_t col = col0 + 8 * (lane & 7), left = T - col;
-  int64_t row = row0 + (lane >> 3), i = row * T + col;
+  const int64_t row = row0 + (lane >> 3), col = col0 + 8 * (lane & 7), left = T - col;
   const float* sums = slab + (lane >> 3) * kSlabPitch + 8 * (lane & 7);
-#pragma unroll 1  // the activations' code once: cur's pieces move down instead
-  for (int k = 0; k < 4; ++k, row += 8, i += 8 * T, sums += 8 * kSlabPitch) {
-    if (row < R && left > 0) {
-      const float4_t a = *reinterpret_cast<const float4_t*>(sums);
-      const float4_t b = *reinterpret_cast<const float4_t*>(sums + 4);
-      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  float v[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(v[e], cur.scale[0], cur.bias[0]);
-      if constexpr (DT == kF32 || DT == kBF16 || DT == kF16)
-        if (ep.z) store_eight(ep.z, DT, i, left, v);
-      act_values(ep.act, v);
-      if (ep.residual) {
-        float x[8];
-        to_floats(cur.residual[0], y_type<DT>(ep), x);
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += x[e];
-      }
-      store_eight(ep.y, y_type<DT>(ep), i, left, v);
+    for (int h = 0; h < 2; ++h) {
+      const float4_t a = *reinterpret_cast<const float4_t*>(sums + 8 * k * kSlabPitch + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][4 * h + e] = __builtin_fmaf(a[e], in.scale[k], in.bias[k]);
     }
+  if (left <= 0) return;
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      cur.residual[j] = cur.residual[j + 1];
-      cur.scale[j] = cur.scale[j + 1];
-      cur.bias[j] = cur.bias[j + 1];
+  for (int k = 0; k < 4; ++k) {
+    if (row + 8 * k >= R) break;
+    const int64_t i = (row + 8 * k) * T + col;
+    if constexpr (DT == kF32 || DT == kBF16 || DT == kF16)
+      if (ep.z) store_eight(ep.z, DT, i, left, v[k]);
+    act_values(ep.act, v[k]);
+    if (ep.residual) {
+      float x[8];
+      to_floats(in.residual[k], y_type<DT>(ep), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] += x[e];
     }
+    store_eight(ep.y, y_type<DT>(ep), i, left, v[k]);
   }
 }
 
-// The slab's two groups; `first` are the first one's inputs.
+// The slab's two groups (their code once); `first` are the first one's inputs.
 template <int DT>
 __device__ __forceinline__ void slab_finish(const GroupInputs& first, const float* slab,
                                             const Epilogue& ep, int64_t row0, int64_t col0, int64_t R,
@@ -376,32 +373,17 @@ __device__ __forceinline__ void slab_write(const AccV (&a)[2], const AccV (&b)[2
 // keep it.
 __device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
 
-// Stores a wave's FM (2 or 4) blocks of 32 rows x 64 columns through its own kSlabBytes of LDS.
-template <int DT, int FM, typename AccV>
-__device__ __forceinline__ void finish_block(const AccV (&acc)[FM][2], uint8_t* lds,
-                                             const Epilogue& ep, int64_t row0, int64_t col0,
-                                             int64_t R, int64_t T, int lane) {
+// Stores a wave's 64 x 64 block through its own kSlabBytes of LDS.
+template <int DT, typename AccV>
+__device__ __forceinline__ void finish_block(const AccV (&acc)[2][2], uint8_t* lds, const Epilogue& ep,
+                                             int64_t row0, int64_t col0, int64_t R, int64_t T,
+                                             int lane) {
   float* slab = reinterpret_cast<float*>(lds);
-  AccV cur[FM][2];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int f = 0; f < 2; ++f) cur[i][f] = acc[i][f];
-#pragma unroll 1  // (as in group_finish)
-  for (int h = 0; h < FM / 2; ++h) {
-    GroupInputs in;
-    group_load<DT>(in, ep, row0 + 64 * h, col0, R, T, lane);
-    slab_write(cur[0], cur[1], slab, lane);
-    keep_order();
-    slab_finish<DT>(in, slab, ep, row0 + 64 * h, col0, R, T, lane);
-    keep_order();
-    if constexpr (FM == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) cur[i][f] = cur[i + 2][f];
-    }
-  }
+  GroupInputs in;
+  group_load<DT>(in, ep, row0, col0, R, T, lane);
+  slab_write(acc[0], acc[1], slab, lane);
+  keep_order();
+  slab_finish<DT>(in, slab, ep, row0, col0, R, T, lane);
 }
 
 // The same for a workgroup of four waves that hold 128 x 64 blocks each and four that do not: the
@@ -419,15 +401,6 @@ __device__ __forceinline__ void finish_half(uint8_t* smem, const Epilogue& ep, i
   group_load<DT>(in, ep, row0, col0, R, T, lane);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every block is in LDS
   slab_finish<DT>(in, slab_of(smem, wave), ep, row0, col0, R, T, lane);
-}
-
-// A wave's block of a product to its output, of either kind (DT: as above).
-template <int DT, int YT, typename AccV = float16v_t>
-__device__ __forceinline__ void store_out_128x64(const AccV (&acc)[4][2], uint8_t* lds,
-                                                 const typename OutOf<YT>::type& Y, int row0,
-                                                 int col0, int R, int T, int lane) {
-  if constexpr (YT == kAct) finish_block<DT, 4>(acc, lds, Y, row0, col0, R, T, lane);
-  else store_block_128x64<YT, AccV>(acc, lds, Y, row0, col0, R, T, lane);
 }
 
 }  // namespace

@@ -6,7 +6,7 @@
 // with the next step's loads in flight, no barrier and no LDS until their sums are joined there in wave
 // order.  Both operands come from memory as the structured-sparse instruction (v_smfmac_f32_16x16x64)
 // wants them: the compressed rows as they lie, and X from a transposed copy in which a lane's K are
-// contiguous, made by a first small launch.  fp8 and int8 become bf16 exactly on the way (int8 sums are
+// contiguous, made by a first small launch; one column needs none.  fp8 and int8 become bf16 exactly on the way (int8 sums are
 // exact: fp32 holds 1024 K of products of up to 2^14, then they move to int32).  1:2 places become
 // 2:4's by their bits, a 1:4 group a pair with a zero.  fp32, which has no sparse instruction, is
 // expanded in registers for v_mfma_f32_16x16x4_f32.
@@ -225,12 +225,14 @@ __device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t&
                                                      0);
 }
 
-// RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).
-template <int DT, int PAT, bool BLOCKED, bool RAGGED, int RG, int NT>
+// RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).  NT = 0: one column, X as it
+// lies, in each of the instruction's sixteen.
+template <int DT, int PAT, bool BLOCKED, bool RAGGED, int RG, int COLS>
 __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   typedef typename ThinElem<DT>::type E;
   typedef ThinRaw<DT, PAT> Raw;
-  constexpr bool kF = DT == kF32;
+  constexpr bool kF = DT == kF32, kOne = COLS == 0;
+  constexpr int NT = kOne ? 1 : COLS;
   constexpr int kRows = 16 * RG, kCols = 16 * NT;
   constexpr int kRowValues = PAT == kP14 ? 16 : 32, kRowMeta = PAT == kP24 ? 8 : 4;  // a row and step
   constexpr int kPitch = kCols + 4;  // of the sums in LDS
@@ -260,7 +262,21 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   constexpr int kMStep = (BLOCKED ? 16 : 1) * kRowMeta;
   constexpr int kPieces = kF ? 4 : 2;  // of X's copy to a lane, step and fragment
   const u32x4_t* x = static_cast<const u32x4_t*>(p.xt) + (t0 / 16 * steps) * (64 * kPieces) + lane;
+  const E* column = static_cast<const E*>(p.xt);
 
+  const auto one_column = [](const E* k, int q, int i) {  // piece i of the lane, as the copy has it
+    if constexpr (kF) return *reinterpret_cast<const u32x4_t*>(k + 16 * q + 4 * i);
+    else if constexpr (sizeof(E) == 2) return *reinterpret_cast<const u32x4_t*>(k + 32 * i + 8 * q);
+    else {
+      const u32x2_t raw = *reinterpret_cast<const u32x2_t*>(k + 32 * i + 8 * q);
+      u32x4_t h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        h[e] = to_half<DT>((raw[e / 2] >> (16 * (e & 1))) & 0xFFu) |
+               to_half<DT>((raw[e / 2] >> (16 * (e & 1) + 8)) & 0xFFu) << 16;
+      return h;
+    }
+  };
   struct Step {
     Raw a[RG];
     u32x4_t b[NT][kPieces];
@@ -274,9 +290,14 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const u32x4_t* at = x + ((int64_t)t * steps + s) * (64 * kPieces);
+      if constexpr (kOne) {
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) f.b[t][i] = at[64 * i];
+        for (int i = 0; i < kPieces; ++i) f.b[t][i] = one_column(column + 64 * (int64_t)s, q, i);
+      } else {
+        const u32x4_t* at = x + ((int64_t)t * steps + s) * (64 * kPieces);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) f.b[t][i] = at[64 * i];
+      }
     }
   };
   float4_t acc[RG][NT];
@@ -393,11 +414,14 @@ template <int DT, int PAT, bool BLOCKED, bool RAGGED>
 hipError_t launch_cols(const ThinArgs& p, const ThinPlan& plan, hipStream_t s) {
   const auto go = [&](auto rg, auto nt) {
     constexpr int RG = decltype(rg)::value, NT = decltype(nt)::value;
-    const dim3 grid((unsigned)((p.R + 16 * RG - 1) / (16 * RG)), (unsigned)(plan.Tp / (16 * NT)));
+    const unsigned cols = NT == 0 ? 1u : (unsigned)(plan.Tp / (16 * (NT == 0 ? 1 : NT)));
+    const dim3 grid((unsigned)((p.R + 16 * RG - 1) / (16 * RG)), cols);
     thin_kernel<DT, PAT, BLOCKED, RAGGED, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, 1> One;
+  if constexpr (!RAGGED)
+    if (p.T == 1) return go(One{}, std::integral_constant<int, 0>{});
   typedef std::integral_constant<int, 2> Two;
   if (plan.nt == 1) return go(One{}, One{});
   if (plan.nt == 2 || DT == kF32) return go(Two{}, Two{});
@@ -405,12 +429,16 @@ hipError_t launch_cols(const ThinArgs& p, const ThinPlan& plan, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t launch_thin_as(const ThinArgs& p, const ThinPlan& plan, int pat, bool blocked, const void* X,
+hipError_t launch_thin_as(ThinArgs p, const ThinPlan& plan, int pat, bool blocked, const void* X,
                           void* xt, hipStream_t s) {
-  const TurnArgs turn{X, p.K, p.T, p.Tp, xt};
-  turn_kernel<DT><<<dim3((unsigned)((p.K + 63) / 64), (unsigned)((p.Tp + 63) / 64)), 256, 0, s>>>(turn);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (p.T == 1 && p.K % 64 == 0) {
+    p.xt = X;
+  } else {
+    const TurnArgs turn{X, p.K, p.T, p.Tp, xt};
+    turn_kernel<DT><<<dim3((unsigned)((p.K + 63) / 64), (unsigned)((p.Tp + 63) / 64)), 256, 0, s>>>(turn);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const auto go = [&](auto pattern) {
     constexpr int PAT = decltype(pattern)::value;
     if (blocked) return launch_cols<DT, PAT, true, false>(p, plan, s);

@@ -126,16 +126,19 @@ struct ThinPlan {
   }
 };
 
-// Estimated time of the tiled kernels on the same product: a tile's steps alone where there are few
-// tiles, the rate where there are many.  Measured alone, us a step of 64 K: 2:4 and 1:2 in 16 bits
-// 0.49, in 8 bits 0.22, expanded 16 and 8 bits 1.45, fp32 5.25.
+// Estimated time (us) of the tiled kernels on the same product: a tile's steps alone where there are few
+// tiles, a flow of tiles over the units where there are many.  Measured: 2:4 and 1:2 in 16 bits 4096 x
+// 1024, 8 columns 15.5, 4096 x 4096 38.9, with 1024 columns 41, 8192 x 4096 40.7, 262144 x 256, 8
+// columns 39; in 8 bits 4096 x 4096 24, 8192 x 4096, 1024 columns 32; expanded in 16 bits 100 and 128,
+// in fp32 342 and 594.
 inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
-  const double S = (double)((K + 63) / 64), work = 2.0 * (double)R * (double)K * (double)T;
+  const double S = (double)((K + 63) / 64);
   const bool sparse = ((n == 2 && m == 4) || (n == 1 && m == 2)) && K % 64 == 0;
-  if (elem == 4) return std::max(5.3 + 5.25 * S, 5 + work / 0.115e9);
-  if (!sparse || (elem == 1 && K % 128 != 0)) return std::max(7 + 1.45 * S, 5 + work / 0.54e9);
-  if (elem == 1) return std::max(9.7 + 0.22 * S, 6 + work / 3.0e9);
-  return std::max(7.2 + 0.49 * S, 5 + work / 1.6e9);
+  const double tiles = (double)((R + 127) / 128) * (double)((T + 127) / 128);
+  if (elem == 4) return std::max(5.3 + 5.25 * S, tiles / 512 * (5 + 9.2 * S));
+  if (!sparse || (elem == 1 && K % 128 != 0)) return std::max(7 + 1.45 * S, tiles / 512 * (5 + 1.9 * S));
+  if (elem == 1) return std::max(9.7 + 0.22 * S, tiles / 512 * (6 + 0.2 * S));
+  return std::max(7.2 + 0.49 * S, tiles / 256 * (3.9 + 0.25 * S));
 }
 
 // Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).

@@ -83,6 +83,28 @@ def test_sizes(R, K, T, layout):
     run(R, K, T, 2, 4, "bf16", layout, "gelu", True, True, True, "bf16")
 
 
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4), (4, 8)])
+@pytest.mark.parametrize("layout", ["rows", "blocked"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32", "int8", "fp8"])
+@pytest.mark.parametrize("R,K", [(70, 640), (1100, 2048)])
+def test_one_token(n, m, layout, dtype, R, K):
+    run(R, K, 1, n, m, dtype, layout, "gelu", True, True, dtype not in EIGHT,
+        "fp32" if dtype in EIGHT else dtype)
+
+
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32", "int8", "fp8"])
+@pytest.mark.parametrize("K", [8, 72, 148, 1020])
+def test_few_tokens_of_every_type_and_any_width(n, m, dtype, K):
+    run(45, K, 20, n, m, dtype, "rows", "silu", True, False, False, "fp32" if dtype in EIGHT else dtype)
+
+
+def test_bytes_without_a_scale():
+    values, meta, X, W, Xd = inputs(40, 128, 24, 2, 4, "int8", "blocked")
+    Y = nm.spmm_act(values, meta, X, out_dtype=torch.float32, layout="blocked", rows=40)
+    assert torch.equal(Y.double().cpu(), W @ Xd)  # whole numbers below 2^24
+
+
 @pytest.mark.parametrize("K", [4, 20, 100, 1004])
 @pytest.mark.parametrize("T", [1, 2, 9, 64])
 def test_row_layout_of_any_width(K, T):
