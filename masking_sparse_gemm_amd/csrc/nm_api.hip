@@ -844,7 +844,7 @@ nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, 
                      {Z, act != NM_ACT_NONE ? R * T * 2 : 0},
                      {dY, R * T * 2}};
   if (any_alias(r, 5, 10)) return NM_ERR_ALIAS;
-  if (R * K + R * T + K * T == 0) return NM_OK;
+  if (R * K + R * T + K * T == 0 && (R == 0 || dbias == nullptr)) return NM_OK;
   if ((st = check_device()) != NM_OK) return st;
   const nm::SpmmGradCall c{values, meta, R, K, n, m, layout == NM_LAYOUT_BLOCKED, X, T, dt == NM_BF16,
                            (int)act, Z, dY, dW, dX, dbias, dZ};

@@ -73,6 +73,18 @@ def test_no_tokens_give_zeros():
     assert bool((dW == 0).all()) and dX.shape == (64, 0) and bool((db == 0).all())
 
 
+def test_neither_tokens_nor_columns_nor_rows():
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    torch.full((7,), 9.0, device="cuda")  # (what an allocation may find)
+    (db,) = nm.spmm_act_grad(None, None, None, torch.zeros(7, 0, **bf), want=("dbias",))
+    dW, db2 = nm.spmm_act_grad(None, None, torch.zeros(0, 0, **bf), torch.zeros(7, 0, **bf),
+                               want=("dW", "dbias"))
+    assert db.tolist() == [0.0] * 7 == db2.tolist() and dW.shape == (7, 0)
+    values, meta = nm.compress(torch.zeros(0, 64, **bf), 2, 4)
+    dW, dX, db = nm.spmm_act_grad(values, meta, torch.ones(64, 5, **bf), torch.zeros(0, 5, **bf))
+    assert dW.shape == (0, 64) and bool((dX == 0).all()) and db.shape == (0,)
+
+
 def test_infinite_columns_stay_where_they_are():
     """Z of +-infinity has slope 1 or 0; a masked (relu) entry of dY may hold anything."""
     Z = torch.tensor([[math.inf, -math.inf, 1e30, -1e30, 0.0]]).to(torch.bfloat16).cuda()
