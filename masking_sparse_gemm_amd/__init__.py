@@ -913,15 +913,15 @@ class _Tensors:
             raise ValueError("no tensors")
         # (a step of a model has hundreds of tensors, and a look at one costs more than its clipping)
         dts = [_FLOAT_DT.get(g.dtype) for g in grads]
-        self.contiguous = all([g.is_contiguous() for g in grads])
-        devices = set([g.get_device() for g in grads])
+        self.contiguous = all(map(torch.Tensor.is_contiguous, grads))
+        devices = set(map(torch.Tensor.get_device, grads))
         if None in dts or len(devices) != 1 or min(devices) < 0 or not (self.contiguous or all(
                 g.is_contiguous() or (g.dim() == 2 and g.t().is_contiguous()) for g in grads)):
-            raise ValueError("gradients must be float32, float16 or bfloat16 tensors without gaps on "
-                             "one GPU")
+            raise ValueError("gradients must be contiguous (or transposed matrices), float32, float16 "
+                             "or bfloat16, on one GPU")
         self.device = devices.pop()
-        self.pointers = array.array("q", [g.data_ptr() for g in grads])
-        self.counts = array.array("q", [g.numel() for g in grads])
+        self.pointers = array.array("q", list(map(torch.Tensor.data_ptr, grads)))
+        self.counts = array.array("q", list(map(torch.Tensor.numel, grads)))
         self.dts = array.array("i", dts)
 
     def addresses(self):
@@ -945,8 +945,8 @@ def grad_norm(grads) -> torch.Tensor:
     ptrs, counts, dts, n = t.addresses()
     L = lib()
     ws, ws_ptr = _workspace(like, L.nm_grad_norm_workspace_bytes(counts, n))
-    _launch("nm_grad_norm", like, ptrs, counts, dts, n, norm.data_ptr(), ws_ptr,
-                                          0 if ws is None else ws.numel())
+    _launch("nm_grad_norm", like,
+        ptrs, counts, dts, n, norm.data_ptr(), ws_ptr, 0 if ws is None else ws.numel())
     return norm
 
 

@@ -23,19 +23,21 @@ namespace nm {
 namespace {
 
 constexpr int kTable = 112;       // tensors a launch: the arguments stay below 4 KB
+constexpr int kSmallTable = 32;   // of a call with no more
 constexpr int kPieces = 8;        // of 16 bytes to a work-item and chunk, all of them in flight at once
 constexpr int kChunkBytes = 256 * 16 * kPieces;
 constexpr int kMostGroups = 2048;
 
+template <int N>
 struct TensorTable {
-  const void* in[kTable];
-  void* out[kTable];
-  int64_t count[kTable];
-  uint32_t first[kTable + 1];  // chunk that a tensor begins with
-  int dt[kTable];
+  const void* in[N];
+  void* out[N];
+  int64_t count[N];
+  uint32_t first[N + 1];  // chunk that a tensor begins with
+  int dt[N];
   int tensors;
 };
-static_assert(sizeof(TensorTable) < 3900, "kernel arguments");
+static_assert(sizeof(TensorTable<kTable>) < 3900, "kernel arguments");
 
 template <int DT>
 struct ClipElem {
@@ -97,8 +99,8 @@ __device__ __forceinline__ void by_type(int dt, F&& f) {
 
 // Calls f(tensor, first entry, entries left in the tensor) for chunks blockIdx.x, + gridDim.x, ..., or
 // for the same counted from the last one.
-template <bool BACK, typename F>
-__device__ __forceinline__ void each_chunk(const TensorTable& t, F&& f) {
+template <bool BACK, int N, typename F>
+__device__ __forceinline__ void each_chunk(const TensorTable<N>& t, F&& f) {
   const uint32_t all = t.first[t.tensors];
   int i = BACK ? t.tensors - 1 : 0;
   for (uint32_t n = blockIdx.x; n < all; n += gridDim.x) {
@@ -127,7 +129,8 @@ __device__ __forceinline__ double add_group(double v, double* part) {
   return (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-__global__ void __launch_bounds__(256) square_kernel(TensorTable t, double* __restrict__ sums) {
+template <int N>
+__global__ void __launch_bounds__(256) square_kernel(TensorTable<N> t, double* __restrict__ sums) {
   __shared__ double part[4];
   double total = 0;
   each_chunk<false>(t, [&](int i, int64_t at, int64_t left) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(256) square_kernel(TensorTable t, double* __re
         for (int j = 0; j < kPer; ++j) s = __builtin_fmaf(number<DT>(r, j), number<DT>(r, j), s);
         if (s >= 0x1p-100f && s < INFINITY) {  // then no square that counts left fp32's range
           total += (double)s;
-        } else {
+        } else if (((DT == kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu) & (r[0] | r[1] | r[2] | r[3])) != 0u) {
 #pragma unroll 1
           for (int j = 0; j < kPer; ++j) {
             double v = 0;  // (an index that is no constant would put r into memory)
@@ -168,8 +171,9 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) *norm = n;
 }
 
+template <int N>
 __global__ void __launch_bounds__(256)
-    clip_kernel(TensorTable t, const double* __restrict__ sums, int count,
+    clip_kernel(TensorTable<N> t, const double* __restrict__ sums, int count,
                 const float* __restrict__ given, float max_norm, float* __restrict__ norm) {
   __shared__ double part[4];
   const float n = given ? *given : norm_of(sums, count, part);
@@ -221,11 +225,11 @@ int64_t most_groups(int64_t tables) {
   return tables > 0 ? std::max<int64_t>(256, kMostGroups / tables) : 0;
 }
 
-// Calls f(table, workgroups) for each table in turn.
-template <typename F>
+// Calls f(table, workgroups) for each table of N in turn.
+template <int N, typename F>
 hipError_t each_table(const void* const* grads, void* const* outs, const int64_t* counts,
                       const int* dts, int64_t tensors, int64_t most, F&& f) {
-  TensorTable t;
+  TensorTable<N> t;
   t.tensors = 0;
   t.first[0] = 0;
   const auto flush = [&]() {
@@ -243,7 +247,7 @@ hipError_t each_table(const void* const* grads, void* const* outs, const int64_t
     t.count[t.tensors] = counts[i];
     t.dt[t.tensors] = dts[i];
     t.first[t.tensors + 1] = t.first[t.tensors] + (uint32_t)chunks_of(counts[i], dts[i]);
-    if (++t.tensors == kTable) e = flush();
+    if (++t.tensors == N) e = flush();
   }
   return e == hipSuccess ? flush() : e;
 }
@@ -255,31 +259,44 @@ size_t norm_workspace_bytes(const int64_t* counts, int64_t tensors) {
   return (size_t)(tables * most_groups(tables)) * sizeof(double);
 }
 
-hipError_t launch_clip(const void* const* grads, void* const* outs, const int64_t* counts,
-                       const int* dts, int64_t tensors, float max_norm, const float* given,
-                       float* norm, void* workspace, hipStream_t s) {
-  const int64_t tables = tables_of(counts, tensors), most = most_groups(tables);
-  double* sums = static_cast<double*>(workspace);
+namespace {
+template <int N>
+hipError_t clip_tables(const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int* dts, int64_t tensors, int64_t most, float max_norm,
+                       const float* given, float* norm, double* sums, hipStream_t s) {
   int parts = 0;
   hipError_t e = hipSuccess;
   if (!given) {
-    e = each_table(grads, nullptr, counts, dts, tensors, most, [&](const TensorTable& t, unsigned groups) {
-      square_kernel<<<groups, 256, 0, s>>>(t, sums + parts);
+    e = each_table<N>(grads, nullptr, counts, dts, tensors, most,
+                      [&](const TensorTable<N>& t, unsigned groups) {
+      square_kernel<N><<<groups, 256, 0, s>>>(t, sums + parts);
       parts += (int)groups;
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    if (!outs || tables == 0) {
+    if (!outs || most == 0) {
       norm_kernel<<<1, 256, 0, s>>>(sums, parts, norm);
       return hipGetLastError();
     }
   }
   float* write = given ? nullptr : norm;  // by the first table's kernel
-  return each_table(grads, outs, counts, dts, tensors, most, [&](const TensorTable& t, unsigned groups) {
-    clip_kernel<<<groups, 256, 0, s>>>(t, sums, parts, given, max_norm, write);
+  return each_table<N>(grads, outs, counts, dts, tensors, most,
+                       [&](const TensorTable<N>& t, unsigned groups) {
+    clip_kernel<N><<<groups, 256, 0, s>>>(t, sums, parts, given, max_norm, write);
     write = nullptr;
     return hipGetLastError();
   });
+}
+}  // namespace
+
+hipError_t launch_clip(const void* const* grads, void* const* outs, const int64_t* counts,
+                       const int* dts, int64_t tensors, float max_norm, const float* given,
+                       float* norm, void* workspace, hipStream_t s) {
+  const int64_t most = most_groups(tables_of(counts, tensors));
+  double* sums = static_cast<double*>(workspace);
+  return tensors <= kSmallTable
+             ? clip_tables<kSmallTable>(grads, outs, counts, dts, tensors, most, max_norm, given, norm, sums, s)
+             : clip_tables<kTable>(grads, outs, counts, dts, tensors, most, max_norm, given, norm, sums, s);
 }
 
 }  // namespace nm

@@ -123,6 +123,18 @@ def test_mixed_magnitudes():
         check_norm(nm.grad_norm([t.cuda()]), exact_norm([t]))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_rows_of_zeros(dtype):
+    """A gradient of an embedding: few rows in use; zeros of either sign, and a subnormal among them."""
+    g = torch.zeros(300, 128, dtype=dtype)
+    g[::2] = -0.0
+    tiny = torch.finfo(dtype).smallest_normal / 2
+    g[7, 5] = tiny
+    check_norm(nm.grad_norm([g.cuda()]), exact_norm([g]))
+    g[41] = torch.randn(128)
+    check_norm(nm.grad_norm([g.cuda()]), exact_norm([g]))
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 def test_a_norm_that_is_no_number_changes_nothing(bad):
     grads = tensors([(1000,), (50,)])
