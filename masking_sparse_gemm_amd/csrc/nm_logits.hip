@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
   }
   __syncthreads();
   if constexpr (HISTORY == 1) {
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 6;
     const int lane = tid & 63, wave = tid >> 6, waves = threads >> 6;
     // a text's frequent words would have a wave's lanes wait for one another: several copies of the
     // counts, and a column's words on banks of their own
@@ -216,33 +216,42 @@ __global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
 
 int64_t table_bytes(int64_t V, int64_t T) { return V * T * 4; }
 
-// Columns: 32, whose 128 bytes (fp32) of a row are a whole line, or what there are, to a power of two.
-// Entries: as many as fit, since every workgroup reads its columns' tokens (50257 x 64: 8192 a
-// workgroup 18 us, 4096 25, 1024 80), but few enough that all 256 units have a workgroup.
+// Columns: 32, whose 128 bytes (fp32) of a row are a whole line, or what there are, to a power of two;
+// 16 where tokens are counted in LDS, whose readers are then half as many (50257 x 64, 96,000 tokens
+// 20.7 -> 18.0 us, 128000 x 32, 64,000 tokens 25.7 -> 19.6; through the table 28.5 -> 32.7).
+// Entries: as many as fit, since every workgroup reads its columns' tokens (50257 x 64 by 32 columns:
+// 8192 a workgroup 18 us, 4096 25, 1024 80), but few enough that most of the 256 units have a workgroup.
+// Work-items: eight entries each, but all 1024 where there are tokens for them (5000 x 8, 32,000
+// tokens 15.2 -> 8.6).
 LogitsPlan::LogitsPlan(int64_t V, int64_t T, int64_t count) {
-  log_cols = 0;
-  while (log_cols < 5 && ((int64_t)1 << log_cols) < T) ++log_cols;
-  const int64_t cols = (int64_t)1 << log_cols;
-  blocks_t = (T + cols - 1) / cols;
-  const int least = std::max(8, 5 + log_cols);  // whole words of the mask
-  for (log_cells = 13; log_cells > least; --log_cells) {
+  const auto cut = [&](int most) {
+    log_cols = 0;
+    while (log_cols < most && ((int64_t)1 << log_cols) < T) ++log_cols;
+    const int64_t cols = (int64_t)1 << log_cols;
+    blocks_t = (T + cols - 1) / cols;
+    const int least = std::max(8, 5 + log_cols);  // whole words of the mask
+    for (log_cells = 13; log_cells > least; --log_cells) {
+      const int64_t words = ((int64_t)1 << log_cells) / cols;
+      if ((V + words - 1) / words * blocks_t >= 224) break;
+    }
     const int64_t words = ((int64_t)1 << log_cells) / cols;
-    if ((V + words - 1) / words * blocks_t >= 256) break;
-  }
-  const int64_t words = ((int64_t)1 << log_cells) / cols;
-  blocks_v = (V + words - 1) / words;
-  copies = std::min(16, kMostCells >> log_cells);
-  const int64_t each = count / std::max<int64_t>(1, T);  // tokens of a column
-  if (each <= 512) copies = 1;
-  threads = each > 4096 ? kMostThreads : std::max(256, (1 << log_cells) / kEach);
+    blocks_v = (V + words - 1) / words;
+  };
+  cut(T < (int64_t)1 << 19 ? 4 : 5);  // (a grid has 65535 columns at most)
   // In LDS each of blocks_v workgroups reads a column's tokens, as fast as the caches give them to the
   // units that work; through the table they are read once, and the table is written and read, with two
   // more launches.  `count` is the room for tokens, of which a part is in use.  Measured, us in LDS /
-  // through the table: 32000 words, one column of 2000 tokens 5.2 / 9.9, of 100,000 19.7 / 12.5; 50257 x
-  // 64, 48,000 tokens 18 / 22, 256,000 62 / 28, 1,000,000 205 / 40; 128000 x 256 with few 63 / 91.
+  // through the table: 32000 words, one column of 2000 tokens 5.4 / 10.1, of 100,000 19.8 / 12.3; 32000
+  // x 8, 16,000 tokens 7.2 / 10.8, 160,000 25 / 14.5; 50257 x 64, 96,000 tokens 15.7 / 22, 512,000 34 /
+  // 29, 2,000,000 99 / 41; 128000 x 256, 256,000 tokens 88 / 98, 1,000,000 124 / 108.
   const double share = std::min(1.0, (double)(blocks_v * blocks_t) / 256), cells = (double)V * (double)T;
   const double in_lds = 3 + 0.45e-6 * cells + (double)blocks_v * (double)count * 8 / (24e6 * share);
-  table = in_lds > 8 + 1.1e-6 * cells;
+  table = count > 0 && in_lds > 8 + 1.1e-6 * cells;
+  if (table || count == 0) cut(5);
+  copies = std::min(16, kMostCells >> log_cells);
+  const int64_t each = count / std::max<int64_t>(1, T);  // tokens of a column
+  if (each <= 512) copies = 1;
+  threads = each > 512 ? kMostThreads : std::max(256, (1 << log_cells) / kEach);
 }
 
 template <int DT>
