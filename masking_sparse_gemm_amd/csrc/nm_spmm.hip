@@ -2503,8 +2503,8 @@ hipError_t run_smfmac(const void* values, const uint32_t* meta, int64_t R, int64
       return launch_tile<BF16, kPat12, kBlocked, YT, 2, 256, 128, 2, 2, 4, 4, 4>(values, meta, R,
                                                                                 K, X, T, Y, s);
   }
-  // (256 x 256 tiles have no registers left for an epilogue: 16384 x 64, 1000 columns 23 us against 18
-  // in 256 x 128)
+  // (256 x 256 tiles have no registers left for an epilogue: 16384 x 64, 1000 columns 23 us against
+  // 19.5 in 256 x 128)
   switch (pick_tile(R, K, T, YT == kAct ? 1 : 0)) {
     case 0:
       if constexpr (YT != kAct)
