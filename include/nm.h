@@ -437,8 +437,8 @@ typedef enum NM_INT_ENUM {
  * y_dt is dt or NM_F32, and for NM_I8 and NM_FP8 one of NM_F32, NM_F16 and NM_BF16.  Sums as nm_spmm
  * forms them (NM_I8: K < 2^17, exact, then one rounding to fp32).  K = 0 gives Z = b.
  * workspace: nm_spmm_act_workspace_bytes(R, K, n, m, T, dt) bytes of device memory, whose contents do
- * not matter: room for a copy of X where tokens are few or X's rows are not whole 16-byte pieces, else
- * 0. */
+ * not matter: room for a copy of X where X's rows are not whole 16-byte pieces or many workgroups read a
+ * few tokens, else 0. */
 size_t nm_spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, nm_dtype dt);
 nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                       nm_layout layout, const void* X, int64_t T, nm_dtype dt, const float* scale,

@@ -329,11 +329,11 @@ def _check_compressed(values: torch.Tensor, meta: torch.Tensor, n: int, m: int, 
         if values.dim() != 4 or values.shape[0] != (R + 15) // 16:
             raise ValueError(f"blocked values must be ({(R + 15) // 16}, S, 16, V) for R={R}")
     vshape, mshape = compressed_shapes(R, K, n, m, layout)
-    if tuple(values.shape) != tuple(vshape):
+    if values.shape != vshape:
         raise ValueError(f"values must be {tuple(vshape)} for K={K}, {n}:{m}, {layout}")
-    if meta.dtype != torch.int32 or tuple(meta.shape) != tuple(mshape) or not meta.is_contiguous():
+    if meta.dtype != torch.int32 or meta.shape != mshape or not meta.is_contiguous():
         raise ValueError(f"meta must be a contiguous int32 {tuple(mshape)} tensor")
-    if meta.device != values.device:
+    if meta.get_device() != values.get_device():
         raise ValueError("values and meta must be on the same device")
     return _DT[values.dtype], R
 

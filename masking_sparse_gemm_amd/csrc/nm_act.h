@@ -3,7 +3,8 @@
 //
 // All of it is fp32 on the product's fp32 (int8: int32) sums, rounded once where Z and Y are stored.
 // Exponentials and reciprocals are the hardware's (v_exp_f32, v_rcp_f32: one unit in the last place),
-// so a sigmoid takes four instructions and the epilogue's arithmetic hides under its memory traffic.
+// so a sigmoid takes four instructions and the epilogue's arithmetic hides under its memory traffic
+// (bf16 11008 x 4096, 2048 columns: the product alone 105 us, with bias and silu, Z kept, 119-123).
 #pragma once
 
 #include "nm_launch.h"
@@ -388,7 +389,8 @@ __device__ __forceinline__ void finish_block(const AccV (&acc)[2][2], uint8_t* l
 
 // The same for a workgroup of four waves that hold 128 x 64 blocks each and four that do not: the
 // blocks go to LDS whole, and all eight waves finish half of one each, since the activation's
-// arithmetic would keep four waves longer than their stores.  Wave w has block w % 4 and half w / 4.
+// arithmetic would keep four waves longer than their stores (bf16 11008 x 4096, 2048 columns, silu,
+// Z kept: 175 us a call with four, 139 with eight).  Wave w has block w % 4 and half w / 4.
 constexpr int kBlockBytes = 2 * kSlabBytes;
 __device__ __forceinline__ float* slab_of(uint8_t* smem, int wave) {
   return reinterpret_cast<float*>(smem + (wave & 3) * kBlockBytes + (wave >> 2) * kSlabBytes);

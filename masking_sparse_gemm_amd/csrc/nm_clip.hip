@@ -3,15 +3,16 @@
 //   norm = sqrt(sum over all tensors and entries of g^2),   out = g min(1, max_norm / norm)
 //
 // The tensors' addresses and sizes travel as kernel arguments, kTable of them a launch, so nothing is
-// copied to the device and a captured graph keeps them.  Entries are taken in chunks of 32 KB; a
-// workgroup has a run of chunks, so it looks its tensor up once and walks on from there.  Squares are
+// copied to the device and a captured graph keeps them.  Entries are taken in chunks of 32 KB, by
+// workgroups in turn, each of which walks on through the tensors from its last chunk.  Squares are
 // added eight at a time in fp32 and then in fp64 (all in fp64 where eight squares leave fp32's range),
 // and the workgroups' sums are joined in a fixed order by every workgroup of the second pass: two
 // launches for up to kTable tensors.
 //
 // Bound by memory, the first pass by reads, the second by a read and a write.  The second pass takes
 // the chunks last first, since what the first pass read last is still in the 256 MB cache, and writes
-// past the caches, so that it stays there (405 M bf16 gradients 442 -> 423 us, 42 M in fp32 86 -> 81).
+// past the caches, so that it stays there (405 M bf16 gradients 442 -> 423 us, 128 of them the first pass
+// at 6.3 TB/s, 294 the second at 5.5; 42 M in fp32 86 -> 81).
 // Workgroups side by side have chunks side by side: a run of chunks to a workgroup took 498 us.
 #include <algorithm>
 #include <type_traits>

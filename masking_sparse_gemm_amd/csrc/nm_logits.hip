@@ -11,6 +11,8 @@
 // LDS; every workgroup of a column reads that column's tokens again, from cache.  Long histories: the
 // counts go through a table in the workspace (cleared, counted with atomics, read by the pass); integer
 // sums come out the same in any order.  Either way bit 31 of a count stands for a word of the prompt.
+// fp32 50257 x 64 with 96,000 tokens 15.7 us, of which reading and counting them is 5 (the logits alone
+// are 5 at a copy's rate; all workgroups are there at once, so loads and stores do not overlap).
 #include <algorithm>
 
 #include "nm_grid.h"

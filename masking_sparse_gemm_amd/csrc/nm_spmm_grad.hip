@@ -10,7 +10,12 @@
 // groups run along its rows), so W is decompressed and both products are dense (nm_gemm.h).
 //
 // What the products need (dZ, X and W in whole steps) goes out in one launch where W is small, and both
-// products in one, dX's long sums first: alone, each leaves units idle at its end.
+// products in one, dX's long sums first: alone, each leaves units idle at its end (1000 x 768, 333
+// columns: 30 us a call in launches of their own, 21 so).
+//
+// Bound by the matrix cores where matrices are large: bf16 11008 x 4096, 2048 columns, dZ 25.6 us and W
+// 24.8, both at the memory's rate, the products 328-336 (1100-1130 TFLOP/s; a library's product of 8192^3
+// on the same card 1215).  By launches where they are small: 6.9 and 9.9 us for 1000 x 768, 333 columns.
 #include <algorithm>
 
 #include "nm_act.h"
@@ -426,8 +431,8 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
 
 size_t spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, int dt) {
   if (thin_preferred(R, K, n, m, T, elem_of(dt))) {
-    if (T == 1 && K % 64 == 0) return 0;  // X as it lies
-    return (size_t)(ThinPlan(R, K, T, dt == kF32).Tp * pad64(K) * (dt == kF32 ? 4 : 2));
+    const ThinPlan plan(R, K, T, dt == kF32);
+    return plan.direct ? 0 : (size_t)(plan.Tp * pad64(K) * (dt == kF32 ? 4 : 2));
   }
   const int64_t ldx = whole_row(T, dt);
   return ldx == T ? 0 : (size_t)whole256(K * ldx * elem_of(dt));

@@ -6,12 +6,15 @@
 // with the next step's loads in flight, no barrier and no LDS until their sums are joined there in wave
 // order.  Both operands come from memory as the structured-sparse instruction (v_smfmac_f32_16x16x64)
 // wants them: the compressed rows as they lie, and X from a transposed copy in which a lane's K are
-// contiguous, made by a first small launch; one column needs none.  fp8 and int8 become bf16 exactly on the way (int8 sums are
+// contiguous, made by a first small launch; where few workgroups read X, they load its numbers one by
+// one instead, and one column as it lies.  fp8 and int8 become bf16 exactly on the way (int8 sums are
 // exact: fp32 holds 1024 K of products of up to 2^14, then they move to int32).  1:2 places become
 // 2:4's by their bits, a 1:4 group a pair with a zero.  fp32, which has no sparse instruction, is
 // expanded in registers for v_mfma_f32_16x16x4_f32.
 //
-// Bound by the first loads' latency on small matrices and by the reads of W on large ones.
+// Bound by the first loads' latency on small matrices and by the reads of W on large ones: bf16, one
+// column, 1024 x 4096 5.1 us, 4096 x 4096 6.2, 8192 x 4096 8.5 (4.4 TB/s of W; the tiled kernels take 41
+// for the middle one); 1000 x 1024, 517 columns 9.4 and 4.1 for X's copy, against 53 in tiles.
 #include <algorithm>
 #include <type_traits>
 
@@ -225,9 +228,10 @@ __device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t&
                                                      0);
 }
 
-// RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).  NT = 0: one column, X as it
-// lies, in each of the instruction's sixteen.
-template <int DT, int PAT, bool BLOCKED, bool RAGGED, int RG, int COLS>
+// RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).  DIRECT: xt is X itself, whose
+// numbers are loaded one by one.  COLS = 0: one column, X as it lies, in each of the instruction's
+// sixteen.
+template <int DT, int PAT, bool BLOCKED, bool RAGGED, bool DIRECT, int RG, int COLS>
 __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   typedef typename ThinElem<DT>::type E;
   typedef ThinRaw<DT, PAT> Raw;
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int steps = (int)((p.K + 63) / 64);
-  static_assert(!(BLOCKED && RAGGED), "blocks are whole steps");
+  static_assert(!(RAGGED && (BLOCKED || DIRECT)), "blocks are whole steps, a copy ends in zeros");
   const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kCols;
   const int64_t groups = (p.R + 15) / 16;
 
@@ -277,9 +281,32 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
       return h;
     }
   };
+  // DIRECT: number e of the lane's piece i is in row kPieceRows i + e of the step, from the quarter's on;
+  // columns past the last one are the last one again, and not stored
+  constexpr int kEach = kF ? 4 : 8, kPieceRows = kF ? 4 : 32;
+  uint32_t direct[NT];
+  if constexpr (DIRECT) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      direct[t] = (uint32_t)((kF ? 16 : 8) * q * p.T + min(t0 + 16 * t + l16, p.T - 1));
+  }
   struct Step {
     Raw a[RG];
-    u32x4_t b[NT][kPieces];
+    u32x4_t b[DIRECT ? 1 : NT][kPieces];
+    uint32_t one[DIRECT ? NT : 1][DIRECT ? 16 : 1];
+  };
+  const auto piece = [&](const Step& f, int t, int i) {
+    if constexpr (DIRECT) {
+      u32x4_t w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kF) w[e] = f.one[t][4 * i + e];
+        else w[e] = to_half<DT>(f.one[t][8 * i + 2 * e]) | to_half<DT>(f.one[t][8 * i + 2 * e + 1]) << 16;
+      }
+      return w;
+    } else {
+      return f.b[t][i];
+    }
   };
   const auto load = [&](Step& f, int s) {
 #pragma unroll
@@ -290,7 +317,17 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if constexpr (kOne) {
+      if constexpr (DIRECT) {
+        const E* at = column + 64 * (int64_t)s * p.T;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            const E* row = at + (kPieceRows * i + e) * p.T;
+            if constexpr (kF) f.one[t][kEach * i + e] = __float_as_uint(row[direct[t]]);
+            else f.one[t][kEach * i + e] = row[direct[t]];
+          }
+      } else if constexpr (kOne) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) f.b[t][i] = one_column(column + 64 * (int64_t)s, q, i);
       } else {
@@ -315,6 +352,11 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   for (int s = wave; s < steps; s += kThinWaves) {
     const Step cur = next;
     if (s + kThinWaves < steps) load(next, s + kThinWaves);
+    u32x4_t b[NT][kPieces];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) b[t][i] = piece(cur, t, i);
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       if constexpr (kF) {
@@ -324,14 +366,14 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
         for (int k = 0; k < 16; ++k)  // K 16 q + k in lane quarter q
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k], __uint_as_float(cur.b[t][k / 4][k % 4]),
+            acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k], __uint_as_float(b[t][k / 4][k % 4]),
                                                              acc[g][t], 0, 0, 0);
       } else {
         uint32_t ix;
         const u32x4_t a = cur.a[g].operand(ix);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          acc[g][t] = thin_smfmac<DT == kF16>(a, cur.b[t][0], cur.b[t][1], acc[g][t], ix);
+          acc[g][t] = thin_smfmac<DT == kF16>(a, b[t][0], b[t][1], acc[g][t], ix);
       }
     }
     if constexpr (DT == kI8) {
@@ -410,28 +452,29 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   store_eight(p.ep.y, y_type<DT>(p.ep), i, left, y);
 }
 
-template <int DT, int PAT, bool BLOCKED, bool RAGGED>
+template <int DT, int PAT, bool BLOCKED, bool RAGGED, bool DIRECT>
 hipError_t launch_cols(const ThinArgs& p, const ThinPlan& plan, hipStream_t s) {
   const auto go = [&](auto rg, auto nt) {
     constexpr int RG = decltype(rg)::value, NT = decltype(nt)::value;
     const unsigned cols = NT == 0 ? 1u : (unsigned)(plan.Tp / (16 * (NT == 0 ? 1 : NT)));
     const dim3 grid((unsigned)((p.R + 16 * RG - 1) / (16 * RG)), cols);
-    thin_kernel<DT, PAT, BLOCKED, RAGGED, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
+    thin_kernel<DT, PAT, BLOCKED, RAGGED, DIRECT && NT != 0, RG, NT><<<grid, 64 * kThinWaves, 0, s>>>(p);
     return hipGetLastError();
   };
   typedef std::integral_constant<int, 1> One;
-  if constexpr (!RAGGED)
+  if constexpr (DIRECT)
     if (p.T == 1) return go(One{}, std::integral_constant<int, 0>{});
   typedef std::integral_constant<int, 2> Two;
   if (plan.nt == 1) return go(One{}, One{});
-  if (plan.nt == 2 || DT == kF32) return go(Two{}, Two{});
-  return go(Two{}, std::integral_constant<int, 4>{});
+  if constexpr (!DIRECT && DT != kF32)
+    if (plan.nt == 4) return go(Two{}, std::integral_constant<int, 4>{});
+  return go(Two{}, Two{});
 }
 
 template <int DT>
 hipError_t launch_thin_as(ThinArgs p, const ThinPlan& plan, int pat, bool blocked, const void* X,
                           void* xt, hipStream_t s) {
-  if (p.T == 1 && p.K % 64 == 0) {
+  if (plan.direct) {
     p.xt = X;
   } else {
     const TurnArgs turn{X, p.K, p.T, p.Tp, xt};
@@ -441,9 +484,12 @@ hipError_t launch_thin_as(ThinArgs p, const ThinPlan& plan, int pat, bool blocke
   }
   const auto go = [&](auto pattern) {
     constexpr int PAT = decltype(pattern)::value;
-    if (blocked) return launch_cols<DT, PAT, true, false>(p, plan, s);
-    if (p.K % 64 == 0) return launch_cols<DT, PAT, false, false>(p, plan, s);
-    return launch_cols<DT, PAT, false, true>(p, plan, s);
+    if (plan.direct)
+      return blocked ? launch_cols<DT, PAT, true, false, true>(p, plan, s)
+                     : launch_cols<DT, PAT, false, false, true>(p, plan, s);
+    if (blocked) return launch_cols<DT, PAT, true, false, false>(p, plan, s);
+    if (p.K % 64 == 0) return launch_cols<DT, PAT, false, false, false>(p, plan, s);
+    return launch_cols<DT, PAT, false, true, false>(p, plan, s);
   };
   if (pat == kP24) return go(std::integral_constant<int, kP24>{});
   if (pat == kP12) return go(std::integral_constant<int, kP12>{});

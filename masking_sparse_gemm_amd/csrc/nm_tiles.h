@@ -101,23 +101,31 @@ struct XentGradCut {
 // ---- compressed products of few tokens ------------------------------------------------------------
 
 // The thin product's workgroup: 16 rg rows, 16 nt columns, a step of 64 K to each of eight waves at a
-// time; Tp: padded columns.  Estimated time (us): two launches and the first loads, then rounds of
+// time; Tp: padded columns; direct: X's numbers are loaded one by one where they lie, without a copy
+// (T = 1: in whole pieces).  Estimated time (us): one launch or two and the first loads, then rounds of
 // workgroups over 256 units times eight steps at `step`, which a unit's loads set.  Measured for 64
 // steps: one round of 16 x 16 8.3, 32 x 32 10.3, 32 x 64 13.0; 16 rounds of 32 x 64 145; in fp32, whose
-// expanded products set it, 13.2 and 29.
+// expanded products set it, 13.2 and 29.  Through the copy / direct, bf16: 300 x 512, 8 columns 6.0 / 4.1,
+// 1000 x 1024, 128 columns 7.4 / 5.2, 517 columns 11.8 / 14.2; 4096 x 4096, 8 columns 9.4 / 8.7, 32
+// columns 11.0 / 11.5 (int8 10.3 / 12.9); 128 x 4096, 256 columns 11.2 / 7.6.
 struct ThinPlan {
   int rg = 1, nt = 1;
   int64_t Tp = 0;
+  bool direct = false;
   double us = 1e30;
   ThinPlan(int64_t R, int64_t K, int64_t T, bool f32) {
     constexpr int kShapes[3][2] = {{1, 1}, {2, 2}, {2, 4}};
     constexpr double kStep[3] = {0.41, 0.65, 1.0}, kStep32[2] = {1.0, 3.0};
+    constexpr double kOnes[2] = {0.22, 0.6};  // more for X's numbers one by one
     for (int i = 0; i < (f32 ? 2 : 3); ++i) {
       const int64_t rows = 16 * kShapes[i][0], cols = 16 * kShapes[i][1], tp = (T + cols - 1) / cols;
       const int64_t groups = (R + rows - 1) / rows * tp, eights = ((K + 63) / 64 + 7) / 8;
-      const double t = 5 + (double)((groups + 255) / 256) * (double)eights * (f32 ? kStep32[i] : kStep[i]);
-      if (t < us) {
+      const double each = (double)((groups + 255) / 256) * (double)eights, step = f32 ? kStep32[i] : kStep[i];
+      for (int d = 0; d < (K % 64 == 0 && i < 2 ? 2 : 1); ++d) {
+        const double t = d == 0 ? 5 + each * step : 3 + each * (step + (T == 1 ? 0 : kOnes[i]));
+        if (t >= us) continue;
         us = t;
+        direct = d == 1;
         rg = kShapes[i][0];
         nt = kShapes[i][1];
         Tp = tp * cols;

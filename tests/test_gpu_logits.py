@@ -87,7 +87,7 @@ ALL = ("rep", "pres", "freq", "prompts")
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("V,T", [(1, 1), (31, 2), (33, 3), (1000, 1), (8191, 1), (8193, 1), (3001, 5),
-                                 (700, 16), (513, 17), (257, 64), (300, 33), (40, 100)])
+                                 (700, 16), (513, 17), (257, 64), (300, 33), (40, 100), (20011, 20)])
 def test_sizes(V, T, dtype):
     run(V, T, dtype, 50, ALL, "shared", True)
 
@@ -99,9 +99,10 @@ def test_parts(parts, bias, mask):
     run(500, 9, "fp32", 60, parts, bias, mask)
 
 
+@pytest.mark.parametrize("T", [7, 40])
 @pytest.mark.parametrize("bias,mask", [(None, False), ("each", False), (None, True)])
-def test_without_tokens(bias, mask):
-    run(2000, 7, "bf16", None, (), bias, mask)
+def test_without_tokens(bias, mask, T):
+    run(2000, T, "bf16", None, (), bias, mask)
 
 
 @pytest.mark.parametrize("longest", [0, 1, 5000])

@@ -92,6 +92,32 @@ def test_one_token(n, m, layout, dtype, R, K):
         "fp32" if dtype in EIGHT else dtype)
 
 
+# test_more_tiles.py holds the rule to every shape of a workgroup here, with X turned and as it lies
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
+@pytest.mark.parametrize("layout", ["rows", "blocked"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32", "int8", "fp8"])
+@pytest.mark.parametrize("R,K,T", [(1000, 1024, 517), (2048, 1024, 517), (256, 192, 1000), (256, 192, 2000)])
+def test_thin_shapes(n, m, layout, dtype, R, K, T):
+    run(R, K, T, n, m, dtype, layout, "relu", True, True, dtype not in EIGHT,
+        "fp32" if dtype in EIGHT else dtype)
+
+
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
+@pytest.mark.parametrize("K", [192, 180])
+def test_infinite_columns_of_X_stay_where_they_are(n, m, K):
+    """A column's numbers reach no other column, and those past the last one are no column's."""
+    R, T = 77, 33
+    values, meta, X, W, _ = inputs(R, K, T, n, m, "bf16", "rows")
+    want = nm.spmm_act(values, meta, X, n, m)
+    for t in (0, 16, 32):
+        Y = X.clone()
+        Y[:, t] = math.nan
+        got = nm.spmm_act(values, meta, Y, n, m)
+        assert bool(got[:, t].isnan().all())
+        rest = [c for c in range(T) if c != t]
+        assert torch.equal(got[:, rest], want[:, rest])
+
+
 @pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32", "int8", "fp8"])
 @pytest.mark.parametrize("K", [8, 72, 148, 1020])

@@ -21,8 +21,9 @@ def test_sizes():
     assert act(32, 72, 3, 8, 7, BF) == 72 * 8 * 2 // 256 * 256 + 256
     assert act(32, 72, 3, 8, 7, F32) == 72 * 8 * 4 and act(32, 72, 3, 8, 17, I8) == 72 * 32
     assert act(32, 60, 2, 4, 7, BF) == 64 * 16 * 2       # few tokens: X turned, in whole steps
-    assert act(32, 64, 2, 4, 7, BF) == 64 * 16 * 2       # few tokens: X turned, 16 columns
-    assert act(32, 64, 2, 4, 7, F32) == 64 * 16 * 4 and act(32, 64, 1, 2, 7, I8) == 64 * 16 * 2
+    assert act(32, 60, 2, 4, 7, F32) == 64 * 16 * 4 and act(32, 60, 1, 2, 7, I8) == 64 * 16 * 2
+    assert act(32, 64, 2, 4, 7, BF) == act(32, 64, 1, 2, 7, I8) == act(32, 64, 2, 4, 1, F32) == 0  # as it lies
+    assert act(1000, 1024, 2, 4, 517, BF) == 1024 * 544 * 2   # many workgroups read it: turned
     assert act(8192, 4096, 2, 4, 2048, BF) == 0          # many: as it lies
     assert act(32, -4, 2, 4, 7, BF) == act(32, 64, 2, 4, 7, 9) == act(32, 64, 5, 4, 7, BF) == 0
     need = L.nm_spmm_act_grad_workspace_bytes
@@ -60,14 +61,15 @@ def test_spmm_act_refusals():
     assert spmm_act(act=6) == spmm_act(act=-1) == "unsupported"
     assert spmm_act(dt=I8, Z=None, n=1, m=8, ydt=F32) == "unsupported"
     assert spmm_act(values=None) == spmm_act(meta=None) == spmm_act(X=None) == spmm_act(Y=None) == "null"
-    assert spmm_act(ws=None) == "null" and spmm_act(size=100) == "scratch"
+    many = dict(R=1000, K=1024, T=517)                             # (whose X is turned)
+    assert spmm_act(ws=None, **many) == "null" and spmm_act(size=100, **many) == "scratch"
     for name in ("values", "meta", "X", "bias", "residual", "Z", "Y"):
         assert spmm_act(**{name: ODD}) == "align", name
     assert spmm_act(ws=ODD) == "align"
     assert spmm_act(dt=I8, Z=None, scale=ODD, ydt=F32) == "align"
     for name in ("values", "meta", "X", "bias", "Z"):
         assert spmm_act(**{name: far(7)}) == "alias", name
-    assert spmm_act(Z=far(5)) == spmm_act(ws=far(3)) == spmm_act(ws=far(6)) == "alias"
+    assert spmm_act(Z=far(5)) == spmm_act(ws=far(3), **many) == spmm_act(ws=far(6), **many) == "alias"
     assert spmm_act(residual=ctypes.c_void_p(far(7).value + 64)) == "alias"
     assert spmm_act(residual=far(7)) == "device"                   # in place: as far as a GPU
     assert spmm_act(bias=None, residual=None, Z=None) == "device"

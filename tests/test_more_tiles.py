@@ -17,8 +17,8 @@ int main(int, char** a) {
   const int n = atoi(a[3]), m = atoi(a[4]), elem = atoi(a[6]);
   const nm::ThinPlan p(R, K, T, elem == 4);
   const nm::SpmmGradCut c(R, K, T, true, true);
-  std::printf("%d %d %d %ld %d %d %d\n", (int)nm::thin_preferred(R, K, n, m, T, elem), p.rg, p.nt,
-              (long)p.Tp, c.tile, c.splits_x, c.splits_w);
+  std::printf("%d %d %d %ld %d %d %d %d\n", (int)nm::thin_preferred(R, K, n, m, T, elem), p.rg, p.nt,
+              (long)p.Tp, c.tile, c.splits_x, c.splits_w, (int)p.direct);
 }
 """
 
@@ -33,7 +33,7 @@ def rule(tmp_path_factory):
     def ask(R, K, n, m, T, elem):
         out = subprocess.run([str(at / "rule"), *map(str, (R, K, n, m, T, elem))], check=True,
                              capture_output=True, text=True).stdout.split()
-        return dict(zip(("thin", "rg", "nt", "Tp", "tile", "splits_x", "splits_w"), map(int, out)))
+        return dict(zip(("thin", "rg", "nt", "Tp", "tile", "splits_x", "splits_w", "direct"), map(int, out)))
     return ask
 
 
@@ -51,6 +51,21 @@ def test_sizes_of_the_tiled_kernels_tests(rule):
         for n, m in ((2, 4), (1, 2), (1, 4)):
             for elem in (1, 2, 4):
                 assert not rule(R, K, n, m, T, elem)["thin"], (R, K, T, n, m, elem)
+
+
+def test_sizes_of_the_thin_kernels_tests(rule):
+    """Every shape of a workgroup, with X turned and as it lies."""
+    shape = lambda *a: [rule(*a)[k] for k in ("thin", "rg", "nt", "direct")]
+    for n, m in ((2, 4), (1, 2), (1, 4)):
+        for elem in (1, 2):
+            assert shape(1000, 1024, n, m, 517, elem) == [1, 2, 2, 0]
+            assert shape(2048, 1024, n, m, 517, elem) == [1, 2, 4, 0]
+            assert shape(77, 192, n, m, 33, elem) == [1, 1, 1, 1]
+            assert shape(256, 192, n, m, 1000, elem) == [1, 2, 2, 1]
+        assert shape(1000, 1024, n, m, 517, 4) == [1, 1, 1, 0] and shape(77, 192, n, m, 33, 4) == [1, 1, 1, 1]
+        assert shape(256, 192, n, m, 2000, 4) == [1, 2, 2, 1]
+        assert shape(256, 180, n, m, 2000, 4) == [1, 2, 2, 0]
+    assert shape(300, 100, 2, 4, 7, 2) == [1, 1, 1, 0] and shape(8192, 4096, 2, 4, 1, 2)[3] == 1
 
 
 def test_columns_are_whole_tiles(rule):
