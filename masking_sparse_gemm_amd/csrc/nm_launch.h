@@ -62,7 +62,7 @@ hipError_t launch_expand_act(const void* values, const uint32_t* meta, int64_t R
                              int m, bool blocked, const void* X, int64_t T, int dt, const Product& p,
                              hipStream_t s);
 
-// 2:4, 1:2 and 1:4 of any type for few tokens (nm_thin.hip; K % 64 == 0); the workspace takes X turned.
+// 2:4, 1:2, 1:4 and 4:8 of any type for few tokens (nm_thin.hip); the workspace takes X turned.
 hipError_t launch_thin(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                        bool blocked, const void* X, int64_t T, int dt, const Product& product,
                        void* workspace, hipStream_t s);

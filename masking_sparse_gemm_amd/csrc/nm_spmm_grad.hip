@@ -431,7 +431,7 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
 
 size_t spmm_act_workspace_bytes(int64_t R, int64_t K, int n, int m, int64_t T, int dt) {
   if (thin_preferred(R, K, n, m, T, elem_of(dt))) {
-    const ThinPlan plan(R, K, T, dt == kF32);
+    const ThinPlan plan(R, K, T, m, dt == kF32);
     return plan.direct ? 0 : (size_t)(plan.Tp * pad64(K) * (dt == kF32 ? 4 : 2));
   }
   const int64_t ldx = whole_row(T, dt);

@@ -1,4 +1,4 @@
-// nm_thin.hip -- nm_spmm_act for few tokens and small matrices (gfx950), 2:4, 1:2 and 1:4, every type.
+// nm_thin.hip -- nm_spmm_act for few tokens and small matrices (gfx950), 2:4, 1:2, 1:4 and 4:8, every type.
 //
 // The tiled kernels of nm_spmm.hip give a workgroup 128 rows or more and walk K in one barrier a
 // step, so with few rows and columns most units have nothing to do and the rest wait.  Here a
@@ -9,12 +9,12 @@
 // contiguous, made by a first small launch; where few workgroups read X, they load its numbers one by
 // one instead, and one column as it lies.  fp8 and int8 become bf16 exactly on the way (int8 sums are
 // exact: fp32 holds 1024 K of products of up to 2^14, then they move to int32).  1:2 places become
-// 2:4's by their bits, a 1:4 group a pair with a zero.  fp32, which has no sparse instruction, is
-// expanded in registers for v_mfma_f32_16x16x4_f32.
+// 2:4's by their bits, a 1:4 group a pair with a zero.  What the sparse instruction cannot have is
+// expanded in registers: 4:8 for v_mfma_f32_16x16x32, fp32 for v_mfma_f32_16x16x4_f32.
 //
 // Bound by the first loads' latency on small matrices and by the reads of W on large ones: bf16, one
 // column, 1024 x 4096 5.1 us, 4096 x 4096 6.2, 8192 x 4096 8.5 (4.4 TB/s of W; the tiled kernels take 41
-// for the middle one); 1000 x 1024, 517 columns 9.4 and 4.1 for X's copy, against 53 in tiles.
+// for the middle one); 1000 x 1024, 517 columns 9.4 and 4.1 for X's copy, against 53 in tiles; 4:8 2358 x 1856, 6 columns 7.4 against 40.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,7 +26,7 @@ namespace nm {
 namespace {
 
 constexpr int kThinWaves = 8;
-enum { kP24, kP12, kP14 };  // patterns
+enum { kP24, kP12, kP14, kP48 };  // patterns
 
 // ---- X, transposed -------------------------------------------------------------------
 
@@ -110,6 +110,8 @@ struct ThinArgs {
 template <int DT, int PAT>
 struct ThinRaw {
   typedef typename ThinElem<DT>::type E;
+  static __device__ __forceinline__ int values_at(int q) { return q * kBytes; }  // of the lane's, in bytes
+  static __device__ __forceinline__ int places_at(int q) { return q * (PAT == kP24 ? 2 : 1); }
   static constexpr int kValues = PAT == kP14 ? 4 : 8;
   static constexpr int kBytes = kValues * (int)sizeof(E);
   uint32_t w[kBytes / 4];
@@ -214,6 +216,83 @@ struct ThinRaw {
   }
 };
 
+// 4:8: two groups, of 4 values and 12 bits each: a lane's numbers of the two dense products of a step,
+// groups q and 4 + q of it, or in fp32 2 q and 2 q + 1, next to one another.
+template <int DT>
+struct ThinRaw<DT, kP48> {
+  typedef typename ThinElem<DT>::type E;
+  static constexpr bool kF = DT == kF32;
+  static constexpr int kGroup = 4 * (int)sizeof(E), kFar = kF ? kGroup : 4 * kGroup;  // bytes
+  uint32_t w[2][kGroup / 4];
+  uint32_t places[2];
+  static __device__ __forceinline__ int values_at(int q) { return q * (kF ? 2 * kGroup : kGroup); }
+  static __device__ __forceinline__ int places_at(int q) { return kF ? 3 * q : 3 * q / 2; }
+
+  template <bool RAGGED>
+  __device__ __forceinline__ void load_groups(const uint8_t* v, const uint8_t* m, int q, int64_t left) {
+    typedef uint32_t one_t __attribute__((aligned(1)));
+    typedef uint16_t half_t __attribute__((aligned(1)));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint8_t* at = v + j * kFar;
+#pragma unroll
+      for (int i = 0; i < kGroup / 4; ++i) w[j][i] = 0u;
+      places[j] = 0u;
+      if (RAGGED && left <= (kF ? 8 * q + 4 * j : 16 * j + 4 * q)) continue;
+      if constexpr (RAGGED || kGroup == 4) {
+#pragma unroll
+        for (int i = 0; i < kGroup / 4; ++i) w[j][i] = reinterpret_cast<const one_t*>(at)[i];
+      } else if constexpr (kGroup == 8) {
+        const u32x2_t x = *reinterpret_cast<const u32x2_t*>(at);
+        w[j][0] = x[0];
+        w[j][1] = x[1];
+      } else {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[j][i] = x[i];
+      }
+      const int shift = kF ? 4 * j : 4 * (q & 1);
+      places[j] = (uint32_t)*reinterpret_cast<const half_t*>(m + (kF ? j : 6 * j)) >> shift;
+    }
+  }
+  __device__ __forceinline__ void load(const uint8_t* v, const uint8_t* m, int q) {
+    load_groups<false>(v, m, q, 0);
+  }
+  // left: the row's values from this step on (whole groups)
+  __device__ __forceinline__ void load_ragged(const uint8_t* v, const uint8_t* m, int q, int64_t left) {
+    load_groups<true>(v, m, q, left);
+  }
+
+  __device__ __forceinline__ uint32_t raw(int j, int i) const {
+    if constexpr (sizeof(E) == 4) return w[j][i];
+    else if constexpr (sizeof(E) == 2) return (w[j][i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+    else return (w[j][0] >> (8 * i)) & 0xFFu;
+  }
+  // The eight numbers of group j.
+  __device__ __forceinline__ u32x4_t dense(int j) const {
+    u32x4_t d{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = (places[j] >> (3 * i)) & 7u, v = to_half<DT>(raw(j, i)) << (16 * (p & 1u));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] |= (p >> 1) == (uint32_t)k ? v : 0u;
+    }
+    return d;
+  }
+  __device__ __forceinline__ void expand(float (&d)[16]) const {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x = ((places[j] >> (3 * i)) & 7u) == (uint32_t)k ? __uint_as_float(w[j][i]) : x;
+        d[8 * j + k] = x;
+      }
+  }
+};
+
 template <bool F16>
 __device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t& b0, const u32x4_t& b1,
                                                 const float4_t& c, uint32_t ix) {
@@ -228,6 +307,16 @@ __device__ __forceinline__ float4_t thin_smfmac(const u32x4_t& a, const u32x4_t&
                                                      0);
 }
 
+template <bool F16>
+__device__ __forceinline__ float4_t thin_mfma(const u32x4_t& a, const u32x4_t& b, const float4_t& c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
 // RAGGED: the row layout, K not in whole steps (X's copy ends in zeros).  DIRECT: xt is X itself, whose
 // numbers are loaded one by one.  COLS = 0: one column, X as it lies, in each of the instruction's
 // sixteen.
@@ -238,7 +327,7 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   constexpr bool kF = DT == kF32, kOne = COLS == 0;
   constexpr int NT = kOne ? 1 : COLS;
   constexpr int kRows = 16 * RG, kCols = 16 * NT;
-  constexpr int kRowValues = PAT == kP14 ? 16 : 32, kRowMeta = PAT == kP24 ? 8 : 4;  // a row and step
+  constexpr int kRowValues = PAT == kP14 ? 16 : 32, kRowMeta = PAT == kP48 ? 12 : PAT == kP24 ? 8 : 4;  // a row and step
   constexpr int kPitch = kCols + 4;  // of the sums in LDS
   __shared__ __attribute__((aligned(16))) float sums[kThinWaves][kRows * kPitch];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
@@ -254,12 +343,12 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
   for (int g = 0; g < RG; ++g) {
     if constexpr (BLOCKED) {
       const int64_t b = min(r0 / 16 + g, groups - 1);
-      v[g] = p.values + (b * steps * 16 + l16) * kRowValues * (int64_t)sizeof(E) + q * Raw::kBytes;
-      m[g] = p.meta + (b * steps * 16 + l16) * kRowMeta + q * (kRowMeta / 4);
+      v[g] = p.values + (b * steps * 16 + l16) * kRowValues * (int64_t)sizeof(E) + Raw::values_at(q);
+      m[g] = p.meta + (b * steps * 16 + l16) * kRowMeta + Raw::places_at(q);
     } else {
       const int64_t row = min(r0 + 16 * g + l16, p.R - 1);
-      v[g] = p.values + row * p.row_values * (int64_t)sizeof(E) + q * Raw::kBytes;
-      m[g] = p.meta + row * p.row_meta + q * (kRowMeta / 4);
+      v[g] = p.values + row * p.row_values * (int64_t)sizeof(E) + Raw::values_at(q);
+      m[g] = p.meta + row * p.row_meta + Raw::places_at(q);
     }
   }
   constexpr int kVStep = (BLOCKED ? 16 : 1) * kRowValues * (int)sizeof(E);
@@ -312,7 +401,9 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       const uint8_t *va = v[g] + (int64_t)s * kVStep, *ma = m[g] + (int64_t)s * kMStep;
-      if constexpr (RAGGED) f.a[g].load_ragged(va, ma, p.row_values - (4 * (int64_t)s + q) * Raw::kValues);
+      if constexpr (PAT == kP48 && RAGGED) f.a[g].load_ragged(va, ma, q, p.row_values - 32 * (int64_t)s);
+      else if constexpr (PAT == kP48) f.a[g].load(va, ma, q);
+      else if constexpr (RAGGED) f.a[g].load_ragged(va, ma, p.row_values - (4 * (int64_t)s + q) * Raw::kValues);
       else f.a[g].load(va, ma);
     }
 #pragma unroll
@@ -368,6 +459,13 @@ __global__ void __launch_bounds__(64 * kThinWaves) thin_kernel(ThinArgs p) {
           for (int t = 0; t < NT; ++t)
             acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k], __uint_as_float(b[t][k / 4][k % 4]),
                                                              acc[g][t], 0, 0, 0);
+      } else if constexpr (PAT == kP48) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const u32x4_t a = cur.a[g].dense(i);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[g][t] = thin_mfma<DT == kF16>(a, b[t][i], acc[g][t]);
+        }
       } else {
         uint32_t ix;
         const u32x4_t a = cur.a[g].operand(ix);
@@ -493,6 +591,7 @@ hipError_t launch_thin_as(ThinArgs p, const ThinPlan& plan, int pat, bool blocke
   };
   if (pat == kP24) return go(std::integral_constant<int, kP24>{});
   if (pat == kP12) return go(std::integral_constant<int, kP12>{});
+  if (pat == kP48) return go(std::integral_constant<int, kP48>{});
   return go(std::integral_constant<int, kP14>{});
 }
 
@@ -501,12 +600,12 @@ hipError_t launch_thin_as(ThinArgs p, const ThinPlan& plan, int pat, bool blocke
 hipError_t launch_thin(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                        bool blocked, const void* X, int64_t T, int dt, const Product& product,
                        void* workspace, hipStream_t s) {
-  const ThinPlan plan(R, K, T, dt == kF32);
+  const ThinPlan plan(R, K, T, m, dt == kF32);
   void* xt = workspace;
   const ThinArgs p{static_cast<const uint8_t*>(values), reinterpret_cast<const uint8_t*>(meta), xt, R,
-                   K, T, plan.Tp, K / m * n, ((K / m * n) * (m == 2 ? 1 : 2) + 31) / 32 * 4,
+                   K, T, plan.Tp, K / m * n, ((K / m * n) * (m == 2 ? 1 : m == 4 ? 2 : 3) + 31) / 32 * 4,
                    epilogue_of(product)};
-  const int pat = m == 2 ? kP12 : n == 2 ? kP24 : kP14;
+  const int pat = m == 8 ? kP48 : m == 2 ? kP12 : n == 2 ? kP24 : kP14;
   if (dt == kBF16) return launch_thin_as<kBF16>(p, plan, pat, blocked, X, xt, s);
   if (dt == kF16) return launch_thin_as<kF16>(p, plan, pat, blocked, X, xt, s);
   if (dt == kF32) return launch_thin_as<kF32>(p, plan, pat, blocked, X, xt, s);

@@ -107,20 +107,22 @@ struct XentGradCut {
 // steps: one round of 16 x 16 8.3, 32 x 32 10.3, 32 x 64 13.0; 16 rounds of 32 x 64 145; in fp32, whose
 // expanded products set it, 13.2 and 29.  Through the copy / direct, bf16: 300 x 512, 8 columns 6.0 / 4.1,
 // 1000 x 1024, 128 columns 7.4 / 5.2, 517 columns 11.8 / 14.2; 4096 x 4096, 8 columns 9.4 / 8.7, 32
-// columns 11.0 / 11.5 (int8 10.3 / 12.9); 128 x 4096, 256 columns 11.2 / 7.6.
+// columns 11.0 / 11.5 (int8 10.3 / 12.9); 128 x 4096, 256 columns 11.2 / 7.6.  4:8 is expanded in
+// registers: 4096 x 4096 with 8, 32 and 256 columns 11.8, 17.3 and 36 where 2:4 takes 8.7, 11.1 and 24.
 struct ThinPlan {
   int rg = 1, nt = 1;
   int64_t Tp = 0;
   bool direct = false;
   double us = 1e30;
-  ThinPlan(int64_t R, int64_t K, int64_t T, bool f32) {
+  ThinPlan(int64_t R, int64_t K, int64_t T, int m, bool f32) {
     constexpr int kShapes[3][2] = {{1, 1}, {2, 2}, {2, 4}};
     constexpr double kStep[3] = {0.41, 0.65, 1.0}, kStep32[2] = {1.0, 3.0};
     constexpr double kOnes[2] = {0.22, 0.6};  // more for X's numbers one by one
     for (int i = 0; i < (f32 ? 2 : 3); ++i) {
       const int64_t rows = 16 * kShapes[i][0], cols = 16 * kShapes[i][1], tp = (T + cols - 1) / cols;
       const int64_t groups = (R + rows - 1) / rows * tp, eights = ((K + 63) / 64 + 7) / 8;
-      const double each = (double)((groups + 255) / 256) * (double)eights, step = f32 ? kStep32[i] : kStep[i];
+      const double each = (double)((groups + 255) / 256) * (double)eights, more = m != 8 ? 1 : f32 ? 1.2 : 1.7;
+      const double step = more * (f32 ? kStep32[i] : kStep[i]);
       for (int d = 0; d < (K % 64 == 0 && i < 2 ? 2 : 1); ++d) {
         const double t = d == 0 ? 5 + each * step : 3 + each * (step + (T == 1 ? 0 : kOnes[i]));
         if (t >= us) continue;
@@ -138,12 +140,15 @@ struct ThinPlan {
 // tiles, a flow of tiles over the units where there are many.  Measured: 2:4 and 1:2 in 16 bits 4096 x
 // 1024, 8 columns 15.5, 4096 x 4096 38.9, with 1024 columns 41, 8192 x 4096 40.7, 262144 x 256, 8
 // columns 39; in 8 bits 4096 x 4096 24, 8192 x 4096, 1024 columns 32; expanded in 16 bits 100 and 128,
-// in fp32 342 and 594.
+// in fp32 342 and 594; 4:8 in 16 bits 300 x 512 13.9, 2358 x 1856 40, 4096 x 4096 65, 8192 x 512, 1024
+// columns 18.5.
 inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
   const double S = (double)((K + 63) / 64);
   const bool sparse = ((n == 2 && m == 4) || (n == 1 && m == 2)) && K % 64 == 0;
   const double tiles = (double)((R + 127) / 128) * (double)((T + 127) / 128);
   if (elem == 4) return std::max(5.3 + 5.25 * S, tiles / 512 * (5 + 9.2 * S));
+  if (n == 4 && m == 8 && elem == 2 && K % 64 == 0)
+    return std::max(7 + 0.9 * S, tiles / 256 * (4.5 + 0.41 * S));
   if (!sparse || (elem == 1 && K % 128 != 0)) return std::max(7 + 1.45 * S, tiles / 512 * (5 + 1.9 * S));
   if (elem == 1) return std::max(9.7 + 0.22 * S, tiles / 512 * (6 + 0.2 * S));
   return std::max(7.2 + 0.49 * S, tiles / 256 * (3.9 + 0.25 * S));
@@ -151,9 +156,9 @@ inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) 
 
 // Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).
 inline bool thin_preferred(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
-  const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4));
+  const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4)) || (n == 4 && m == 8);
   if (!pattern || K == 0 || T > 4096) return false;
-  return ThinPlan(R, K, T, elem == 4).us < tiled_us(R, K, n, m, T, elem);
+  return ThinPlan(R, K, T, m, elem == 4).us < tiled_us(R, K, n, m, T, elem);
 }
 
 // ---- gradient of the compressed product ---------------------------------------------------------

@@ -93,7 +93,7 @@ def test_one_token(n, m, layout, dtype, R, K):
 
 
 # test_more_tiles.py holds the rule to every shape of a workgroup here, with X turned and as it lies
-@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4), (4, 8)])
 @pytest.mark.parametrize("layout", ["rows", "blocked"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32", "int8", "fp8"])
 @pytest.mark.parametrize("R,K,T", [(1000, 1024, 517), (2048, 1024, 517), (256, 192, 1000), (256, 192, 2000)])
@@ -102,8 +102,8 @@ def test_thin_shapes(n, m, layout, dtype, R, K, T):
         "fp32" if dtype in EIGHT else dtype)
 
 
-@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4)])
-@pytest.mark.parametrize("K", [192, 180])
+@pytest.mark.parametrize("n,m", [(2, 4), (1, 2), (1, 4), (4, 8)])
+@pytest.mark.parametrize("K", [192, 184])
 def test_infinite_columns_of_X_stay_where_they_are(n, m, K):
     """A column's numbers reach no other column, and those past the last one are no column's."""
     R, T = 77, 33
@@ -123,6 +123,13 @@ def test_infinite_columns_of_X_stay_where_they_are(n, m, K):
 @pytest.mark.parametrize("K", [8, 72, 148, 1020])
 def test_few_tokens_of_every_type_and_any_width(n, m, dtype, K):
     run(45, K, 20, n, m, dtype, "rows", "silu", True, False, False, "fp32" if dtype in EIGHT else dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32", "int8", "fp8"])
+@pytest.mark.parametrize("K", [8, 16, 72, 120, 152, 1016])
+@pytest.mark.parametrize("T", [1, 20])
+def test_4_of_8_of_any_width(dtype, K, T):
+    run(45, K, T, 4, 8, dtype, "rows", "silu", True, False, False, "fp32" if dtype in EIGHT else dtype)
 
 
 def test_bytes_without_a_scale():

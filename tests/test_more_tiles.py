@@ -15,7 +15,7 @@ PROGRAM = r"""
 int main(int, char** a) {
   const long R = atol(a[1]), K = atol(a[2]), T = atol(a[5]);
   const int n = atoi(a[3]), m = atoi(a[4]), elem = atoi(a[6]);
-  const nm::ThinPlan p(R, K, T, elem == 4);
+  const nm::ThinPlan p(R, K, T, m, elem == 4);
   const nm::SpmmGradCut c(R, K, T, true, true);
   std::printf("%d %d %d %ld %d %d %d %d\n", (int)nm::thin_preferred(R, K, n, m, T, elem), p.rg, p.nt,
               (long)p.Tp, c.tile, c.splits_x, c.splits_w, (int)p.direct);
@@ -41,14 +41,14 @@ def test_thin_or_tiled(rule):
     assert rule(4096, 4096, 2, 4, 1, 2)["thin"] and rule(1000, 1024, 2, 4, 517, 2)["thin"]
     assert not rule(11008, 4096, 2, 4, 2048, 2)["thin"] and not rule(4096, 11008, 2, 4, 2048, 2)["thin"]
     assert rule(64, 100, 2, 4, 1, 2)["thin"]           # K need not be whole steps
-    assert not rule(64, 64, 4, 8, 1, 2)["thin"] and not rule(64, 64, 2, 2, 1, 2)["thin"]
+    assert rule(64, 64, 4, 8, 1, 2)["thin"] and not rule(64, 64, 2, 2, 1, 2)["thin"]
     assert rule(4096, 4096, 1, 4, 256, 2)["thin"] and rule(4096, 4096, 2, 4, 512, 4)["thin"]
     assert not rule(16, 64, 2, 4, 1 << 20, 2)["thin"]
 
 
 def test_sizes_of_the_tiled_kernels_tests(rule):
     for R, K, T in ((2000, 128, 2056), (2000, 128, 2061), (2000, 192, 2061)):
-        for n, m in ((2, 4), (1, 2), (1, 4)):
+        for n, m in ((2, 4), (1, 2), (1, 4), (4, 8)):
             for elem in (1, 2, 4):
                 assert not rule(R, K, n, m, T, elem)["thin"], (R, K, T, n, m, elem)
 
@@ -56,7 +56,7 @@ def test_sizes_of_the_tiled_kernels_tests(rule):
 def test_sizes_of_the_thin_kernels_tests(rule):
     """Every shape of a workgroup, with X turned and as it lies."""
     shape = lambda *a: [rule(*a)[k] for k in ("thin", "rg", "nt", "direct")]
-    for n, m in ((2, 4), (1, 2), (1, 4)):
+    for n, m in ((2, 4), (1, 2), (1, 4), (4, 8)):
         for elem in (1, 2):
             assert shape(1000, 1024, n, m, 517, elem) == [1, 2, 2, 0]
             assert shape(2048, 1024, n, m, 517, elem) == [1, 2, 4, 0]
