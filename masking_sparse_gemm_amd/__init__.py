@@ -794,7 +794,7 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
     _expect(residual, "residual", (R, T), y_dtype, device)
     _expect(out, "out", (R, T), y_dtype, device)
     if out is None:
-        out = X.new_empty((R, T), dtype=y_dtype)
+        out = torch.empty_like(residual) if residual is not None else X.new_empty((R, T), dtype=y_dtype)
     Z = X.new_empty((R, T)) if keep else None
     L = lib()
     ws, ws_ptr = _workspace(X, L.nm_spmm_act_workspace_bytes(R, K, n, m, T, dt))
@@ -844,9 +844,10 @@ def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: tor
         vdt, vrows = _check_compressed(values, meta, n, m, K, layout, R)
         if vdt != dt or vrows != R or values.get_device() != device:
             raise ValueError("values must have dY's rows, dtype and device")
-    shapes = dict(dW=((R, K), dY.dtype), dX=((K, T), dY.dtype), dbias=((R,), torch.float32),
-                  dZ=((R, T), dY.dtype))
-    res = {w: dY.new_empty(shapes[w][0], dtype=shapes[w][1]) for w in want}
+    res = {}
+    for w in want:
+        res[w] = (torch.empty_like(X) if w == "dX" else torch.empty_like(dY) if w == "dZ" else
+                  dY.new_empty((R, K)) if w == "dW" else dY.new_empty(R, dtype=torch.float32))
     L = lib()
     dx = "dX" in want
     ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_workspace_bytes(
@@ -888,7 +889,7 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
     _expect(residual, "residual", (rows, T), y_dtype, device)
     _expect(out, "out", (rows, T), y_dtype, device)
     if out is None:
-        out = X.new_empty((rows, T), dtype=y_dtype)
+        out = torch.empty_like(residual) if residual is not None else X.new_empty((rows, T), dtype=y_dtype)
     L = lib()
     ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
     _launch("nm_matvec_act", X,
