@@ -452,10 +452,14 @@ nm_status nm_spmm_act(const void* values, const uint32_t* meta, int64_t R, int64
  * all but dbias in dt; the residual's gradient is dY itself.  act' of RELU and RELU2 is 0 at 0.
  * Each of dW, dX, dbias and dZ may be NULL and is then not computed; X is needed for dW, values and meta
  * for dX alone, Z only with an activation (each else NULL if one likes).  dZ is rounded to dt before
- * the products, whose sums are fp32 and rounded once.  R, K, T < 2^22, R*T and K*T < 2^36, else
- * NM_ERR_SHAPE.  Fastest where R and T are multiples of 64.
- * workspace: nm_spmm_act_grad_workspace_bytes of the sizes, of which results are wanted, and of
- * whether there is an activation. */
+ * the products, whose sums are fp32 and rounded once; in NM_F16 over a power of two of its row for dW and
+ * of its column for dX, so that no finite dZ leaves fp16's range there.  R, K, T < 2^22, R*T and
+ * K*T < 2^36, else NM_ERR_SHAPE.  Fastest where R and T are multiples of 64.
+ * workspace: nm_spmm_act_grad_dt_workspace_bytes of the sizes, the type, the activation, and of which
+ * results are wanted.  nm_spmm_act_grad_workspace_bytes is that of NM_BF16, which is also enough for
+ * NM_F16 with NM_ACT_NONE and NM_ACT_RELU, whose dZ needs no rounding. */
+size_t nm_spmm_act_grad_dt_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_dtype dt, nm_act act,
+                                           int want_dW, int want_dX, int want_dZ);
 size_t nm_spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_act act, int want_dW,
                                         int want_dX, int want_dZ);
 nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,

@@ -69,7 +69,7 @@ EXPORTS = ("nm_abi_version", "nm_status_str", "nm_values_bytes", "nm_meta_bytes"
            "nm_xent_grad_workspace_bytes", "nm_orthogonalize",
            "nm_orthogonalize_workspace_bytes",
            "nm_spmm_act", "nm_spmm_act_workspace_bytes", "nm_spmm_act_grad",
-           "nm_spmm_act_grad_workspace_bytes", "nm_matvec_act", "nm_grad_norm",
+           "nm_spmm_act_grad_workspace_bytes", "nm_spmm_act_grad_dt_workspace_bytes", "nm_matvec_act", "nm_grad_norm",
            "nm_grad_norm_workspace_bytes", "nm_clip_grads", "nm_adjust_logits",
            "nm_adjust_logits_workspace_bytes")
 GROUPS = (32, 64, 128)   # stored columns that share a scale of the 4-bit codes
@@ -141,6 +141,7 @@ def lib() -> ctypes.CDLL:
         L.nm_spmm_act.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, vp, vp,
                                   vp, i32, vp, size, vp]
         L.nm_spmm_act_grad_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32]
+        L.nm_spmm_act_grad_dt_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32]
         L.nm_spmm_act_grad.argtypes = [vp, vp, i64, i64, i32, i32, i32, vp, i64, i32, i32, vp, vp,
                                        vp, vp, vp, vp, vp, size, vp]
         L.nm_matvec_act.argtypes = [vp, vp, vp, i64, i64, i32, vp, i64, i32, vp, i32, vp, vp, i32,
@@ -154,7 +155,8 @@ def lib() -> ctypes.CDLL:
         for f in ("nm_codes_bytes", "nm_scales_bytes", "nm_matvec_workspace_bytes",
                   "nm_xent_workspace_bytes", "nm_xent_grad_workspace_bytes",
                   "nm_orthogonalize_workspace_bytes", "nm_spmm_act_workspace_bytes",
-                  "nm_spmm_act_grad_workspace_bytes", "nm_grad_norm_workspace_bytes",
+                  "nm_spmm_act_grad_workspace_bytes", "nm_spmm_act_grad_dt_workspace_bytes",
+                  "nm_grad_norm_workspace_bytes",
                   "nm_adjust_logits_workspace_bytes"):
             getattr(L, f).restype = size
         for f in ("nm_quantize", "nm_dequantize", "nm_matvec", "nm_xent", "nm_xent_grad",
@@ -850,8 +852,8 @@ def spmm_act_grad(values: torch.Tensor | None, meta: torch.Tensor | None, X: tor
                   dY.new_empty((R, K)) if w == "dW" else dY.new_empty(R, dtype=torch.float32))
     L = lib()
     dx = "dX" in want
-    ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_workspace_bytes(
-        R, K, T, code, "dW" in want, dx, "dZ" in want))
+    ws, ws_ptr = _workspace(dY, L.nm_spmm_act_grad_dt_workspace_bytes(
+        R, K, T, dt, code, "dW" in want, dx, "dZ" in want))
     _launch("nm_spmm_act_grad", dY,
         _addr(values) if dx else None, _addr(meta) if dx else None, R, K, n, m, lay,
         _addr(X) if "dW" in want else None, T, dt, code, _addr(Z) if code else None,

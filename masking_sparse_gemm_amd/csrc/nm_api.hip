@@ -808,9 +808,14 @@ nm_status check_spmm_grad(int64_t R, int64_t K, int64_t T) {
 
 size_t nm_spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_act act, int want_dW,
                                         int want_dX, int want_dZ) {
-  if (check_spmm_grad(R, K, T) != NM_OK || !act_ok(act)) return 0;
-  return nm::spmm_act_grad_workspace_bytes(R, K, T, want_dW && R * K > 0, want_dX && K * T > 0,
-                                           want_dZ != 0, act != NM_ACT_NONE);
+  return nm_spmm_act_grad_dt_workspace_bytes(R, K, T, NM_BF16, act, want_dW, want_dX, want_dZ);
+}
+
+size_t nm_spmm_act_grad_dt_workspace_bytes(int64_t R, int64_t K, int64_t T, nm_dtype dt, nm_act act,
+                                           int want_dW, int want_dX, int want_dZ) {
+  if (!half_dtype(dt) || check_spmm_grad(R, K, T) != NM_OK || !act_ok(act)) return 0;
+  return nm::spmm_act_grad_workspace_bytes(R, K, T, dt == NM_BF16, (int)act, want_dW && R * K > 0,
+                                           want_dX && K * T > 0, want_dZ != 0);
 }
 
 nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, int64_t K, int n,
@@ -830,8 +835,8 @@ nm_status nm_spmm_act_grad(const void* values, const uint32_t* meta, int64_t R, 
   if (!aligned16(values) || !aligned16(meta) || !aligned16(X) || !aligned16(Z) || !aligned16(dY) ||
       !aligned16(dW) || !aligned16(dX) || !aligned16(dbias) || !aligned16(dZ))
     return NM_ERR_ALIGN;
-  const size_t need =
-      nm_spmm_act_grad_workspace_bytes(R, K, T, act, dW != nullptr, dX != nullptr, dZ != nullptr);
+  const size_t need = nm_spmm_act_grad_dt_workspace_bytes(R, K, T, dt, act, dW != nullptr, dX != nullptr,
+                                                          dZ != nullptr);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != NM_OK) return st;
   const Range r[] = {{dW, dW ? R * K * 2 : 0},
                      {dX, dX ? K * T * 2 : 0},

@@ -90,8 +90,8 @@ struct SpmmGradCall {
   float* dbias;
   void* dZ;
 };
-size_t spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, bool want_w, bool want_x,
-                                     bool want_z, bool act);
+size_t spmm_act_grad_workspace_bytes(int64_t R, int64_t K, int64_t T, bool bf16, int act, bool want_w,
+                                     bool want_x, bool want_z);
 hipError_t launch_spmm_act_grad(const SpmmGradCall& c, void* workspace, hipStream_t s);
 
 // Compress of W's transpose (the K x R matrix, groups of m along R; R % m == 0, and
