@@ -354,27 +354,30 @@ __global__ void __launch_bounds__(256) slope_kernel(SlopeArgs p) {
 
 // ---- W ---------------------------------------------------------------------------------------------
 
-// The dense W of a pair of any pattern and layout, 16 bits, rows of Kp numbers with zeros after the K-th:
-// a thread eight of them.  For small matrices and widths that are not multiples of 8; the others are
-// decompressed by nm_compress.hip's kernels, which are specialised for each pattern.
+// The dense W of a pair of any pattern and layout, 16 bits, rows of Kp numbers with zeros after the K-th
+// and rows of zeros after the R-th: a thread eight of them.  For small matrices and widths that are not
+// multiples of 8; the others are decompressed by nm_compress.hip's kernels, which are specialised for each
+// pattern, and have only the rows of zeros from here.  (Rows read twice instead would meet dZ's zeros, and
+// an infinity in the last one would be NaN.)
 struct ExpandArgs {
   const uint16_t* values;
   const uint8_t* meta;
   int64_t R, K, Kp;
+  int64_t begin, end;  // rows that are written
   int n, m, bits;
   bool blocked;
   uint16_t* out;
 };
 __device__ __forceinline__ void expand_pieces(const ExpandArgs& p, int64_t first, int64_t stride) {
-  const int64_t pieces = p.Kp / 8, total = p.R * pieces, row_values = p.K / p.m * p.n;
+  const int64_t pieces = p.Kp / 8, total = p.end * pieces, row_values = p.K / p.m * p.n;
   const int per = 64 / p.m * p.n;  // values of a row and step of the blocked layout
   const int64_t meta_row = (row_values * p.bits + 31) / 32 * 4;
-  for (int64_t i = first; i < total; i += stride) {
+  for (int64_t i = p.begin * pieces + first; i < total; i += stride) {
     const int64_t r = i / pieces;
     const int k0 = (int)(i % pieces * 8);
     uint64_t half[2] = {0, 0};  // numbers 0 .. 3 and 4 .. 7
     const int groups = 8 / p.m;
-    for (int g = 0; g < groups && k0 + g * p.m < p.K; ++g) {
+    for (int g = 0; g < groups && r < p.R && k0 + g * p.m < p.K; ++g) {
       const int64_t f0 = (int64_t)(k0 / p.m + g) * p.n;  // the group's first value in its row
       int64_t vi, bit;
       const uint8_t* places;
@@ -553,7 +556,7 @@ struct SpmmGradLayout {
     most = col_back + (scaled && want_x ? whole256(Tp * 4) : 0);
     x = most + (chunks > 1 ? whole256(chunks * Tp * 4) : 0);
     w = x + (pad_x ? whole256(K * Tp * 2) : 0);
-    sums_x = w + (want_x ? whole256(R * Kp * 2) : 0);
+    sums_x = w + (want_x ? whole256(Rp * Kp * 2) : 0);
     sums_w = sums_x + (cut.splits_x > 1 ? whole256(cut.splits_x * K * ((T + 3) / 4 * 4) * 4) : 0);
     total = sums_w + (cut.splits_w > 1 ? whole256(cut.splits_w * R * ((K + 3) / 4 * 4) * 4) : 0);
   }
@@ -652,13 +655,16 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
   }
   if (want_x && R > 0) {
     uint16_t* to = reinterpret_cast<uint16_t*>(ws + L.w);
-    if (R * K > kSmallW && L.Kp == K) {
+    const bool large = R * K > kSmallW && L.Kp == K;
+    if (large) {
       e = launch_decompress(c.values, c.meta, 2, R, K, c.n, c.m, c.blocked, to, s);
       if (e != hipSuccess) return e;
-    } else {
+    }
+    const int64_t begin = large ? R : 0;
+    if (begin < L.Rp) {
       a.w = ExpandArgs{static_cast<const uint16_t*>(c.values), reinterpret_cast<const uint8_t*>(c.meta), R,
-                       K, L.Kp, c.n, c.m, c.m == 2 ? 1 : c.m == 4 ? 2 : 3, c.blocked, to};
-      a.w_groups = stride_grid(R * L.Kp / 8, 256);
+                       K, L.Kp, begin, L.Rp, c.n, c.m, c.m == 2 ? 1 : c.m == 4 ? 2 : 3, c.blocked, to};
+      a.w_groups = stride_grid((L.Rp - begin) * L.Kp / 8, 256);
     }
   }
   const unsigned groups = a.slope_groups + a.x_groups + a.w_groups;
@@ -671,7 +677,7 @@ hipError_t run_spmm_act_grad(const SpmmGradCall& c, uint8_t* ws, hipStream_t s) 
   GradProducts p{};
   p.x.a = GemmOperand{reinterpret_cast<const uint16_t*>(ws + L.w), L.Kp, L.Kp, 0};
   p.x.b = GemmOperand{dz_x, L.Tp, L.Tp, 0};
-  p.x.klen = R;
+  p.x.klen = L.Rp;
   p.x.steps = (int)(L.Rp / kGemmStep);
   p.x.splits = L.cut.splits_x;
   p.x.rows = K;

@@ -176,3 +176,21 @@ def test_replays_of_a_graph(R, T):
         for a, b in zip(out, call(*new)):
             assert torch.equal(a, b)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, HALF])
+@pytest.mark.parametrize("R,K,layout", [(70, 128, "blocked"), (70, 100, "rows"), (1, 64, "blocked"),
+                                        (2051, 2112, "blocked")])
+def test_an_infinity_in_the_last_row_of_W(dtype, R, K, layout):
+    """Rows that make W whole steps hold zeros: the last one's infinity is infinite in dX, not NaN, and
+    reaches no other row of dX."""
+    T = 33
+    w = torch.randn(R, K, generator=torch.Generator().manual_seed(1)).to(dtype)
+    w[R - 1, 4] = math.inf
+    dY = (normal(R, T, 11).abs() + 0.5).to(dtype)
+    dY[:, ::2] *= -1
+    values, meta = nm.compress(w.cuda(), 2, 4, layout=layout)
+    X = torch.zeros(K, T, dtype=dtype, device="cuda")
+    (dX,) = nm.spmm_act_grad(values, meta, X, dY.cuda(), layout=layout, rows=R, want=("dX",))
+    assert torch.equal(dX[4].cpu(), torch.where(dY[R - 1] > 0, math.inf, -math.inf).to(dtype))
+    assert bool(dX[[k for k in range(K) if k != 4]].isfinite().all())
