@@ -481,14 +481,15 @@ nm_status nm_matvec_act(const void* codes, const void* scales, const uint32_t* m
  * grads, outs, counts and dts are HOST arrays, read before the call returns: device pointers, numbers of
  * entries and types (NM_F32, NM_F16 or NM_BF16, mixed as one likes).  A pointer needs its element's
  * alignment only; a tensor without entries is left out.  Squares are summed in fp64 (eight at a time in
- * fp32 where they fit), so no finite gradient overflows; a norm past fp32 is +infinity, and NaN and
- * infinities show in it.  At most 2^20 tensors of less than 2^40 entries each, else NM_ERR_SHAPE. */
+ * fp32 where they fit), so no finite gradient overflows there; a norm past fp32 is written as +infinity,
+ * and NaN and infinities show in it.  At most 2^20 tensors of less than 2^40 entries each, else NM_ERR_SHAPE. */
 size_t nm_grad_norm_workspace_bytes(const int64_t* counts, int64_t tensors);
 nm_status nm_grad_norm(const void* const* grads, const int64_t* counts, const nm_dtype* dts,
                        int64_t tensors, float* norm, void* workspace, size_t workspace_bytes,
                        nm_stream_t stream);
 
-/* out = g * (max_norm / norm), rounded once, where max_norm < norm < infinity, and g itself else.
+/* out = g * (max_norm / norm), rounded once, where max_norm < norm and the norm is finite, and g itself
+ * else.  The tensors' own norm counts as fp64 has it: finite gradients whose norm is past fp32 are clipped.
  * outs[i] may be grads[i] (and is then not written where nothing is clipped); any other overlap of what is
  * written returns NM_ERR_ALIAS, the same tensor given twice among them.  given: NULL, or a norm to
  * clip by, one fp32 number on the device (every rank's, joined); with NULL the tensors' own norm is

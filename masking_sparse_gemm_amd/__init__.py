@@ -954,8 +954,8 @@ def grad_norm(grads) -> torch.Tensor:
 
 
 def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=None) -> torch.Tensor:
-    """Every gradient times max_norm / norm where the norm of all of them is finite and above
-    max_norm, in place or into `out` (tensors of the same sizes, types and order of entries); returns the
+    """Every gradient times max_norm / norm where the norm of all of them is finite (in fp64: one past
+    fp32 is clipped by, and returned as infinity) and above max_norm, in place or into `out` (tensors of the same sizes, types and order of entries); returns the
     norm before clipping.  `norm` (float32, one number on the GPU) takes the place of the gradients' own, as
     where each rank holds a part of them: join grad_norm's squares over the ranks first."""
     t = _Tensors(grads)

@@ -159,16 +159,16 @@ __global__ void __launch_bounds__(256) square_kernel(TensorTable<N> t, double* _
   if (threadIdx.x == 0) sums[blockIdx.x] = total;
 }
 
-__device__ __forceinline__ float norm_of(const double* __restrict__ sums, int count, double* part) {
+__device__ __forceinline__ double norm_of(const double* __restrict__ sums, int count, double* part) {
   double v = 0;
   for (int i = threadIdx.x; i < count; i += 256) v += sums[i];
-  return (float)sqrt(add_group(v, part));
+  return sqrt(add_group(v, part));
 }
 
 __global__ void __launch_bounds__(256)
     norm_kernel(const double* __restrict__ sums, int count, float* __restrict__ norm) {
   __shared__ double part[4];
-  const float n = norm_of(sums, count, part);
+  const float n = (float)norm_of(sums, count, part);
   if (threadIdx.x == 0) *norm = n;
 }
 
@@ -177,11 +177,17 @@ __global__ void __launch_bounds__(256)
     clip_kernel(TensorTable<N> t, const double* __restrict__ sums, int count,
                 const float* __restrict__ given, float max_norm, float* __restrict__ norm) {
   __shared__ double part[4];
-  const float n = given ? *given : norm_of(sums, count, part);
+  const double wide = given ? (double)*given : norm_of(sums, count, part);
+  const float n = (float)wide;
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-  // a norm that is no number leaves everything as it is
-  const bool clip = n > max_norm && n < INFINITY;
-  const float f = clip ? max_norm / n : 1.f;
+  // A norm that is no number leaves everything as it is.  One past fp32 does not: the sum of squares has
+  // it.  A ratio below fp32's normal numbers goes as a number in 1/2 .. 1 and a power of two.
+  const bool clip = n > max_norm && wide < (double)INFINITY;
+  const bool small = clip && (n == INFINITY || max_norm / n < 0x1p-126f);
+  const double ratio = (double)max_norm / (n == INFINITY ? wide : (double)n);
+  int power = 0;
+  float f = clip ? max_norm / n : 1.f;
+  if (small) f = (float)frexp(ratio, &power);
   each_chunk<true>(t, [&](int i, int64_t at, int64_t left) {
     if (!clip && t.out[i] == t.in[i]) return;
     by_type(t.dt[i], [&](auto type) {
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(256)
         u32x4_t w{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          const float v = number<DT>(r, j) * f;
+          const float v = __builtin_ldexpf(number<DT>(r, j) * f, power);
           if constexpr (DT == kF32) w[j] = __float_as_uint(v);
           else w[j / 2] |= (DT == kBF16 ? f32_to_bf16(v) : f32_to_f16(v)) << (16 * (j & 1));
         }
