@@ -154,10 +154,11 @@ inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) 
   return std::max(7.2 + 0.49 * S, tiles / 256 * (3.9 + 0.25 * S));
 }
 
-// Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).
+// Whether nm_spmm_act's product goes to the thin kernel (elem: bytes of an element).  Its 512 work-items for
+// 16 rows at least have to stay below the 2^32 of a launch's dimension.
 inline bool thin_preferred(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
   const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4)) || (n == 4 && m == 8);
-  if (!pattern || K == 0 || T > 4096) return false;
+  if (!pattern || K == 0 || T > 4096 || (R + 15) / 16 * 512 >= (int64_t)1 << 32) return false;
   return ThinPlan(R, K, T, m, elem == 4).us < tiled_us(R, K, n, m, T, elem);
 }
 

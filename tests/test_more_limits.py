@@ -1,5 +1,6 @@
 """Host-only checks at the limits of the epilogue, gradient, clipping and logits calls."""
 import os
+import subprocess
 
 import pytest
 
@@ -24,3 +25,36 @@ def test_workspace_of_a_gradient_by_type():
     # dW's copy of dZ, dX's, what brings rows and columns back, the dense W
     assert typed(64, 64, 64, half, 3, 1, 1, 0) == 2 * 64 * 64 * 2 + 2 * 256 + 64 * 64 * 2
     assert typed(64, 64, 64, nm.NM_F32, 3, 1, 1, 0) == typed(64, 64, 64, half, 6, 1, 1, 0) == 0
+
+
+def test_a_launch_of_the_thin_kernel_has_fewer_than_2_32_work_items(tmp_path):
+    """Whatever the shape that the plan takes: one direct column launches 16 rows a workgroup."""
+    (tmp_path / "rule.cpp").write_text(r"""
+#include <cstdio>
+#include "nm_tiles.h"
+int main() {
+  const int patterns[][2] = {{2, 4}, {1, 2}, {1, 4}, {4, 8}};
+  long thin = 0, most = 0;
+  for (const auto& p : patterns)
+    for (int elem : {1, 2, 4})
+      for (long K : {8L, 64L, 128L, 256L, 1024L})
+        for (long T : {1L, 2L, 16L, 17L, 33L, 512L, 4096L})
+          for (int bit = 20; bit <= 36; ++bit)
+            for (long d : {-17L, -16L, -1L, 0L, 1L, 16L}) {
+              const long R = (1L << bit) + d;
+              if (!nm::thin_preferred(R, K, p[0], p[1], T, elem)) continue;
+              ++thin;
+              const nm::ThinPlan plan(R, K, T, p[1], elem == 4);
+              const long rows = T == 1 && plan.direct ? 16 : 16 * plan.rg;
+              const long items = (R + rows - 1) / rows * 512;
+              if (items > most) most = items;
+            }
+  std::printf("%ld %d\n", thin, most < (1L << 32));
+}
+""")
+    csrc = os.path.join(os.path.dirname(nm.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "rule.cpp"), "-o", str(tmp_path / "rule")],
+                   check=True)
+    thin, fits = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
+                                text=True).stdout.split()
+    assert int(thin) > 100 and fits == "1"
