@@ -18,24 +18,13 @@
 #include "nm_grid.h"
 #include "nm_launch.h"
 #include "nm_mfma.h"
+#include "nm_tiles.h"
 
 namespace nm {
 namespace {
 
-constexpr int kMostCells = 8192;           // words x columns of a workgroup
-constexpr int kEach = 8;                   // of them to a work-item, at most
-constexpr int kMostThreads = 1024;
 constexpr int kCounts = 8448;              // in LDS: columns of one more than the tile's words, and copies
 constexpr uint32_t kSeen = 0x80000000u;    // of a count: the word is in the prompt
-
-// A workgroup's tile: 2^log_cols columns, 2^log_cells entries, `threads` work-items.
-struct LogitsPlan {
-  int log_cols, log_cells, threads;
-  int copies;        // of a workgroup's counts
-  int64_t blocks_v, blocks_t;
-  bool table;        // the counts go through the workspace
-  LogitsPlan(int64_t V, int64_t T, int64_t count);
-};
 
 struct LogitsArgs {
   LogitsCall c;
@@ -117,24 +106,25 @@ __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
 
 // HISTORY: 0 none, 1 counted here in LDS, 2 from the table.
 template <int DT, int HISTORY>
-__global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
+__global__ void __launch_bounds__(kLogitsThreads, 8) adjust_kernel(LogitsArgs a) {
   __shared__ uint32_t cells[HISTORY == 1 ? kCounts : 1];
-  __shared__ uint32_t bits[kMostCells / 32];
+  __shared__ uint32_t bits[kLogitsCells / 32];
   __shared__ int64_t ranges[HISTORY == 1 ? 32 : 1][3];
   const LogitsCall& c = a.c;
   const int tid = threadIdx.x, threads = blockDim.x;
   const int cols = 1 << a.log_cols, all = 1 << a.log_cells, words = all >> a.log_cols;
-  const int64_t t0 = (int64_t)blockIdx.y * cols, v0 = (int64_t)blockIdx.x * words;
+  const int64_t t0 = (int64_t)blockIdx.y * cols, v0 = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * words;
+  if (v0 >= c.V) return;
   const int64_t t = t0 + (tid & (cols - 1));  // this work-item's column
   const bool live = t < c.T;
   // the logits are under way while the tokens are counted
-  float x[kEach];
+  float x[kLogitsEach];
   const auto place = [&](int k) {  // of entry k of this work-item, held within the matrix
     const int64_t v = v0 + ((tid + k * threads) >> a.log_cols);
     return min(v, c.V - 1) * c.T + min(t, c.T - 1);
   };
 #pragma unroll
-  for (int k = 0; k < kEach; ++k)
+  for (int k = 0; k < kLogitsEach; ++k)
     if (tid + k * threads < all) x[k] = logit_at<DT>(c.logits, place(k));
   if constexpr (HISTORY == 1) {
     for (int i = tid; i < a.copies * cols * (words + 1); i += threads) cells[i] = 0u;
@@ -178,17 +168,17 @@ __global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
   const float repetition = HISTORY && c.repetition ? c.repetition[t] : 1.f;
   const float presence = HISTORY && c.presence ? c.presence[t] : 0.f;
   const float frequency = HISTORY && c.frequency ? c.frequency[t] : 0.f;
-  float b[kEach];
-  uint32_t n[kEach];
+  float b[kLogitsEach];
+  uint32_t n[kLogitsEach];
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
+  for (int k = 0; k < kLogitsEach; ++k) {
     if (tid + k * threads >= all) continue;
     const int64_t v = v0 + ((tid + k * threads) >> a.log_cols);
     if (c.bias) b[k] = c.bias[c.bias_each ? place(k) : min(v, c.V - 1)];
     if constexpr (HISTORY == 2) n[k] = a.counts[place(k)];
   }
 #pragma unroll
-  for (int k = 0; k < kEach; ++k) {
+  for (int k = 0; k < kLogitsEach; ++k) {
     const int i = tid + k * threads, w = i >> a.log_cols;
     const int64_t v = v0 + w;
     if (i >= all || v >= c.V) continue;
@@ -218,47 +208,9 @@ __global__ void __launch_bounds__(kMostThreads, 8) adjust_kernel(LogitsArgs a) {
 
 int64_t table_bytes(int64_t V, int64_t T) { return V * T * 4; }
 
-// Columns: 32, whose 128 bytes (fp32) of a row are a whole line, or what there are, to a power of two;
-// 16 where tokens are counted in LDS, whose readers are then half as many (50257 x 64, 96,000 tokens
-// 20.7 -> 18.0 us, 128000 x 32, 64,000 tokens 25.7 -> 19.6; through the table 28.5 -> 32.7).
-// Entries: as many as fit, since every workgroup reads its columns' tokens (50257 x 64 by 32 columns:
-// 8192 a workgroup 18 us, 4096 25, 1024 80), but few enough that most of the 256 units have a workgroup.
-// Work-items: eight entries each, but all 1024 where there are tokens for them (5000 x 8, 32,000
-// tokens 15.2 -> 8.6).
-LogitsPlan::LogitsPlan(int64_t V, int64_t T, int64_t count) {
-  const auto cut = [&](int most) {
-    log_cols = 0;
-    while (log_cols < most && ((int64_t)1 << log_cols) < T) ++log_cols;
-    const int64_t cols = (int64_t)1 << log_cols;
-    blocks_t = (T + cols - 1) / cols;
-    const int least = std::max(8, 5 + log_cols);  // whole words of the mask
-    for (log_cells = 13; log_cells > least; --log_cells) {
-      const int64_t words = ((int64_t)1 << log_cells) / cols;
-      if ((V + words - 1) / words * blocks_t >= 224) break;
-    }
-    const int64_t words = ((int64_t)1 << log_cells) / cols;
-    blocks_v = (V + words - 1) / words;
-  };
-  cut(T < (int64_t)1 << 19 ? 4 : 5);  // (a grid has 65535 columns at most)
-  // In LDS each of blocks_v workgroups reads a column's tokens, as fast as the caches give them to the
-  // units that work; through the table they are read once, and the table is written and read, with two
-  // more launches.  `count` is the room for tokens, of which a part is in use.  Measured, us in LDS /
-  // through the table: 32000 words, one column of 2000 tokens 5.4 / 10.1, of 100,000 19.8 / 12.3; 32000
-  // x 8, 16,000 tokens 7.2 / 10.8, 160,000 25 / 14.5; 50257 x 64, 96,000 tokens 15.7 / 22, 512,000 34 /
-  // 29, 2,000,000 99 / 41; 128000 x 256, 256,000 tokens 88 / 98, 1,000,000 124 / 108.
-  const double share = std::min(1.0, (double)(blocks_v * blocks_t) / 256), cells = (double)V * (double)T;
-  const double in_lds = 3 + 0.45e-6 * cells + (double)blocks_v * (double)count * 8 / (24e6 * share);
-  table = count > 0 && in_lds > 8 + 1.1e-6 * cells;
-  if (table || count == 0) cut(5);
-  copies = std::min(16, kMostCells >> log_cells);
-  const int64_t each = count / std::max<int64_t>(1, T);  // tokens of a column
-  if (each <= 512) copies = 1;
-  threads = each > 512 ? kMostThreads : std::max(256, (1 << log_cells) / kEach);
-}
-
 template <int DT>
 hipError_t launch_adjust(const LogitsArgs& a, const LogitsPlan& p, int history, hipStream_t s) {
-  const dim3 grid((unsigned)p.blocks_v, (unsigned)p.blocks_t);
+  const dim3 grid((unsigned)p.grid_v, (unsigned)p.blocks_t, (unsigned)p.grid_z);
   if (history == 0) adjust_kernel<DT, 0><<<grid, p.threads, 0, s>>>(a);
   else if (history == 1) adjust_kernel<DT, 1><<<grid, p.threads, 0, s>>>(a);
   else adjust_kernel<DT, 2><<<grid, p.threads, 0, s>>>(a);

@@ -1,5 +1,5 @@
-// nm_tiles.h -- which kernel a 4-bit product takes, which tile a dense product of the cross entropy or
-// of the orthogonalised update takes, and how the cross entropy's gradient is cut.  Plain C++ with no
+// nm_tiles.h -- which kernel a 4-bit product or a compressed one with an epilogue takes, which tile a dense
+// product takes, and how the gradients and the logits are cut.  Plain C++ with no
 // HIP types, so that a host-only test can compile it and say which kernels a size runs.
 #ifndef NM_TILES_H
 #define NM_TILES_H
@@ -205,6 +205,63 @@ struct SpmmGradCut {
         }
   }
 };
+
+// ---- logits ------------------------------------------------------------------------------------
+
+constexpr int kLogitsCells = 8192;  // words x columns of a workgroup
+constexpr int kLogitsEach = 8;      // of them to a work-item, at most
+constexpr int kLogitsThreads = 1024;
+
+// A workgroup's tile: 2^log_cols columns, 2^log_cells entries, `threads` work-items.
+struct LogitsPlan {
+  int log_cols, log_cells, threads;
+  int copies;        // of a workgroup's counts
+  int64_t blocks_v, blocks_t;
+  int64_t grid_v, grid_z;  // blocks_v in two dimensions of the launch, the last ones empty
+  bool table;        // the counts go through the workspace
+  LogitsPlan(int64_t V, int64_t T, int64_t count);
+};
+
+// Columns: 32, whose 128 bytes (fp32) of a row are a whole line, or what there are, to a power of two;
+// 16 where tokens are counted in LDS, whose readers are then half as many (50257 x 64, 96,000 tokens
+// 20.7 -> 18.0 us, 128000 x 32, 64,000 tokens 25.7 -> 19.6; through the table 28.5 -> 32.7).
+// Entries: as many as fit, since every workgroup reads its columns' tokens (50257 x 64 by 32 columns:
+// 8192 a workgroup 18 us, 4096 25, 1024 80), but few enough that most of the 256 units have a workgroup.
+// Work-items: eight entries each, but all 1024 where there are tokens for them (5000 x 8, 32,000
+// tokens 15.2 -> 8.6).
+inline LogitsPlan::LogitsPlan(int64_t V, int64_t T, int64_t count) {
+  const auto cut = [&](int most) {
+    log_cols = 0;
+    while (log_cols < most && ((int64_t)1 << log_cols) < T) ++log_cols;
+    const int64_t cols = (int64_t)1 << log_cols;
+    blocks_t = (T + cols - 1) / cols;
+    const int least = std::max(8, 5 + log_cols);  // whole words of the mask
+    for (log_cells = 13; log_cells > least; --log_cells) {
+      const int64_t words = ((int64_t)1 << log_cells) / cols;
+      if ((V + words - 1) / words * blocks_t >= 224) break;
+    }
+    const int64_t words = ((int64_t)1 << log_cells) / cols;
+    blocks_v = (V + words - 1) / words;
+  };
+  cut(T < (int64_t)1 << 19 ? 4 : 5);  // (a grid has 65535 columns at most)
+  // In LDS each of blocks_v workgroups reads a column's tokens, as fast as the caches give them to the
+  // units that work; through the table they are read once, and the table is written and read, with two
+  // more launches.  `count` is the room for tokens, of which a part is in use.  Measured, us in LDS /
+  // through the table: 32000 words, one column of 2000 tokens 5.4 / 10.1, of 100,000 19.8 / 12.3; 32000
+  // x 8, 16,000 tokens 7.2 / 10.8, 160,000 25 / 14.5; 50257 x 64, 96,000 tokens 15.7 / 22, 512,000 34 /
+  // 29, 2,000,000 99 / 41; 128000 x 256, 256,000 tokens 88 / 98, 1,000,000 124 / 108.
+  const double share = std::min(1.0, (double)(blocks_v * blocks_t) / 256), cells = (double)V * (double)T;
+  const double in_lds = 3 + 0.45e-6 * cells + (double)blocks_v * (double)count * 8 / (24e6 * share);
+  table = count > 0 && in_lds > 8 + 1.1e-6 * cells;
+  if (table || count == 0) cut(5);
+  copies = std::min(16, kLogitsCells >> log_cells);
+  const int64_t each = count / std::max<int64_t>(1, T);  // tokens of a column
+  if (each <= 512) copies = 1;
+  threads = each > 512 ? kLogitsThreads : std::max(256, (1 << log_cells) / kLogitsEach);
+  // a dimension of a launch has fewer than 2^32 work-items
+  grid_v = std::min<int64_t>(blocks_v, 1 << 20);
+  grid_z = (blocks_v + grid_v - 1) / std::max<int64_t>(1, grid_v);
+}
 
 // ---- orthogonalised update ---------------------------------------------------------------------
 

@@ -39,3 +39,38 @@ def test_product_of_many_rows(R, K, T):
     whole = R // period * period
     assert bool((Y[:whole].view(-1, period, T) == Y[:period]).all())
     assert torch.equal(Y[whole:], Y[:R - whole])
+
+
+@pytest.mark.parametrize("V,T,count", [(2 ** 30, 17, 0), (2 ** 30 - 999, 16, 0), (2 ** 31 - 1, 16, 40)])
+def test_logits_of_many_words(V, T, count):
+    from tests.test_gpu_logits import expected
+
+    period = 8192
+    base = randn(period, T, seed=4)
+    x = base.cuda().repeat(-(-V // period), 1)[:V]
+    if count == 0:
+        shared = torch.randn(period, generator=torch.Generator().manual_seed(5))
+        nm.adjust_logits(x, bias=shared.cuda().repeat(-(-V // period))[:V].contiguous(), out=x)
+        want = expected(base, None, None, None, None, None, None, shared, None)
+    else:
+        # words of every part of the vocabulary, at their places modulo the period
+        gen = torch.Generator().manual_seed(6)
+        tokens = torch.randint(0, V, (count * T,), generator=gen)
+        tokens[0], tokens[count] = V - 1, 2 ** 30
+        starts = torch.arange(T + 1) * count
+        rep = torch.rand(T, generator=gen) + 1
+        nm.adjust_logits(x, tokens.cuda(), starts.cuda(), repetition=rep.cuda(), out=x)
+        col = torch.arange(T).repeat_interleave(count)
+        before = base[tokens % period, col].double()
+        after = torch.where(before > 0, before / rep[col].double(), before * rep[col].double())
+        got = x[tokens.cuda(), col.cuda()]
+        ref.check(got, after, 4 * ref.F32 * after.abs() + ref.rounding(after, BF) * (1 + 2.0 ** -7), "words")
+        x[tokens.cuda(), col.cuda()] = base[tokens % period, col].cuda()
+        want = expected(base, None, None, None, None, None, None, None, None)
+    ref.check(x[:period], *want, "logits")
+    first = x[:period].clone()
+    for v in range(0, V, 2 ** 28):
+        part = x[v:v + 2 ** 28]
+        whole = part.shape[0] // period * period
+        assert bool((part[:whole].view(-1, period, T) == first).all())
+        assert torch.equal(part[whole:], first[:part.shape[0] - whole])

@@ -58,3 +58,39 @@ int main() {
     thin, fits = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
                                 text=True).stdout.split()
     assert int(thin) > 100 and fits == "1"
+
+
+def test_a_launch_of_the_logits_kernel_has_fewer_than_2_32_work_items(tmp_path):
+    """Over all that the call accepts: V < 2^31, T < 2^20, V T < 2^36, with and without tokens."""
+    (tmp_path / "rule.cpp").write_text(r"""
+#include <cstdio>
+#include "nm_tiles.h"
+int main() {
+  long seen = 0, wrong = 0;
+  for (int bit = 0; bit <= 31; ++bit)
+    for (long dv : {-1L, 0L, 1L})
+      for (int t = 0; t <= 20; ++t)
+        for (long d : {-1L, 0L, 1L})
+          for (long count : {0L, 1L, 1000L, 1L << 20, (1L << 31) - 1}) {
+            const long V = (1L << bit) + dv, T = (1L << t) + d;
+            if (V < 1 || T < 1 || V >= 1L << 31 || T >= 1L << 20 || V * T >= 1L << 36) continue;
+            const nm::LogitsPlan p(V, T, count);
+            ++seen;
+            const long words = (1L << p.log_cells) >> p.log_cols, cols = 1L << p.log_cols;
+            const bool fits = p.threads <= nm::kLogitsThreads && p.grid_v * p.threads < 1L << 32 &&
+                              p.blocks_t < 65536 && p.grid_z < 65536 && p.grid_z >= 1;
+            const bool covers = p.grid_v * p.grid_z * words >= V && p.blocks_t * cols >= T &&
+                                p.grid_v * (p.grid_z - 1) * words < V;
+            const bool holds = (1 << p.log_cells) <= nm::kLogitsEach * p.threads && words % 32 == 0 &&
+                               cols <= 32 && p.copies * cols * (words + 1) <= 8448;
+            if (!fits || !covers || !holds) ++wrong;
+          }
+  std::printf("%ld %ld\n", seen, wrong);
+}
+""")
+    csrc = os.path.join(os.path.dirname(nm.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "rule.cpp"), "-o", str(tmp_path / "rule")],
+                   check=True)
+    seen, wrong = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
+                                 text=True).stdout.split()
+    assert int(seen) > 5000 and wrong == "0"
