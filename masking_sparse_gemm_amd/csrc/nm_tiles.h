@@ -159,7 +159,9 @@ inline double tiled_us(int64_t R, int64_t K, int n, int m, int64_t T, int elem) 
 inline bool thin_preferred(int64_t R, int64_t K, int n, int m, int64_t T, int elem) {
   const bool pattern = (n == 2 && m == 4) || (n == 1 && (m == 2 || m == 4)) || (n == 4 && m == 8);
   if (!pattern || K == 0 || T > 4096 || (R + 15) / 16 * 512 >= (int64_t)1 << 32) return false;
-  return ThinPlan(R, K, T, m, elem == 4).us < tiled_us(R, K, n, m, T, elem);
+  const ThinPlan plan(R, K, T, m, elem == 4);
+  if (!plan.direct && (K + 63) / 64 * 256 >= (int64_t)1 << 32) return false;  // (X turned, 256 for 64 K)
+  return plan.us < tiled_us(R, K, n, m, T, elem);
 }
 
 // ---- gradient of the compressed product ---------------------------------------------------------

@@ -94,3 +94,31 @@ int main() {
     seen, wrong = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
                                  text=True).stdout.split()
     assert int(seen) > 5000 and wrong == "0"
+
+
+def test_a_copy_of_X_for_the_thin_kernel_has_fewer_than_2_32_work_items(tmp_path):
+    (tmp_path / "rule.cpp").write_text(r"""
+#include <cstdio>
+#include "nm_tiles.h"
+int main() {
+  long copies = 0, most = 0;
+  for (int bit = 20; bit < 36; ++bit)
+    for (long d : {-60L, 4L, 8L, 64L})
+      for (long T : {1L, 2L, 33L, 4096L})
+        for (long R : {1L, 3L, 16L})
+          for (int elem : {1, 2, 4}) {
+            const long K = (1L << bit) + d;
+            const nm::ThinPlan plan(R, K, T, 4, elem == 4);
+            if (plan.direct || !nm::thin_preferred(R, K, 2, 4, T, elem)) continue;
+            ++copies;
+            if ((K + 63) / 64 * 256 > most) most = (K + 63) / 64 * 256;
+          }
+  std::printf("%ld %d\n", copies, most < (1L << 32));
+}
+""")
+    csrc = os.path.join(os.path.dirname(nm.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "rule.cpp"), "-o", str(tmp_path / "rule")],
+                   check=True)
+    copies, fits = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
+                                  text=True).stdout.split()
+    assert int(copies) > 50 and fits == "1"
