@@ -122,3 +122,24 @@ int main() {
     copies, fits = subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True,
                                   text=True).stdout.split()
     assert int(copies) > 50 and fits == "1"
+
+
+def test_long_rows_of_bytes_take_the_thin_kernel(tmp_path):
+    """The sizes of test_gpu_act_exact.py: more than sixteen steps of 64 to each of eight waves."""
+    (tmp_path / "rule.cpp").write_text(r"""
+#include <cstdio>
+#include "nm_tiles.h"
+int main() {
+  const int patterns[][2] = {{2, 4}, {1, 2}, {1, 4}, {4, 8}};
+  const long sizes[][3] = {{33, (1 << 17) - 64, 1}, {33, (1 << 17) - 64, 20}, {20, (1 << 17) - 24, 20},
+                           {20, (1 << 17) - 24, 1}};
+  int thin = 0;
+  for (const auto& p : patterns)
+    for (const auto& s : sizes) thin += nm::thin_preferred(s[0], s[1], p[0], p[1], s[2], 1);
+  std::printf("%d\n", thin);
+}
+""")
+    csrc = os.path.join(os.path.dirname(nm.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "rule.cpp"), "-o", str(tmp_path / "rule")],
+                   check=True)
+    assert subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True, text=True).stdout == "16\n"
