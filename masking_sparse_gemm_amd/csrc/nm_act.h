@@ -2,7 +2,8 @@
 // (gfx950): what nm_spmm_act, nm_matvec_act and nm_spmm_act_grad share.
 //
 // All of it is fp32 on the product's fp32 (int8: int32) sums, rounded once where Z and Y are stored.
-// Exponentials and reciprocals are the hardware's (v_exp_f32, v_rcp_f32: one unit in the last place),
+// Exponentials and reciprocals are the hardware's (v_exp_f32, v_rcp_f32: one unit in the last place of what
+// they are given: an exponent a that was rounded before is 2^-22 a of a relative error at most),
 // so a sigmoid takes four instructions and the epilogue's arithmetic hides under its memory traffic
 // (bf16 11008 x 4096, 2048 columns: the product alone 105 us, with bias and silu, Z kept, 119-123).
 #pragma once
@@ -28,7 +29,8 @@ __device__ __forceinline__ float sigmoid(float z) {
 // The normal distribution function of z, and e^(-z^2 / 2).  The tail Phi(-u), u = |z|, is
 // e^(-u^2 / 2) t p(t) with t = 1 / (1 + 0.28 u): p is a polynomial of degree 8 fitted to
 // e^(u^2 / 2) Phi(-u) / t for u in 0 .. 60 by weighted least squares (relative error 9.2e-8, 4e-7 as
-// evaluated here), so the tail keeps its relative accuracy, which 1 + erf loses.
+// evaluated here), so the tail keeps a relative accuracy, which 1 + erf loses: that and 2^-22 u^2 / 2 at
+// most, since u^2 / 2 is rounded before the exponential (2e-6 at u = 4, 1e-5 at 9).
 __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
   const float u = fabsf(z), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.28f, u, 1.f));
   gauss = __builtin_amdgcn_exp2f(z * z * (-0.5f * kActLog2e));
