@@ -771,7 +771,8 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
     """Y (R, T) = act(Z) + residual with Z = W_sparse @ X + bias: spmm with what a layer does to its
     result in the product's epilogue, all in fp32 and rounded once.  act is one of ACTS; bias is
     float32 (R,); residual (R, T) in Y's type may be out itself.  keep=True: (Y, Z), Z in X's type,
-    which spmm_act_grad takes.  int8 and float8 products take scale, float32 (R,): Z = scale *
+    which spmm_act_grad takes of bfloat16 and float16.  A column's sums may be added up in another order
+    than spmm's, or beside another number of columns.  int8 and float8 products take scale, float32 (R,): Z = scale *
     (W_sparse @ X) + bias, and keep no Z.  out_dtype is X's type or float32, of int8 and float8
     float32, float16 or bfloat16 (default bfloat16)."""
     xdt = _dense_input(X, "X")
