@@ -744,6 +744,12 @@ def _act(act: str) -> int:
     return code
 
 
+def _written(out) -> None:
+    """A tensor of the caller's, or several, that the library wrote by address: their version counters move,
+    as with torch's own operations in place, so that autograd notices a saved tensor that changed."""
+    torch.autograd.graph.increment_version(out)
+
+
 def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -772,9 +778,9 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
     result in the product's epilogue, all in fp32 and rounded once.  act is one of ACTS; bias is
     float32 (R,); residual (R, T) in Y's type may be out itself.  keep=True: (Y, Z), Z in X's type,
     which spmm_act_grad takes of bfloat16 and float16.  A column's sums may be added up in another order
-    than spmm's, or beside another number of columns.  int8 and float8 products take scale, float32 (R,): Z = scale *
-    (W_sparse @ X) + bias, and keep no Z.  out_dtype is X's type or float32, of int8 and float8
-    float32, float16 or bfloat16 (default bfloat16)."""
+    than spmm's, or beside another number of columns.  int8 and float8 products take scale, float32
+    (R,): Z = scale * (W_sparse @ X) + bias, and keep no Z.  out_dtype is X's type or float32, of int8
+    and float8 float32, float16 or bfloat16 (default bfloat16)."""
     xdt = _dense_input(X, "X")
     code = _act(act)
     K, T = X.shape
@@ -796,7 +802,8 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
     scale = _row_numbers(scale, "scale", R, device)
     _expect(residual, "residual", (R, T), y_dtype, device)
     _expect(out, "out", (R, T), y_dtype, device)
-    if out is None:
+    mine = out is None
+    if mine:
         out = torch.empty_like(residual) if residual is not None else X.new_empty((R, T), dtype=y_dtype)
     Z = X.new_empty((R, T)) if keep else None
     L = lib()
@@ -805,6 +812,8 @@ def spmm_act(values: torch.Tensor, meta: torch.Tensor, X: torch.Tensor, n: int =
         values.data_ptr(), meta.data_ptr(), R, K, n, m, _layout(layout), X.data_ptr(), T, dt,
         _addr(scale), _addr(bias), code, _addr(residual), _addr(Z), out.data_ptr(),
         _DT[y_dtype], ws_ptr, 0 if ws is None else ws.numel())
+    if not mine:
+        _written(out)
     return (out, Z) if keep else out
 
 
@@ -891,7 +900,8 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
     bias = _row_numbers(bias, "bias", rows, device)
     _expect(residual, "residual", (rows, T), y_dtype, device)
     _expect(out, "out", (rows, T), y_dtype, device)
-    if out is None:
+    mine = out is None
+    if mine:
         out = torch.empty_like(residual) if residual is not None else X.new_empty((rows, T), dtype=y_dtype)
     L = lib()
     ws, ws_ptr = _workspace(X, L.nm_matvec_workspace_bytes(rows, K, T, meta is not None))
@@ -899,6 +909,8 @@ def matvec_act(codes: torch.Tensor, scales: torch.Tensor, X: torch.Tensor, group
         codes.data_ptr(), scales.data_ptr(), _addr(meta), rows, K, group, X.data_ptr(), T, dt,
         _addr(bias), code, _addr(residual), out.data_ptr(), _DT[y_dtype], ws_ptr,
         0 if ws is None else ws.numel())
+    if not mine:
+        _written(out)
     return out
 
 
@@ -976,6 +988,7 @@ def clip_grads(grads, max_norm: float, norm: torch.Tensor | None = None, out=Non
     _launch("nm_clip_grads", like,
         ptrs, o.pointers.buffer_info()[0], counts, dts, n, float(max_norm), _addr(given),
         norm.data_ptr(), ws_ptr, 0 if ws is None else ws.numel())
+    _written(o.grads)
     return norm
 
 
@@ -1018,7 +1031,8 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
     _expect(out, "out", (V, T), logits.dtype, device)
     bias = None if bias is None else _token_numbers(bias)
     allowed = None if allowed is None else _token_numbers(allowed)
-    if out is None:
+    mine = out is None
+    if mine:
         out = torch.empty_like(logits)
     L = lib()
     ws, ws_ptr = _workspace(logits, L.nm_adjust_logits_workspace_bytes(V, T, count))
@@ -1026,4 +1040,6 @@ def adjust_logits(logits: torch.Tensor, tokens: torch.Tensor | None = None,
         logits.data_ptr(), dt, V, T, _addr(tokens), count, _addr(starts), _addr(prompts),
         *map(_addr, penalties), _addr(bias), each, _addr(allowed), out.data_ptr(), ws_ptr,
         0 if ws is None else ws.numel())
+    if not mine:
+        _written(out)
     return out
