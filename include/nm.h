@@ -434,10 +434,10 @@ typedef enum NM_INT_ENUM {
  *   residual  R x T in y_dt, or NULL; may be Y itself, which is then added to
  *   Z         R x T in dt, the activation's argument, which nm_spmm_act_grad takes of NM_F16 and NM_BF16, or
  *             NULL (NM_I8 and NM_FP8: NULL, or NM_ERR_DTYPE)
- * y_dt is dt or NM_F32, and for NM_I8 and NM_FP8 one of NM_F32, NM_F16 and NM_BF16.  Sums are fp32 (NM_I8:
- * K < 2^17, exact, then one rounding to fp32), in an order of their own where T or R is small, so a column
- * may differ from nm_spmm's, and from its own beside another number of columns, within their rounding;
- * the same call gives the same bits.  K = 0 gives Z = b.
+ * y_dt is dt or NM_F32, and for NM_I8 and NM_FP8 one of NM_F32, NM_F16 and NM_BF16.  Sums are held as
+ * nm_spmm's (NM_I8: K < 2^17, exact, then one rounding to fp32), but in an order of their own where T or R
+ * is small, so a column may differ from nm_spmm's, and from its own beside another number of columns,
+ * within their rounding; the same call gives the same bits.  K = 0 gives Z = b.
  * workspace: nm_spmm_act_workspace_bytes(R, K, n, m, T, dt) bytes of device memory, whose contents do
  * not matter: room for a copy of X where X's rows are not whole 16-byte pieces or many workgroups read a
  * few tokens, else 0. */

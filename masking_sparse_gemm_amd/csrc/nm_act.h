@@ -5,7 +5,8 @@
 // Exponentials and reciprocals are the hardware's (v_exp_f32, v_rcp_f32: one unit in the last place of what
 // they are given: an exponent a that was rounded before is 2^-22 a of a relative error at most),
 // so a sigmoid takes four instructions and the epilogue's arithmetic hides under its memory traffic
-// (bf16 11008 x 4096, 2048 columns: the product alone 105 us, with bias and silu, Z kept, 119-123).
+// (bf16 11008 x 4096, 2048 columns, in turn on warm caches: the product alone 107 us, with silu, Z kept,
+// 124, of which the stores are most; 4096 x 11008 with a residual 94 and 101).
 #pragma once
 
 #include "nm_launch.h"

@@ -22,9 +22,10 @@
 // products in one, dX's long sums first: alone, each leaves units idle at its end (1000 x 768, 333
 // columns: 30 us a call in launches of their own, 21 so).
 //
-// Bound by the matrix cores where matrices are large: bf16 11008 x 4096, 2048 columns, dZ 25.6 us and W
-// 24.8, both at the memory's rate, the products 328-336 (1100-1130 TFLOP/s; a library's product of 8192^3
-// on the same card 1215).  By launches where they are small: 6.9 and 9.9 us for 1000 x 768, 333 columns.
+// Bound by the matrix cores where matrices are large: bf16 11008 x 4096, 2048 columns, dZ 26 us and W 24.5,
+// both at the memory's rate, the products 314 in a replayed graph (1180 TFLOP/s; a library's product of
+// 8192^3 on the same card 1199) and 350 under a profiler.  By load latency and launches where they are
+// small: 6.8 and 10.0 us for 1000 x 768, 333 columns, in fp16 with a smooth activation 6.2, 8.2 and 10.1.
 #include <algorithm>
 
 #include "nm_act.h"
