@@ -143,3 +143,15 @@ int main() {
     subprocess.run(["g++", "-std=c++17", "-I", csrc, str(tmp_path / "rule.cpp"), "-o", str(tmp_path / "rule")],
                    check=True)
     assert subprocess.run([str(tmp_path / "rule")], check=True, capture_output=True, text=True).stdout == "16\n"
+
+
+def test_a_gradient_in_fp16_is_refused_the_other_types_workspace():
+    from tests.test_more_host import grad
+
+    sizes = dict(R=32, K=128, T=16, act=3)
+    L = nm.lib()
+    plain = L.nm_spmm_act_grad_workspace_bytes(32, 128, 16, 3, 1, 1, 1)
+    typed = L.nm_spmm_act_grad_dt_workspace_bytes(32, 128, 16, nm.NM_F16, 3, 1, 1, 1)
+    assert grad(dt=nm.NM_F16, size=plain, **sizes) == grad(dt=nm.NM_F16, size=typed - 1, **sizes) == "scratch"
+    assert grad(dt=nm.NM_F16, size=typed, **sizes) == grad(dt=nm.NM_BF16, size=plain, **sizes) == "device"
+    assert grad(dt=nm.NM_F16, size=plain, **dict(sizes, act=1)) == "device"
